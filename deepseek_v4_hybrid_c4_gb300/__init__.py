@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libcsa.so")
 _lib = None
 
 CSA_OK, CSA_ERR_INVALID_ARG, CSA_ERR_UNSUPPORTED, CSA_ERR_CUDA, CSA_ERR_TIMEOUT, CSA_ERR_DEVICE_BOUNDS, \
-    CSA_ERR_WORKSPACE = range(7)
+    CSA_ERR_WORKSPACE, CSA_ERR_NO_PAGES = range(8)
 CSA_BF16, CSA_FP8_E4M3, CSA_FP32 = range(3)
 
 
@@ -35,6 +35,15 @@ CSA_COPY_MAX = 16
 
 class csa_copy(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("bytes", ctypes.c_uint64)]
+
+
+CSA_POOLS_MAX = 4
+
+
+class csa_page_pools(ctypes.Structure):
+    _fields_ = [("n_pools", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("base", ctypes.c_void_p * CSA_POOLS_MAX), ("page_bytes", ctypes.c_int64 * CSA_POOLS_MAX),
+                ("page_stride", ctypes.c_int64 * CSA_POOLS_MAX)]
 
 
 class csa_decode_params(ctypes.Structure):
@@ -95,6 +104,20 @@ def lib() -> ctypes.CDLL:
         L.csa_version.restype = i32
         L.csa_selftest_bounded_wait.argtypes = [vp]
         L.csa_copy_batch.argtypes = [i32, ctypes.POINTER(csa_copy), vp]
+        L.csa_prefix_attn.argtypes = [vp, i32, i32, f32, csa_paged, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+        L.csa_prefix_attn_workspace_size.argtypes = [i32, i32, i64, i64]
+        L.csa_prefix_attn_workspace_size.restype = sz
+        L.csa_window_attn.argtypes = [vp, i32, f32, csa_paged, i64, i32, vp, vp, i64, i64, i32, i32, vp, vp, vp, sz, vp]
+        L.csa_window_attn_workspace_size.argtypes = [i32, i32, i64, i64, i32, i32]
+        L.csa_window_attn_workspace_size.restype = sz
+        pools = ctypes.POINTER(csa_page_pools)
+        L.csa_pages_workspace_size.argtypes = [i64]
+        L.csa_pages_workspace_size.restype = sz
+        L.csa_pages_alloc.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, sz, vp]
+        L.csa_pages_free.argtypes = [vp, i64, vp, i64, i32, vp, i32, vp]
+        L.csa_pages_fork.argtypes = [pools, vp, vp, i64, i32, vp, vp, i32, vp, i32, vp, sz, vp]
+        L.csa_pages_compact.argtypes = [pools, vp, vp, vp, vp, i64, i32, vp, vp, sz, vp]
+        L.csa_pages_copy.argtypes = [pools, vp, vp, i32, vp]
         L.csa_hisparse_create.argtypes = [i32, i64, i64, ctypes.POINTER(vp)]
         L.csa_hisparse_destroy.argtypes = [vp]
         L.csa_hisparse_destroy.restype = None
@@ -110,7 +133,9 @@ def lib() -> ctypes.CDLL:
                      "csa_topk_cluster", "csa_topk_merge", "csa_sparse_attn_partial", "csa_attn_merge", "csa_sparse_attn",
                      "csa_decode", "csa_decode_timed", "csa_decode_noalloc", "csa_read_device_status",
                      "csa_hisparse_create", "csa_hisparse_plan", "csa_hisparse_update", "csa_hisparse_collect",
-                     "csa_hisparse_apply", "csa_selftest_bounded_wait", "csa_copy_batch"):
+                     "csa_hisparse_apply", "csa_selftest_bounded_wait", "csa_copy_batch", "csa_prefix_attn",
+                     "csa_window_attn", "csa_pages_alloc", "csa_pages_free", "csa_pages_fork", "csa_pages_compact",
+                     "csa_pages_copy"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -187,6 +212,18 @@ def _scratch(nbytes: int, like):
     return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device if hasattr(like, "device") else "cuda")
 
 
+def _workspace(workspace, ws_bytes: int, need: int, like, stream):
+    """The caller's workspace, or a scratch tensor of `need` bytes that stays allocated until the work on
+    `stream` that uses it is done."""
+    if workspace is not None:
+        return workspace, ws_bytes
+    ws = _scratch(need, like)
+    if stream is not None and ws.is_cuda:
+        import torch
+        ws.record_stream(torch.cuda.ExternalStream(stream, ws.device) if isinstance(stream, int) else stream)
+    return ws, need
+
+
 def csa_topk(scores, G: int, k: int, idx_out, keys_out=None, workspace=None, ws_bytes: int = 0,
              stream=None) -> None:
     """workspace None: a scratch tensor of csa_topk_workspace_size(1, G, k) bytes is allocated."""
@@ -248,6 +285,90 @@ def csa_sparse_attn_partial(q, H: int, scale: float, kv_c: csa_paged, sel, n_sel
 def csa_attn_merge(o_parts, lse_parts, R: int, H: int, out, lse=None, stream=None) -> None:
     _check(lib().csa_attn_merge(_ptr(o_parts), _ptr(lse_parts), R, H, _ptr(out), _ptr(lse), _stream(stream)),
            "csa_attn_merge")
+
+
+def csa_prefix_attn_workspace_size(B: int, H: int, n_shared: int, max_rows: int) -> int:
+    return int(lib().csa_prefix_attn_workspace_size(B, H, n_shared, max_rows))
+
+
+def csa_prefix_attn(q, B: int, H: int, scale: float, kv: csa_paged, page_table_stride: int, n_shared: int, n_rows,
+                    max_rows: int, out, lse=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    """One token per request over a batch whose requests share their first n_shared rows (kv: the pool
+    with the [B, page_table_stride] table).  workspace None: a scratch tensor is allocated."""
+    if workspace is None:
+        workspace, ws_bytes = _workspace(None, 0, csa_prefix_attn_workspace_size(B, H, n_shared, max_rows), q, stream)
+    _check(lib().csa_prefix_attn(_ptr(q), B, H, scale, kv, page_table_stride, n_shared, _ptr(n_rows), max_rows,
+                                 _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), "csa_prefix_attn")
+
+
+def csa_window_attn_workspace_size(B: int, H: int, total_q: int, max_q: int, window: int, n_sink: int) -> int:
+    return int(lib().csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink))
+
+
+def csa_window_attn(q, H: int, scale: float, kv_raw: csa_paged, page_table_stride: int, B: int, q_offsets, n_tokens,
+                    total_q: int, max_q: int, window: int, n_sink: int, out, lse=None, workspace=None,
+                    ws_bytes: int = 0, stream=None) -> None:
+    """Causal attention of each sequence's new tokens over a sliding window and the first n_sink tokens.
+    workspace None: a scratch tensor is allocated."""
+    if workspace is None:
+        need = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink)
+        workspace, ws_bytes = _workspace(None, 0, need, q, stream)
+    _check(lib().csa_window_attn(_ptr(q), H, scale, kv_raw, page_table_stride, B, _ptr(q_offsets), _ptr(n_tokens),
+                                 total_q, max_q, window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                                 _stream(stream)), "csa_window_attn")
+
+
+def page_pools(pools, n_pages: int) -> csa_page_pools:
+    """Describe the pools that share page ids: device tensors whose first dimension is the page, each
+    page contiguous (n_pages of them); the struct keeps references to them."""
+    d = csa_page_pools()
+    if not 1 <= len(pools) <= CSA_POOLS_MAX:
+        raise ValueError(f"1 to {CSA_POOLS_MAX} pools")
+    d.n_pools, d.n_pages = len(pools), n_pages
+    for i, t in enumerate(pools):
+        if t.shape[0] < n_pages or not t[0].is_contiguous():
+            raise ValueError("a pool holds n_pages pages, each contiguous")
+        d.base[i] = _ptr(t)
+        d.page_bytes[i] = t[0].numel() * t.element_size()
+        d.page_stride[i] = t.stride(0) * t.element_size()
+    d._keep = tuple(pools)
+    return d
+
+
+def csa_pages_workspace_size(n_pages: int) -> int:
+    return int(lib().csa_pages_workspace_size(n_pages))
+
+
+def csa_pages_alloc(refs, n_pages: int, page_table, table_stride: int, B: int, first, count, workspace=None,
+                    ws_bytes: int = 0, stream=None) -> None:
+    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(n_pages), refs, stream)
+    _check(lib().csa_pages_alloc(_ptr(refs), n_pages, _ptr(page_table), table_stride, B, _ptr(first), _ptr(count),
+                                 _ptr(ws), ws_bytes, _stream(stream)), "csa_pages_alloc")
+
+
+def csa_pages_free(refs, n_pages: int, page_table, table_stride: int, B: int, rows, R: int, stream=None) -> None:
+    _check(lib().csa_pages_free(_ptr(refs), n_pages, _ptr(page_table), table_stride, B, _ptr(rows), R,
+                                _stream(stream)), "csa_pages_free")
+
+
+def csa_pages_fork(pools: csa_page_pools, refs, page_table, table_stride: int, B: int, src, dst, F: int, n_tokens,
+                   rows_per_page: int, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(pools.n_pages), refs, stream)
+    _check(lib().csa_pages_fork(ctypes.byref(pools), _ptr(refs), _ptr(page_table), table_stride, B, _ptr(src),
+                                _ptr(dst), F, _ptr(n_tokens), rows_per_page, _ptr(ws), ws_bytes, _stream(stream)),
+           "csa_pages_fork")
+
+
+def csa_pages_compact(pools: csa_page_pools, refs, refs_out, page_table, page_table_out, table_stride: int, B: int,
+                      n_used=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
+    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(pools.n_pages), refs, stream)
+    _check(lib().csa_pages_compact(ctypes.byref(pools), _ptr(refs), _ptr(refs_out), _ptr(page_table),
+                                   _ptr(page_table_out), table_stride, B, _ptr(n_used), _ptr(ws), ws_bytes,
+                                   _stream(stream)), "csa_pages_compact")
+
+
+def csa_pages_copy(pools: csa_page_pools, src, dst, n: int, stream=None) -> None:
+    _check(lib().csa_pages_copy(ctypes.byref(pools), _ptr(src), _ptr(dst), n, _stream(stream)), "csa_pages_copy")
 
 
 def csa_decode_workspace_size(p: csa_decode_params) -> int:

@@ -72,21 +72,6 @@ cudaError_t set_func_attr_once(const void* func, cudaFuncAttribute attr, int val
 // Query positions per request from which the decode step scores through the tensor-core bounds.
 constexpr int kBoundMinQueries = 2;
 
-static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-static bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-static csa_status from_cuda(cudaError_t e) {
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
-}
-
-static csa_status check_paged(const csa_paged& p, int row_bytes) {
-    if (!p.base || !al16(p.base)) return CSA_ERR_INVALID_ARG;
-    if (p.rows_per_page < 1 || p.page_stride_bytes % 16 || p.n_pages < 1) return CSA_ERR_INVALID_ARG;
-    if ((int64_t)p.rows_per_page * row_bytes > p.page_stride_bytes) return CSA_ERR_INVALID_ARG;
-    return CSA_OK;
-}
-
 static HPaged host_paged(const csa_paged& p) {
     HPaged h;
     h.base = p.base;
@@ -117,6 +102,7 @@ const char* csa_status_string(csa_status s) {
         case CSA_ERR_TIMEOUT: return "device wait timed out";
         case CSA_ERR_DEVICE_BOUNDS: return "device bounds check failed";
         case CSA_ERR_WORKSPACE: return "workspace missing or too small";
+        case CSA_ERR_NO_PAGES: return "no free page left in the pool";
     }
     return "unknown status";
 }

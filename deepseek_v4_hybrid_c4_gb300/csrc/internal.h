@@ -19,6 +19,21 @@ inline int bound_hist_bits(int nq) { return nq <= 1 ? 14 : (nq == 2 ? 13 : 12); 
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Argument checks and the status of a launch, shared by the entry points.
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool al8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline csa_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+inline csa_status check_paged(const csa_paged& p, int row_bytes) {
+    if (!p.base || !al16(p.base)) return CSA_ERR_INVALID_ARG;
+    if (p.rows_per_page < 1 || p.page_stride_bytes % 16 || p.n_pages < 1) return CSA_ERR_INVALID_ARG;
+    if ((int64_t)p.rows_per_page * row_bytes > p.page_stride_bytes) return CSA_ERR_INVALID_ARG;
+    return CSA_OK;
+}
+
 // Per-device launch facts, safe to call from several host threads and on several devices:
 // the current device's SM count (0 on failure), and a kernel attribute set per device
 // (cudaFuncSetAttribute applies to the current device only) -- again whenever the value asked for

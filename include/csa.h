@@ -56,7 +56,8 @@ typedef enum {
     CSA_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
     CSA_ERR_TIMEOUT = 4,       /* device status: a bounded wait ran out */
     CSA_ERR_DEVICE_BOUNDS = 5, /* device status: a page id / index outside its pool (access skipped) */
-    CSA_ERR_WORKSPACE = 6      /* workspace missing or smaller than the *_workspace_size query */
+    CSA_ERR_WORKSPACE = 6,     /* workspace missing or smaller than the *_workspace_size query */
+    CSA_ERR_NO_PAGES = 7       /* device status: a page was asked for and the pool has no free one left */
 } csa_status;
 
 typedef enum { CSA_BF16 = 0, CSA_FP8_E4M3 = 1, CSA_FP32 = 2 } csa_dtype;
@@ -237,6 +238,132 @@ csa_status csa_sparse_attn_partial(const void* q, int32_t H, float scale, csa_pa
  * Partials with lse = -inf contribute nothing; if all are empty, out = 0 and lse = -inf.
  */
 csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t R, int32_t H, void* out, float* lse,
+                          void* stream);
+
+/*
+ * Dense attention of one token per request over a batch whose requests share their first rows (a
+ * prompt sampled many times, beams, a common document): the shared rows are attended once for the
+ * whole batch, B * H query rows at a time, instead of once per request.
+ * kv: bf16 latent rows of 1024 B; kv.page_table [B, page_table_stride] (required) gives request
+ * b's pages in its row b.  The first n_shared logical rows are the same for every request and are
+ * read through row 0 of the table; rows n_shared .. n_rows[b]-1 are request b's own, read through
+ * row b (csa_pages_fork makes such tables).  For request b and head h, over j < n_rows[b]:
+ *   l_j = scale * q_bh . K_j,  o_bh = softmax(l) . V   (K = V = the row)
+ * q bf16 [B, H, 512]; n_rows device int64 [B], 0 <= n_rows[b] <= max_rows (above it: the excess is
+ * not read and the device status gets CSA_ERR_DEVICE_BOUNDS); n_rows[b] may be below n_shared, and
+ * 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32 [B, H] (natural
+ * log, nullable).  Entries of the page table behind a request's rows are not read.  A page id
+ * outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
+ * infinity reaches only the requests that attend it.
+ * B * H rows are padded to 128-row tensor-core tiles; key ranges are split and merged by
+ * log-sum-exp, in a fixed order: the same inputs give the same bits.
+ * 1 <= H <= 128, 1 <= B <= 65535, 0 <= n_shared <= max_rows <= 2^31 - 1; page_stride_bytes a
+ * multiple of 1024 and n_pages * page_stride_bytes / 1024 < 2^31 (else CSA_ERR_UNSUPPORTED);
+ * page_table_stride * rows_per_page >= max_rows.  workspace: 16-byte aligned, at least
+ * csa_prefix_attn_workspace_size(B, H, n_shared, max_rows) bytes, contents overwritten.  Graph
+ * capture: yes.
+ */
+size_t csa_prefix_attn_workspace_size(int32_t B, int32_t H, int64_t n_shared, int64_t max_rows);
+csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa_paged kv, int64_t page_table_stride,
+                           int64_t n_shared, const int64_t* n_rows, int64_t max_rows, void* out, float* lse,
+                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention over a sliding window of the raw latent cache and the first tokens of the
+ * sequence (sinks, which stay visible): prompt chunks of any length, and single tokens.
+ * B sequences; sequence b's new tokens are rows q_offsets[b] .. q_offsets[b+1]-1 of q (device int64
+ * [B+1], non-decreasing) and are the last of its n_tokens[b] tokens (device int64 [B]), whose
+ * latent rows are in kv_raw already (kv_raw.page_table [B, page_table_stride], required).  The token
+ * at position p attends every position j <= p with j > p - window or j < n_sink:
+ *   l_j = scale * q_h . K_j,  o_h = softmax(l) . V   (K = V = the row)
+ * q bf16 [total_q, H, 512]; out bf16 [total_q, H, 512]; lse fp32 [total_q, H] (nullable).  Rows of
+ * out and lse that no sequence covers are left as they were.  total_q and max_q are host bounds: the
+ * rows of the buffers, and the most new tokens of a sequence; a sequence whose offsets leave them is
+ * skipped (CSA_ERR_DEVICE_BOUNDS).  A token before position 0 (more new tokens than n_tokens)
+ * sees nothing: out 0, lse -inf.  Pages that hold only positions no new token sees are not read and
+ * their table entries may be anything (a cache that gives the pages behind the window back).  A page
+ * id outside the pool, or a position behind page_table_stride pages, leaves its rows out
+ * (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an infinity reaches only the tokens that see it.
+ * The same inputs give the same bits.
+ * 1 <= H <= 128, 1 <= B <= 65535, 1 <= window <= 2^30, 0 <= n_sink <= 2^30, 0 <= total_q,
+ * total_q * H < 2^31 (else CSA_ERR_UNSUPPORTED), 1 <= max_q; the limits of csa_prefix_attn on kv.
+ * workspace: 16-byte aligned, csa_window_attn_workspace_size(...) bytes, contents overwritten
+ * (0 bytes where no key range is split).  Graph capture: yes.
+ */
+size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
+                                      int32_t n_sink);
+csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_raw, int64_t page_table_stride,
+                           int32_t B, const int64_t* q_offsets, const int64_t* n_tokens, int64_t total_q,
+                           int64_t max_q, int32_t window, int32_t n_sink, void* out, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * The pages that page tables name.  refs (device int32 [n_pages]) holds the number of table entries
+ * that name each page, 0 for a free page; it is the whole state of the pool, shared by the pools
+ * of a csa_page_pools (shadow paging: one page id, a page in every pool).  Page tables are device
+ * int32 [B, table_stride], -1 for an entry without a page.  New pages are the free pages of the
+ * lowest ids.  Nothing here waits for the host; every result is the same from run to run.  Calls on
+ * one refs array belong on one stream, or need events between them.
+ * workspace (alloc, fork, compact): 16-byte aligned, at least csa_pages_workspace_size(n_pages) bytes,
+ * contents overwritten.  1 <= n_pages <= 2^28, 1 <= B <= 65535, 1 <= table_stride <= 2^31 - 1 and
+ * B * table_stride <= 2^40.  Graph capture: yes.
+ */
+#define CSA_POOLS_MAX 4
+typedef struct {
+    int32_t n_pools;                        /* 1 .. CSA_POOLS_MAX */
+    int64_t n_pages;                        /* pages in every pool */
+    void* base[CSA_POOLS_MAX];              /* 16-byte aligned */
+    int64_t page_bytes[CSA_POOLS_MAX];      /* bytes of a page, a multiple of 16 */
+    int64_t page_stride[CSA_POOLS_MAX];     /* bytes between pages, a multiple of 16, >= page_bytes */
+} csa_page_pools;
+size_t csa_pages_workspace_size(int64_t n_pages);
+
+/* Request b's table entries first[b] .. first[b] + count[b] - 1 (device int32 [B]) get new pages,
+ * in (request, entry) order, with refs 1.  The entries' old values are overwritten (they should be
+ * -1).  Where the pool runs out: -1 and CSA_ERR_NO_PAGES.  A range outside the table is skipped
+ * (CSA_ERR_DEVICE_BOUNDS).  B <= 4096. */
+csa_status csa_pages_alloc(int32_t* refs, int64_t n_pages, int32_t* page_table, int64_t table_stride, int32_t B,
+                           const int32_t* first, const int32_t* count, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* The R table rows that rows lists (device int32 [R]) give their pages back: refs of every entry's
+ * page goes down by one and the entry becomes -1; a row listed twice gives its pages back once.  A row
+ * outside the table, a page id outside the pool or a page whose refs is 0 already is skipped
+ * (CSA_ERR_DEVICE_BOUNDS). */
+csa_status csa_pages_free(int32_t* refs, int64_t n_pages, int32_t* page_table, int64_t table_stride, int32_t B,
+                          const int32_t* rows, int32_t R, void* stream);
+
+/* Forks F requests: table row dst[f] becomes a copy of row src[f] (device int32 [F]) at the parent's
+ * n_tokens[src[f]] tokens (device int64 [B]; rows_per_page tokens to a page).  Whole pages are shared
+ * (their refs go up by one); a last, partly filled page is copied, in every pool, to a new page,
+ * so that parent and children can each write on; entries behind it become -1 and n_tokens[dst[f]]
+ * = n_tokens[src[f]].  New pages go to the children in the order of f.  Entries of the parent without a
+ * page (pages behind a window, given back) are -1 in the child too.  A child whose last page finds no
+ * free page keeps the whole pages and the tokens in them (CSA_ERR_NO_PAGES).  Entries that row dst[f] held
+ * before are overwritten: give them back first (csa_pages_free).  A child is skipped
+ * (CSA_ERR_DEVICE_BOUNDS) where a row is outside the table, dst[f] is a parent of this call or another
+ * child's row, or the parent's tokens do not fit its row; a page id outside the pool becomes -1
+ * (CSA_ERR_DEVICE_BOUNDS).  1 <= F <= 1024. */
+csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* page_table, int64_t table_stride,
+                          int32_t B, const int32_t* src, const int32_t* dst, int32_t F, int64_t* n_tokens,
+                          int32_t rows_per_page, void* workspace, size_t ws_bytes, void* stream);
+
+/* Moves the pages in use to the front of the pools: with U pages in use, those with an id of U or
+ * more are copied, in every pool and in the order of their ids, to the free ids below U, ascending.
+ * page_table_out and refs_out receive the tables and the counts after the move (in place where they
+ * are the same arrays; partly overlapping ones are not allowed); n_used (device int64, nullable) receives
+ * U.  The pages moved from keep their bytes, so that work enqueued with the old tables still reads
+ * the rows that it should until they are allocated again.  A table entry outside the pool, or
+ * naming a page whose refs is 0, is left as it is (CSA_ERR_DEVICE_BOUNDS; negative entries are no
+ * pages and cost nothing). */
+csa_status csa_pages_compact(const csa_page_pools* pools, const int32_t* refs, int32_t* refs_out,
+                             const int32_t* page_table, int32_t* page_table_out, int64_t table_stride, int32_t B,
+                             int64_t* n_used, void* workspace, size_t ws_bytes, void* stream);
+
+/* Copies page src[i] to page dst[i] (device int32 [n]) in every pool, all pairs at once: a page that is
+ * the destination of one pair may appear in no other pair (its bytes are unspecified otherwise).  A
+ * pair with an id outside the pool is skipped (CSA_ERR_DEVICE_BOUNDS). */
+csa_status csa_pages_copy(const csa_page_pools* pools, const int32_t* src, const int32_t* dst, int32_t n,
                           void* stream);
 
 /*
