@@ -110,6 +110,10 @@ cudaError_t launch_score(const ScoreLaunch& a, cudaStream_t s, bool pdl);
 // The TMA tensor map (a CUtensorMap at `map`) of an index-key pool seen as [pages][rows per
 // page][128 dims], box 16 rows x 128 B, 128-byte swizzle; false when it cannot be encoded.
 bool make_kidx_map(void* map, const HPaged& p, bool fp8, int64_t rows_per_page, int64_t n_pages);
+// A tensor map of nd (2 or 3) dimensions over bf16 data, 128-byte swizzle: extents and box in elements,
+// strides[i] the bytes between steps of dimension i + 1.
+bool make_bf16_map(void* map, const void* base, int nd, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box);
 // Stage 2 on the tensor cores, bf16 keys: for every candidate a bracket [lower, upper] that holds
 // the fixed-order score (upper to `scores`, lower to `lower` when set), and, with hist, the first
 // digit of the lower bounds' keys.  Needs Hi <= 16, nq <= 4.

@@ -4,115 +4,827 @@
 //
 //   l_j = scale * q . K_j,  o = sum_j softmax(l)_j V_j,  lse = ln sum_j exp(l_j)
 //
-// One warp per query row: a lane holds 16 of the row's 512 dims, a key's dot product is a warp
-// reduction, and the softmax is the running one (maximum m, sum l, O rescaled when m moves).
+// Both are the same work: 128 query rows (heads of one or several tokens or requests) against a list of
+// key rows.  A pair of CTAs (one cluster, one CTA per SM) takes an item: 128 query rows and the
+// key rows of one or more tiles of 128.  The tensor-core products run over the pair (tcgen05, cta_group::2,
+// M = 128): each CTA holds 64 of the query rows, and
+//   S = Q K^T   N = 128 keys, K = 512: each CTA stages half of the tile's keys, all dims
+//   O += P V    N = 256 twice, K = 128: each CTA stages all of the tile's keys, half of the dims
+// so that the 128 x 512 fp32 accumulator takes 256 of the pair's TMEM columns and S another 64 (two
+// buffers), where a single CTA would need all of its TMEM for O alone (and with O cut in two along its
+// dims would have to compute S twice).  Measured on GB300 with nothing but these products in flight: 2,056 cycles
+// a tile against 2,048 at the nominal rate.
+//
+// Roles (10 warps a CTA): warps 0-3 own the TMEM lanes (softmax, output); warps 4-7 load key rows; warp 8
+// issues the products (even CTA) or passes on that the odd CTA's rows have landed; warp 9 loads Q.
+// Key rows come through a ring of 8 slots of 16 KB in the order in which the products take them: S of a tile
+// in four slots (128 dims each of the CTA's own keys), P V in up to four (32 keys each, the CTA's
+// half of the dims).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
+// Key rows are copied by TMA in the products' swizzle: boxes of 16 rows where 16 rows always share a page
+// (rows_per_page a multiple of 16), four-row gathers otherwise.  The list of key rows is made of
+// 16-row units; rows of a unit that no query sees are masked.
+//
+// Softmax: a thread holds one row's logits of half of a tile; the row's two threads exchange their
+// maxima.  The running maximum moves only when a tile exceeds it by 2^8 (O is then rescaled in TMEM);
+// P is rounded to bf16 for the product, its sum is taken in fp32 before the rounding.
+//
+// A masked weight is exactly 0, but 0 * NaN is NaN, and the products see every row of a unit.  In
+// a tile with masked rows a NaN or an infinity in any row makes that row's logits of all 128 query rows
+// non-finite; where a thread finds one, its CTA replaces the non-finite values of the tile's V rows by 0 before the
+// product.  Query rows that do attend such a key have a NaN weight from its logit and stay NaN.
+#include <cuda.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace csa {
 
+constexpr int LP_T = 320;
+constexpr int LP_SLOTS = 8;
+constexpr int LP_PAIRS = 76;                              // pairs of SMs: sizes the splits (and so the workspace)
+constexpr uint32_t LP_SLOT = 16384;
+constexpr uint32_t LP_QSLAB = 64 * 128;                   // 64 dims of the CTA's 64 query rows
+constexpr uint32_t LP_SM_RING = 8 * LP_QSLAB;             // behind Q
+constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 64 keys x 64 rows; output staging
+constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
+constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_QFULL = LP_EMPTY + 64, LP_QEMPTY = LP_QFULL + 8;
+constexpr uint32_t LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16, LP_PVDONE = LP_PREADY + 8;
+constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 256, LP_SM_DEAD = LP_SM_TMEM + 8;
+constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits
+constexpr uint32_t LP_SM_MAX = LP_SM_VALID + 128;         // [2][128] row maxima of the threads
+constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 1024;          // [128] row sums of the threads
+constexpr uint32_t LP_SMEM = LP_SM_SUM + 512 + 1024;      // + alignment slack
+static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
+constexpr float LP_LOG2E = 1.4426950408889634f;
+constexpr float LP_LN2 = 0.6931471805599453f;
+constexpr float LP_RESCALE = 8.0f;                        // log2 units
+
 struct LatArgs {
-    const uint16_t* q;
     int H;
-    float scale;
+    float sl2;                 // scale * log2(e)
     DPaged kv;
     int64_t table_pages;       // entries of a request's page table
+    int B;
     // prefix: request b = row / H sees rows [0, n_rows[b]); rows below n_shared through table row 0
-    const int64_t* n_rows;
-    int64_t n_shared, max_rows;
-    // window (q_offsets set): B sequences
+    const int64_t* n_rows;     // nullptr: window
+    int n_shared, max_rows;
+    int RT, SP, OS;            // row tiles over the batch; splits of the shared rows, of a request's own rows
+    // window: B sequences
     const int64_t* q_offsets;
     const int64_t* n_tokens;
     int64_t total_q, max_q;
     int window, n_sink;
-    int B;
+    int WS;                    // splits of a row tile's keys
+    int rows;                  // query rows in all (B * H, total_q * H)
+    int parts;                 // partial results of a row (1: written to out directly)
+    float* part_o;             // [parts][rows][512] normalised
+    float* part_lse;           // [parts][rows]
     uint16_t* out;
     float* lse;
     int32_t* status;
 };
 
-__device__ __forceinline__ const uint8_t* lat_row(const LatArgs& a, int b, int64_t r) {
-    if (r / a.kv.rpp >= a.table_pages) {
-        raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-        return nullptr;
-    }
-    return row_addr(a.kv, b, r, ROW_BYTES, a.status);
+// An item: query rows [row0, row0 + nrows) against tiles [t0, t0 + T) of a list of 16-row units: units
+// [0, uA) of the request (sinks), then units uB, uB + 1, ..., nU in all.
+struct LatItem {
+    int T, t0, nU, uA, uB;
+    int row0, nrows;
+    int trow;                  // page-table row
+    int part;
+    int a1, lo, hi;            // rows that a query of the item may see: [0, a1) and [lo, hi)
+    int full_lo, full_hi;      // rows that every query of the item sees
+    int rr0;                   // window: first query row within its sequence
+    int64_t pos0;              // window: position of the sequence's first new token
+    bool shared;               // prefix: the shared rows (else request trow's own)
+};
+
+// Sequences by row tiles, 32 at a time, one per lane; item indices ascend.
+struct SeqCursor {
+    int c0 = -32, base = 0, total = 0;
+    int incl = 0, tiles = 0, ql = 0;
+    int64_t q0 = 0, nt = 0;
+};
+
+__device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t q1, int64_t nt) {
+    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q && nt <= 0x7FFFFFFF;
 }
 
-__global__ void __launch_bounds__(256) lat_rows_kernel(LatArgs a, int64_t rows) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    int b = 0;
-    int64_t sink_hi = 0, lo = 0, hi = 0;
-    if (a.q_offsets) {
-        const int64_t t = row / a.H;
-        int l = 0, r = a.B;  // the last sequence that starts at or before t
+__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
+
+// Item number `it` (warp-collective), or false behind the last one.
+__device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
+    int split, splits;
+    if (a.n_rows) {
+        if (it >= a.RT * a.SP + a.B * a.OS) return false;
+        int kb0, kb1;
+        x.shared = it < a.RT * a.SP;
+        x.a1 = x.uA = x.rr0 = 0;
+        x.pos0 = 0;
+        if (x.shared) {  // neighbouring items read the same keys
+            split = it / a.RT;
+            splits = a.SP;
+            x.row0 = (it - split * a.RT) * 128;
+            x.nrows = min(128, a.rows - x.row0);
+            x.trow = 0;
+            x.part = split;
+            // the shortest and the longest of the rows' requests
+            const int b0 = x.row0 / a.H, b1 = (x.row0 + x.nrows - 1) / a.H;
+            int mn = 0x7FFFFFFF, mx = 0;
+            for (int b = b0 + lane; b <= b1; b += 32) {
+                const int64_t n = __ldg(a.n_rows + b);
+                const int c = n < 0 ? 0 : (n > a.n_shared ? a.n_shared : (int)n);
+                mn = min(mn, c);
+                mx = max(mx, c);
+            }
+            for (int o = 16; o; o >>= 1) {
+                mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            }
+            kb0 = 0;
+            kb1 = mx;
+            x.full_lo = 0;
+            x.full_hi = mn;
+            x.nU = ceil_div(a.n_shared, 16);  // the same split of the keys for every row tile
+        } else {
+            const int j = it - a.RT * a.SP, b = j / a.OS;
+            split = j - b * a.OS;
+            splits = a.OS;
+            x.row0 = b * a.H;
+            x.nrows = a.H;
+            x.trow = b;
+            x.part = a.SP + split;
+            const int64_t n = __ldg(a.n_rows + b);
+            if (report && lane == 0 && split == 0 && (n < 0 || n > a.max_rows)) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+            kb0 = a.n_shared;
+            kb1 = n < 0 ? 0 : (n > a.max_rows ? a.max_rows : (int)n);
+            x.full_lo = kb0;
+            x.full_hi = kb1;
+            x.nU = kb1 > kb0 ? ceil_div(kb1, 16) - kb0 / 16 : 0;
+        }
+        x.uB = kb0 / 16;
+        x.lo = kb0;
+        x.hi = kb1;
+    } else {
+        while (it >= cur.base + cur.total) {
+            cur.base += cur.total;
+            cur.c0 += 32;
+            if (cur.c0 >= a.B) return false;
+            const int b = cur.c0 + lane;
+            cur.tiles = 0;
+            if (b < a.B) {
+                cur.q0 = __ldg(a.q_offsets + b);
+                const int64_t q1 = __ldg(a.q_offsets + b + 1);
+                cur.nt = __ldg(a.n_tokens + b);
+                if (seq_valid(a, cur.q0, q1, cur.nt)) {
+                    cur.ql = (int)(q1 - cur.q0);
+                    cur.tiles = ceil_div(cur.ql * a.H, 128) * a.WS;
+                } else if (report) {
+                    raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+                }
+            }
+            cur.incl = cur.tiles;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, cur.incl, o);
+                if (lane >= o) cur.incl += v;
+            }
+            cur.total = __shfl_sync(0xffffffffu, cur.incl, 31);
+        }
+        const int at = it - cur.base;
+        const int src = __ffs(__ballot_sync(0xffffffffu, cur.incl > at)) - 1;
+        const int d = at - __shfl_sync(0xffffffffu, cur.incl - cur.tiles, src);
+        const int ql = __shfl_sync(0xffffffffu, cur.ql, src);
+        const int64_t q0 = __shfl_sync(0xffffffffu, cur.q0, src), nt = __shfl_sync(0xffffffffu, cur.nt, src);
+        splits = a.WS;
+        split = d % a.WS;
+        x.rr0 = d / a.WS * 128;
+        x.nrows = min(128, ql * a.H - x.rr0);
+        x.row0 = (int)q0 * a.H + x.rr0;
+        x.trow = cur.c0 + src;
+        x.part = split;
+        x.shared = false;
+        x.pos0 = (nt > 0 ? nt : 0) - ql;
+        const int64_t p0 = x.pos0 + x.rr0 / a.H, p1 = x.pos0 + (x.rr0 + x.nrows - 1) / a.H;
+        x.hi = p1 >= 0 ? (int)p1 + 1 : 0;
+        x.lo = p0 >= a.window ? (int)p0 - a.window + 1 : 0;
+        x.a1 = min(a.n_sink, x.hi);
+        x.uA = min(ceil_div(x.a1, 16), ceil_div(x.hi, 16));
+        x.uB = max(x.lo / 16, x.uA);
+        x.nU = x.uA + max(0, ceil_div(x.hi, 16) - x.uB);
+        x.full_lo = p1 >= a.window ? (int)p1 - a.window + 1 : 0;
+        x.full_hi = p0 >= 0 ? (int)p0 + 1 : 0;
+    }
+    const int tiles = ceil_div(x.nU, 8);
+    x.t0 = (int)((int64_t)tiles * split / splits);
+    x.T = (int)((int64_t)tiles * (split + 1) / splits) - x.t0;
+    if (x.shared && x.t0 * 128 >= x.hi) x.T = 0;
+    return true;
+}
+
+__device__ __forceinline__ int item_units(const LatItem& x, int i) { return min(8, x.nU - (x.t0 + i) * 8); }
+__device__ __forceinline__ int unit_row(const LatItem& x, int u) { return (u < x.uA ? u : u - x.uA + x.uB) * 16; }
+
+// Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
+// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
+// further wait returning at once.
+__device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+    for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (*dead) return false;
+        if (i >= 32) __nanosleep(64);
+    }
+    *dead = 1;
+    return false;
+}
+
+__device__ __forceinline__ float lat_ex2(float x) {  // ex2.approx.ftz: relative error below 2^-22
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The lookups of a tile, one lane's share.  Boxes: lane u's unit (page id, row within the page);
+// gathers: the page ids of rows 4 lane .. 4 lane + 3.  Loads only: nothing waits for them here.
+struct TileRef {
+    int pp[4];
+    int slot[4];
+    int need;  // bits of the rows (unit) that are looked up and inside the table
+};
+
+template <bool BOX>
+__device__ __forceinline__ TileRef tile_issue(const LatArgs& a, const LatItem& x, int i, int lane) {
+    TileRef r;
+    r.need = 0;
+    const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
+    const int u0 = (x.t0 + i) * 8;
+#pragma unroll
+    for (int e = 0; e < (BOX ? 1 : 4); ++e) {
+        r.pp[e] = r.slot[e] = 0;
+        const int k = lane * 4 + e;
+        const int u = u0 + (BOX ? lane : k >> 4);
+        if (BOX ? lane >= 8 : false) continue;
+        if (u >= x.nU) continue;
+        const int j = unit_row(x, u) + (BOX ? 0 : k & 15);
+        if (BOX) {
+            if (j >= x.hi) continue;                     // a unit behind the last row that is seen
+        } else if (!(j < x.a1 || (j >= x.lo && j < x.hi))) {
+            continue;                                    // a row of the unit that no query sees
+        }
+        const uint32_t lp = (uint32_t)j / (uint32_t)a.kv.rpp;
+        r.slot[e] = j - (int)lp * a.kv.rpp;
+        if ((int64_t)lp >= a.table_pages) {
+            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+            continue;
+        }
+        r.need |= 1 << e;
+        r.pp[e] = __ldg(pt + lp);
+    }
+    return r;
+}
+
+template <bool BOX>
+__device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensorMap& kmap, const LatArgs& a) {
+    extern __shared__ uint8_t lp_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lp_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(sm + LP_SM_DEAD);
+
+    if (warp == 0) {
+        tmem_alloc_pair(sb + LP_SM_TMEM, 512);
+        tmem_relinquish_pair();
+    }
+    if (tid == 32) {
+        for (int i = 0; i < LP_SLOTS; ++i) {
+            mbar_init(sb + LP_FULL + 8 * i, rank == 0 ? 2 : 1);  // this CTA's rows (and the other's)
+            mbar_init(sb + LP_EMPTY + 8 * i, 1);
+        }
+        mbar_init(sb + LP_QFULL, rank == 0 ? 2 : 1);
+        mbar_init(sb + LP_QEMPTY, 1);
+        mbar_init(sb + LP_SFULL, 1);
+        mbar_init(sb + LP_SFULL + 8, 1);
+        mbar_init(sb + LP_PREADY, 8);  // the softmax warps of both CTAs
+        mbar_init(sb + LP_PVDONE, 1);
+        *dead = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LP_SM_TMEM);
+    SeqCursor cur;
+    LatItem x;
+    int sidx = 0, g = 0, n = 0;  // ring slots, tiles and items so far
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---------------------------------------------------------------- softmax and output
+        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+        const int r = tid & 63, half = tid >> 6;
+        float* mx = reinterpret_cast<float*>(sm + LP_SM_MAX);
+        float* ls = reinterpret_cast<float*>(sm + LP_SM_SUM);
+        for (int it = pair; lat_item(a, cur, it, lane, warp == 0 && rank == 0, x); it += pairs) {
+            const int row = x.row0 + (int)rank * 64 + r;  // this thread's query row
+            const bool mine = (int)rank * 64 + r < x.nrows;
+            // rows that this query sees: [vlo, vhi) and [0, vs)
+            int vlo = 0, vhi = 0, vs = 0;
+            if (mine) {
+                if (!a.n_rows) {
+                    const int64_t pos = x.pos0 + (x.rr0 + (int)rank * 64 + r) / a.H;
+                    vhi = pos >= 0 ? (int)pos + 1 : 0;
+                    vlo = max(0, vhi - a.window);
+                    vs = min(a.n_sink, vhi);
+                } else if (x.shared) {
+                    const int64_t nr = __ldg(a.n_rows + row / a.H);
+                    vhi = nr < 0 ? 0 : (nr > x.hi ? x.hi : (int)nr);
+                } else {
+                    vlo = x.lo;
+                    vhi = x.hi;
+                }
+            }
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int i = 0; i < x.T; ++i, ++g) {
+                const int nu = item_units(x, i), mu = (nu + 1) >> 1;  // units in all, and per half
+                const int u0 = (x.t0 + i) * 8;
+                ok = lat_wait(sb + LP_SFULL + 8 * (g & 1), (g >> 1) & 1, dead) && ok;
+                tc_fence_after();
+                const uint32_t* vw = reinterpret_cast<const uint32_t*>(sm + LP_SM_VALID) + (g & 7) * 4;
+                const uint32_t v0 = vw[0], v1 = vw[1], v2 = vw[2], v3 = vw[3];
+                // every row of the tile seen by every query of the item, and every page there
+                const bool plain = nu == 8 && (v0 & v1 & v2 & v3) == 0xffffffffu && u0 >= x.uA &&
+                                   unit_row(x, u0) >= x.full_lo && unit_row(x, u0 + 7) + 16 <= x.full_hi;
+                uint32_t sr[64];
+                const uint32_t ts = tmem + 256 + (uint32_t)(g & 1) * 64 + lane_off;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < mu) tc_ld16(ts + 16 * c, sr + 16 * c);
+                tc_wait_ld();
+                float mt = -INFINITY;
+                bool bad = false;
+                float* xs = reinterpret_cast<float*>(sr);
+                if (plain) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        xs[j] = __uint_as_float(sr[j]) * a.sl2;
+                        mt = fmaxf(mt, xs[j]);
+                    }
+                } else {
+                    float z = 0.f;  // NaN where a logit of the tile is not finite
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c < mu) {
+                            const int u = half * mu + c;
+                            uint32_t bits = 0;
+                            if (u < nu) {
+                                const int jb = unit_row(x, u0 + u);
+                                const int e0 = min(max(vlo - jb, 0), 16), e1 = min(max(vhi - jb, 0), 16);
+                                const int e2 = min(max(vs - jb, 0), 16);
+                                bits = (((1u << e1) - 1u) & ~((1u << e0) - 1u)) | ((1u << e2) - 1u);
+                                const uint32_t vv = u < 4 ? (u < 2 ? v0 : v1) : (u < 6 ? v2 : v3);
+                                bits &= vv >> ((u & 1) * 16);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float s = __uint_as_float(sr[16 * c + j]);
+                                if (u < nu) z = fmaf(s, 0.f, z);
+                                xs[16 * c + j] = (bits >> j) & 1u ? s * a.sl2 : -INFINITY;
+                                mt = fmaxf(mt, xs[16 * c + j]);
+                            }
+                        }
+                    }
+                    bad = !(z == 0.f);
+                }
+                // the row's other half, and whether any logit of the tile is not finite
+                float* mb = mx + (g & 1) * 128;
+                mb[tid] = mt;
+                const bool any_bad = named_bar_any(1, 128, bad);
+                mt = fmaxf(mt, mb[tid ^ 64]);
+                float alpha = 1.f;
+                if (mt > -INFINITY) {
+                    if (m_run == -INFINITY) {
+                        m_run = mt;
+                    } else if (mt > m_run + LP_RESCALE) {
+                        alpha = lat_ex2(m_run - mt);
+                        m_run = mt;
+                    }
+                }
+                const float mref = m_run == -INFINITY ? 0.f : m_run;
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < mu) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float p0 = lat_ex2(xs[16 * c + j] - mref), p1 = lat_ex2(xs[16 * c + j + 1] - mref);
+                            sum0 += p0;
+                            sum1 += p1;
+                            sr[8 * c + (j >> 1)] = pack_bf16x2(p0, p1);
+                        }
+                    }
+                }
+                l_run = l_run * alpha + (sum0 + sum1);
+                // P and O are free once the product before this one is done
+                if (i > 0) {
+                    ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < 256; c += 32) {
+                            uint32_t o[32];
+                            tc_ld32(tmem + lane_off + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc_st32(tmem + lane_off + c, o);
+                        }
+                        tc_wait_st();
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < mu) {
+                        const int u = half * mu + c;
+                        const uint32_t pb = sb + LP_SM_P + (uint32_t)(u >> 2) * LP_QSLAB + (uint32_t)r * 128;
+#pragma unroll
+                        for (int h2 = 0; h2 < 2; ++h2)
+                            st_shared_v4(pb + ((uint32_t)(((u & 3) * 2 + h2) ^ (r & 7)) << 4),
+                                         make_uint4(sr[8 * c + 4 * h2], sr[8 * c + 4 * h2 + 1], sr[8 * c + 4 * h2 + 2],
+                                                    sr[8 * c + 4 * h2 + 3]));
+                    }
+                }
+                if (any_bad) {  // non-finite values of this CTA's V rows -> 0
+                    const int vs0 = sidx + 4 * min(i + 2, x.T) + 4 * i;
+                    for (int s = 0; s < (nu + 1) >> 1; ++s) {
+                        const int sl = (vs0 + s) & (LP_SLOTS - 1);
+                        ok = lat_wait(sb + LP_FULL + 8 * sl, ((vs0 + s) / LP_SLOTS) & 1, dead) && ok;
+                        const uint32_t bytes = (uint32_t)min(2, nu - 2 * s) * 2048u;  // of each 4,096-byte slab
+                        for (uint32_t c = tid * 16; c < LP_SLOT; c += 128 * 16) {
+                            if ((c & 4095u) >= bytes) continue;
+                            const uint32_t ad = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT + c;
+                            uint4 v = ld_shared_v4(ad);
+                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                                if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+                            }
+                            st_shared_v4(ad, v);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_rank(sb + LP_PREADY, 0);
+            }
+            if (x.T > 0) {
+                sidx += 8 * x.T - 4 + ((item_units(x, x.T - 1) + 1) >> 1);
+                ls[tid] = l_run;
+                ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
+                tc_fence_after();
+                named_bar_sync(1, 128);
+                l_run += ls[tid ^ 64];
+            }
+            // ---- rows [32 (warp & 1), + 32) of the CTA, dims [256 half, + 256): normalised, staged 128 bytes a row
+            //      in the P buffer, written 128 bytes a row
+            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const uint32_t stg = sb + LP_SM_P + (uint32_t)warp * 4096;
+            const bool direct = a.parts == 1;
+            const int wrow = (int)rank * 64 + (warp & 1) * 32;  // the warp's first row of the item
+            if (direct || x.T > 0) {
+#pragma unroll 1
+                for (int c = 0; c < (direct ? 4 : 8); ++c) {
+                    uint32_t w[32];
+                    if (x.T == 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = 0;
+                    } else if (direct) {
+                        uint32_t o[64];
+                        tc_ld32(tmem + lane_off + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
+                        tc_ld32(tmem + lane_off + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                    } else {
+                        tc_ld32(tmem + lane_off + 32 * c, w);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(stg + lane * 128 + ((uint32_t)(e ^ (lane & 7)) << 4),
+                                     make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = e * 4 + (lane >> 3);
+                        if (wrow + rr < x.nrows) {
+                            const uint4 v = ld_shared_v4(stg + rr * 128 + ((uint32_t)((lane & 7) ^ (rr & 7)) << 4));
+                            const int64_t gr = x.row0 + wrow + rr;
+                            uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out + gr * D + half * 256 + c * 64)
+                                                  : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr) * D +
+                                                                               half * 256 + c * 32);
+                            *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
+                        }
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+            }
+            if (tid < 64 && mine) {
+                const float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
+                if (!direct) a.part_lse[(int64_t)x.part * a.rows + row] = e;
+                else if (a.lse) a.lse[row] = e;
+            }
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- key rows
+        const int w = warp - 4;
+        auto claim = [&](uint32_t bytes) -> bool {  // slot sidx: free, and its bytes announced
+            const int sl = sidx & (LP_SLOTS - 1);
+            if (sidx >= LP_SLOTS && !lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)) return false;
+            if (lane == 0) {
+                if (bytes) mbar_arrive_expect_tx(sb + LP_FULL + 8 * sl, bytes);
+                else mbar_arrive(sb + LP_FULL + 8 * sl);
+            }
+            __syncwarp();
+            return true;
+        };
+        // ids of the tile's rows, checked: TMA coordinates (page, row) of lane u's unit, or four row ids
+        auto resolve = [&](TileRef& t) -> uint32_t {
+            uint32_t good = 0;
+#pragma unroll
+            for (int e = 0; e < (BOX ? 1 : 4); ++e) {
+                const bool in = (t.need >> e) & 1;
+                const bool there = in && t.pp[e] >= 0 && t.pp[e] < a.kv.n_pages;
+                if (in && !there) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+                if (there) good |= 1u << e;
+                if (BOX) {
+                    if (!there) t.pp[e] = 0;
+                    if (!there) t.slot[e] = 0;
+                } else {
+                    t.pp[e] = there ? t.pp[e] * (int)(a.kv.page_stride / ROW_BYTES) + t.slot[e] : 0;
+                }
+            }
+            return good;
+        };
+        auto emit_k = [&](TileRef& t, uint32_t good, int nu) -> bool {
+            const int mu = (nu + 1) >> 1, ku = min(max(nu - (int)rank * mu, 0), mu);
+            for (int kk = 0; kk < 4; ++kk, ++sidx) {
+                if ((sidx & 3) != w) continue;
+                if (kk == 0) {  // which rows are there, for the softmax
+                    uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + (g & 7) * 4;
+                    if (BOX) {
+                        const uint32_t b = __ballot_sync(0xffffffffu, good);
+                        if (lane < 4)
+                            vw[lane] = ((b >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((b >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
+                    } else {
+                        uint32_t v = good << (4 * (lane & 7));
+                        v |= __shfl_xor_sync(0xffffffffu, v, 1);
+                        v |= __shfl_xor_sync(0xffffffffu, v, 2);
+                        v |= __shfl_xor_sync(0xffffffffu, v, 4);
+                        if ((lane & 7) == 0) vw[lane >> 3] = v;
+                    }
+                    __syncwarp();
+                }
+                const int sl = sidx & (LP_SLOTS - 1);
+                const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = sb + LP_FULL + 8 * sl;
+                if (BOX) {
+                    const int slab = lane >> 2, i = lane & 3;
+                    const int pg = __shfl_sync(0xffffffffu, t.pp[0], ((int)rank * mu + i) & 7);
+                    const int rw = __shfl_sync(0xffffffffu, t.slot[0], ((int)rank * mu + i) & 7);
+                    if (!claim((uint32_t)ku * 4096u)) return false;
+                    if (lane < 8 && i < ku) tma_load_3d(dst + slab * 8192 + i * 2048, &kmap, (2 * kk + slab) * 64, rw, pg, bar);
+                } else {
+                    const int slab = lane >> 4, qd = lane & 15, from = ((int)rank * mu * 4 + qd) & 31;
+                    int4 id;
+                    id.x = __shfl_sync(0xffffffffu, t.pp[0], from);
+                    id.y = __shfl_sync(0xffffffffu, t.pp[1], from);
+                    id.z = __shfl_sync(0xffffffffu, t.pp[2], from);
+                    id.w = __shfl_sync(0xffffffffu, t.pp[3], from);
+                    if (!claim((uint32_t)ku * 4096u)) return false;
+                    if (qd < 4 * ku) tma_gather4(dst + slab * 8192 + qd * 512, &kmap, (2 * kk + slab) * 64, id, bar);
+                }
+            }
+            return true;
+        };
+        auto emit_v = [&](const TileRef& t, int nu) -> bool {
+            for (int v = 0; v < (nu + 1) >> 1; ++v, ++sidx) {
+                if ((sidx & 3) != w) continue;
+                const int vu = min(2, nu - 2 * v);
+                const int sl = sidx & (LP_SLOTS - 1);
+                const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = sb + LP_FULL + 8 * sl;
+                if (BOX) {
+                    const int i = lane & 1, s = (lane >> 1) & 3;
+                    const int pg = __shfl_sync(0xffffffffu, t.pp[0], 2 * v + i);
+                    const int rw = __shfl_sync(0xffffffffu, t.slot[0], 2 * v + i);
+                    if (!claim((uint32_t)vu * 8192u)) return false;
+                    if (lane < 8 && i < vu)
+                        tma_load_3d(dst + s * 4096 + i * 2048, &kmap, (int)rank * 256 + s * 64, rw, pg, bar);
+                } else {
+                    const int s = lane >> 3, qd = lane & 7, from = v * 8 + qd;
+                    int4 id;
+                    id.x = __shfl_sync(0xffffffffu, t.pp[0], from);
+                    id.y = __shfl_sync(0xffffffffu, t.pp[1], from);
+                    id.z = __shfl_sync(0xffffffffu, t.pp[2], from);
+                    id.w = __shfl_sync(0xffffffffu, t.pp[3], from);
+                    if (!claim((uint32_t)vu * 8192u)) return false;
+                    if (qd < 4 * vu) tma_gather4(dst + s * 4096 + qd * 512, &kmap, (int)rank * 256 + s * 64, id, bar);
+                }
+            }
+            return true;
+        };
+        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
+            if (x.T == 0) continue;
+            TileRef now = tile_issue<BOX>(a, x, 0, lane), next = now;
+            if (x.T > 1) next = tile_issue<BOX>(a, x, 1, lane);
+            uint32_t good = resolve(now);
+            ok = emit_k(now, good, item_units(x, 0));
+            for (int i = 0; ok && i < x.T; ++i) {
+                TileRef after = next;
+                ++g;
+                if (i + 1 < x.T) {
+                    good = resolve(next);
+                    ok = emit_k(next, good, item_units(x, i + 1));
+                    if (i + 2 < x.T) after = tile_issue<BOX>(a, x, i + 2, lane);  // in flight behind the V rows
+                }
+                ok = ok && emit_v(now, item_units(x, i));
+                now = next;
+                next = after;
+            }
+        }
+    } else if (warp == 8 && rank == 1) {
+        // ---------------------------------------------------------------- the odd CTA's rows have landed
+        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
+            if (x.T == 0) continue;
+            ok = lat_wait(sb + LP_QFULL, n & 1, dead);
+            if (ok && lane == 0) mbar_arrive_rank(sb + LP_QFULL, 0);
+            ++n;
+            const int end = sidx + 8 * x.T - 4 + ((item_units(x, x.T - 1) + 1) >> 1);
+            for (; ok && sidx < end; ++sidx) {
+                const uint32_t bar = sb + LP_FULL + 8 * (sidx & (LP_SLOTS - 1));
+                ok = lat_wait(bar, (sidx / LP_SLOTS) & 1, dead);
+                if (ok && lane == 0) mbar_arrive_rank(bar, 0);
+            }
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- the products
+        const bool one = elect_one();
+        const uint64_t dk = sdesc_sw128(sb, 16, 1024), dv = sdesc_sw128(sb, 4096, 1024);
+        const uint32_t klo = (uint32_t)dk, khi = (uint32_t)(dk >> 32), vlo = (uint32_t)dv, vhi = (uint32_t)(dv >> 32);
+        auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
+            return ((uint64_t)hi << 32) | (uint64_t)(lo + (off >> 4));
+        };
+        auto do_s = [&](int gt, int nu) -> bool {  // S of tile gt
+            const uint32_t id = idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17), ids = id | ((uint32_t)(4 * ((nu + 1) >> 1)) << 17);
+            const uint32_t d = tmem + 256 + (uint32_t)(gt & 1) * 64;
+#pragma unroll 1
+            for (int kk = 0; kk < 4; ++kk, ++sidx) {
+                const int sl = sidx & (LP_SLOTS - 1);
+                if (!lat_wait(sb + LP_FULL + 8 * sl, (sidx / LP_SLOTS) & 1, dead)) return false;
+                tc_fence_after();
+                if (one) {
+                    const uint32_t ao = (uint32_t)(2 * kk) * LP_QSLAB, bo = LP_SM_RING + (uint32_t)sl * LP_SLOT;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f16_pair(d, desc(klo, khi, ao + s * LP_QSLAB + k * 32), desc(klo, khi, bo + s * 8192 + k * 32),
+                                            ids, (kk | s | k) ? 1u : 0u);
+                    tc_commit_pair(sb + LP_EMPTY + 8 * sl);
+                }
+                __syncwarp();
+            }
+            if (one) tc_commit_pair(sb + LP_SFULL + 8 * (gt & 1));
+            __syncwarp();
+            return true;
+        };
+        auto do_pv = [&](int gt, int nu, bool first) -> bool {
+            if (!lat_wait(sb + LP_PREADY, gt & 1, dead)) return false;
+            constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
+#pragma unroll 1
+            for (int v = 0; v < (nu + 1) >> 1; ++v, ++sidx) {
+                const int sl = sidx & (LP_SLOTS - 1);
+                if (!lat_wait(sb + LP_FULL + 8 * sl, (sidx / LP_SLOTS) & 1, dead)) return false;
+                tc_fence_after();
+                if (one) {
+                    const uint32_t bo = LP_SM_RING + (uint32_t)sl * LP_SLOT;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int u = 2 * v + i;
+                        if (u < nu) {
+                            const uint32_t ao = LP_SM_P + (uint32_t)(u >> 2) * LP_QSLAB + (uint32_t)(u & 3) * 32;
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, ao), desc(vlo, vhi, bo + c * 8192 + i * 2048), idv,
+                                                first && u == 0 ? 0u : 1u);
+                        }
+                    }
+                    tc_commit_pair(sb + LP_EMPTY + 8 * sl);
+                }
+                __syncwarp();
+            }
+            if (one) tc_commit_pair(sb + LP_PVDONE);
+            __syncwarp();
+            return true;
+        };
+        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
+            if (x.T == 0) continue;
+            ok = lat_wait(sb + LP_QFULL, n & 1, dead) && do_s(g, item_units(x, 0));
+            ++n;
+            for (int i = 0; ok && i < x.T; ++i, ++g) {
+                if (i + 1 < x.T) ok = do_s(g + 1, item_units(x, i + 1));
+                else if (one) tc_commit_pair(sb + LP_QEMPTY);
+                __syncwarp();
+                ok = ok && do_pv(g, item_units(x, i), i == 0);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- Q
+        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
+            if (x.T == 0) continue;
+            if (n > 0) ok = lat_wait(sb + LP_QEMPTY, (n - 1) & 1, dead);
+            ++n;
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(sb + LP_QFULL, 8 * LP_QSLAB);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    tma_load_2d(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, sb + LP_QFULL);
+            }
+            __syncwarp();
+        }
+    }
+    __syncwarp();
+    pdl_launch_dependents();
+    if (!ok) {  // a wait ran out: leave the copies and products in flight some time to end
+        if (lane == 0) raise_status(a.status, CSA_ERR_TIMEOUT);
+        for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 0) tmem_dealloc_pair(tmem, 512);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
+    lat_box_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, LatArgs a) {
+    lat_pair<true>(qmap, kmap, a);
+}
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
+    lat_gather_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, LatArgs a) {
+    lat_pair<false>(qmap, kmap, a);
+}
+
+// Log-sum-exp merge of a row's partial results, in their order: one CTA per row, thread t columns
+// 4t .. 4t+3.  Window: rows that no sequence covers are left alone.
+__global__ void __launch_bounds__(128) lat_merge_kernel(LatArgs a) {
+    pdl_wait();
+    const int row = blockIdx.x, t = threadIdx.x;
+    if (!a.n_rows) {
+        const int64_t q = row / a.H;
+        int l = 0, r = a.B;  // the last sequence that starts at or before token q
         while (r - l > 1) {
             const int m = (l + r) / 2;
-            if (__ldg(a.q_offsets + m) <= t) l = m;
+            if (__ldg(a.q_offsets + m) <= q) l = m;
             else r = m;
         }
-        b = l;
-        const int64_t q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1);
-        if (t < q0 || t >= q1) return;
-        if (q1 > a.total_q || q1 - q0 > a.max_q) {
-            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-            return;
-        }
-        const int64_t pos = __ldg(a.n_tokens + b) - (q1 - t);
-        hi = pos + 1 > 0 ? pos + 1 : 0;
-        lo = hi > a.window ? hi - a.window : 0;
-        sink_hi = a.n_sink < lo ? a.n_sink : lo;
-    } else {
-        b = (int)(row / a.H);
-        hi = __ldg(a.n_rows + b);
-        if (hi > a.max_rows || hi < 0) {
-            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-            hi = hi < 0 ? 0 : a.max_rows;
-        }
+        const int64_t q0 = __ldg(a.q_offsets + l), q1 = __ldg(a.q_offsets + l + 1);
+        if (q < q0 || q >= q1 || !seq_valid(a, q0, q1, __ldg(a.n_tokens + l))) return;
     }
-    float q[16], o[16];
-    const uint4* qp = reinterpret_cast<const uint4*>(a.q + row * D + lane * 16);
-    const uint4 q0 = qp[0], q1 = qp[1];
-    const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        q[2 * e] = bf16lo(qw[e]) * a.scale;
-        q[2 * e + 1] = bf16hi(qw[e]) * a.scale;
-        o[2 * e] = o[2 * e + 1] = 0.f;
+    const float* lp = a.part_lse + row;
+    const float* op = a.part_o + (int64_t)row * D + t * 4;
+    const int64_t step = (int64_t)a.rows;
+    float M = -INFINITY;
+    bool nan = false;
+    for (int s = 0; s < a.parts; ++s) {
+        const float v = __ldcg(lp + s * step);
+        M = fmaxf(M, v);
+        nan = nan || v != v;
     }
-    float m = -INFINITY, l = 0.f;
-    auto attend = [&](int64_t j) {
-        const uint8_t* p = lat_row(a, j < a.n_shared ? 0 : b, j);
-        if (!p) return;
-        const uint4* kp = reinterpret_cast<const uint4*>(p) + lane * 2;
-        const uint4 k0 = __ldg(kp), k1 = __ldg(kp + 1);
-        const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x = fmaf(q[2 * e + 1], bf16hi(kw[e]), fmaf(q[2 * e], bf16lo(kw[e]), x));
-        for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-        const float mn = fmaxf(m, x);
-        const float alpha = m == -INFINITY ? 0.f : expf(m - mn), w = expf(x - mn);
-        m = mn;
-        l = l * alpha + w;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            o[2 * e] = fmaf(w, bf16lo(kw[e]), o[2 * e] * alpha);
-            o[2 * e + 1] = fmaf(w, bf16hi(kw[e]), o[2 * e + 1] * alpha);
-        }
-    };
-    for (int64_t j = 0; j < sink_hi; ++j) attend(j);
-    for (int64_t j = lo; j < hi; ++j) attend(j);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    uint4* op = reinterpret_cast<uint4*>(a.out + row * D + lane * 16);
-    op[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    op[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+    float L = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+    for (int s = 0; s < a.parts; ++s) {
+        const float v = __ldcg(lp + s * step);
+        if (v == -INFINITY) continue;
+        const float w = lat_ex2((v - M) * LP_LOG2E);
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(op + s * step * D));
+        L += w;
+        o0 = fmaf(w, f.x, o0);
+        o1 = fmaf(w, f.y, o1);
+        o2 = fmaf(w, f.z, o2);
+        o3 = fmaf(w, f.w, o3);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint2 w;
+    w.x = pack_bf16x2(o0 * inv, o1 * inv);
+    w.y = pack_bf16x2(o2 * inv, o3 * inv);
+    *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + t * 4) = w;
+    if (t == 0 && a.lse) a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f ? -INFINITY : M + log2f(L) * LP_LN2);
 }
 
 // What both calls ask of the cache: a page table, pages of whole 1,024-byte rows, row ids below 2^31.
@@ -151,9 +863,95 @@ static csa_status check_window(int32_t B, int32_t H, int64_t total_q, int64_t ma
     return CSA_OK;
 }
 
-static cudaError_t launch_rows(const LatArgs& a, int64_t rows, cudaStream_t s) {
-    lat_rows_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, rows);
-    return cudaGetLastError();
+// Splits of the shared rows: the number that ends the row tiles soonest on LP_PAIRS pairs, where an
+// item costs its tiles of 128 keys and about three more (its Q, its first and last product, its output).
+static int plan_splits(int row_tiles, int tiles) {
+    int best = 1;
+    double cost = 1e30;
+    for (int s = 1; s <= tiles && s <= LP_PAIRS; ++s) {
+        const int waves = (row_tiles * s + LP_PAIRS - 1) / LP_PAIRS;
+        const double c = (double)waves * ((tiles + s - 1) / s + 3) + 0.05 * s;
+        if (c < cost) cost = c, best = s;
+    }
+    return best;
+}
+
+static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArgs* a) {
+    a->rows = B * H;
+    a->RT = (a->rows + 127) / 128;
+    const int tiles = (int)((n_shared + 127) / 128);
+    a->SP = tiles > 0 ? plan_splits(a->RT, tiles) : 0;
+    const int own = max_rows > n_shared ? (int)((max_rows + 15) / 16 - n_shared / 16 + 7) / 8 : 0;
+    a->OS = 0;
+    if (own > 0) {  // a request's own rows in pieces no longer than the shared ones, or than fill the device
+        const int per = a->SP > 0 ? std::max(4, (tiles + a->SP - 1) / a->SP) : std::max(2, (own * B + LP_PAIRS - 1) / LP_PAIRS);
+        a->OS = std::min((own + per - 1) / per, std::max(1, 4 * LP_PAIRS / B));
+    }
+    if (a->SP + a->OS == 0) a->OS = 1;  // no rows at all: every request is empty
+    a->parts = a->SP + a->OS;
+}
+
+static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, LatArgs* a, int64_t* items) {
+    a->rows = (int)(total_q * H);
+    const int64_t per_seq = (max_q * H + 127) / 128;
+    const int64_t tiles_q = std::min((int64_t)B * per_seq, (total_q * H + 127) / 128 + B);
+    // key tiles of a row tile: its tokens' windows and the sinks
+    const int64_t keys = (int64_t)window + n_sink + 127 / H + 32;
+    const int64_t tiles = (keys + 127) / 128;
+    int64_t s = 1;
+    if (tiles >= 4 && tiles_q <= LP_PAIRS / 2) s = std::min(tiles / 2, LP_PAIRS / std::max<int64_t>(tiles_q, 1));
+    a->WS = (int)std::max<int64_t>(1, s);
+    a->parts = a->WS;
+    if (items) *items = tiles_q * a->WS;
+}
+
+static size_t parts_bytes(const LatArgs& a) {
+    if (a.parts <= 1) return 0;
+    return align_up((size_t)a.parts * a.rows * D * sizeof(float), 256) + align_up((size_t)a.parts * a.rows * sizeof(float), 256);
+}
+
+static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, int64_t items, void* ws, cudaStream_t s) {
+    if (a.parts > 1) {
+        a.part_o = static_cast<float*>(ws);
+        a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                              align_up((size_t)a.parts * a.rows * D * sizeof(float), 256));
+    }
+    const int sms = device_sm_count();
+    if (sms < 2) return cudaErrorInvalidDevice;
+    CUtensorMap qm, km;
+    const uint64_t qd[2] = {(uint64_t)D, (uint64_t)a.rows}, qs[1] = {ROW_BYTES};
+    const uint32_t qb[2] = {64, 64};
+    if (!make_bf16_map(&qm, q, 2, qd, qs, qb)) return cudaErrorInvalidValue;
+    const bool box = kv.rows_per_page % 16 == 0;
+    if (box) {
+        const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
+        const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
+        const uint32_t b[3] = {64, 16, 1};
+        if (!make_bf16_map(&km, kv.base, 3, d, st, b)) return cudaErrorInvalidValue;
+    } else {
+        // rows behind the last page's own are not there: the extent ends with them
+        const uint64_t d[2] = {(uint64_t)D, (uint64_t)((kv.n_pages - 1) * (kv.page_stride_bytes / ROW_BYTES) + kv.rows_per_page)};
+        const uint64_t st[1] = {ROW_BYTES};
+        const uint32_t b[2] = {64, 1};
+        if (!make_bf16_map(&km, kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
+    }
+    void (*kernel)(CUtensorMap, CUtensorMap, LatArgs) = box ? lat_box_kernel : lat_gather_kernel;
+    cudaError_t e = set_func_attr_once((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LP_SMEM);
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, sms / 2));
+    kernel<<<2 * pairs, LP_T, LP_SMEM, s>>>(qm, km, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.parts == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)a.rows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, lat_merge_kernel, a);
 }
 
 }  // namespace csa
@@ -163,7 +961,10 @@ using namespace csa;
 extern "C" {
 
 size_t csa_prefix_attn_workspace_size(int32_t B, int32_t H, int64_t n_shared, int64_t max_rows) {
-    return check_prefix(B, H, n_shared, max_rows) ? 0 : 256;
+    if (check_prefix(B, H, n_shared, max_rows)) return 0;
+    LatArgs a = {};
+    plan_prefix(B, H, n_shared, max_rows, &a);
+    return parts_bytes(a);
 }
 
 csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa_paged kv, int64_t page_table_stride,
@@ -175,29 +976,32 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
         return CSA_ERR_INVALID_ARG;
     if ((rc = check_cache(kv, page_table_stride))) return rc;
     if (page_table_stride < (max_rows + kv.rows_per_page - 1) / kv.rows_per_page) return CSA_ERR_INVALID_ARG;
-    if (!workspace || !al16(workspace) || ws_bytes < csa_prefix_attn_workspace_size(B, H, n_shared, max_rows))
-        return CSA_ERR_WORKSPACE;
     LatArgs a = {};
+    plan_prefix(B, H, n_shared, max_rows, &a);
+    const size_t need = parts_bytes(a);
+    if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
-    a.q = static_cast<const uint16_t*>(q);
     a.H = H;
-    a.scale = scale;
+    a.sl2 = scale * LP_LOG2E;
     a.kv = cache_of(kv, page_table_stride);
     a.table_pages = page_table_stride;
-    a.n_rows = n_rows;
-    a.n_shared = n_shared;
-    a.max_rows = max_rows;
     a.B = B;
+    a.n_rows = n_rows;
+    a.n_shared = (int)n_shared;
+    a.max_rows = (int)max_rows;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    return from_cuda(launch_rows(a, (int64_t)B * H, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_pair(a, q, kv, (int64_t)a.RT * a.SP + (int64_t)B * a.OS, workspace,
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
                                       int32_t n_sink) {
-    (void)B, (void)H, (void)total_q, (void)max_q, (void)window, (void)n_sink;
-    return 0;
+    if (check_window(B, H, total_q, max_q, window, n_sink)) return 0;
+    LatArgs a = {};
+    plan_window(B, H, total_q, max_q, window, n_sink, &a, nullptr);
+    return parts_bytes(a);
 }
 
 csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_raw, int64_t page_table_stride,
@@ -210,27 +1014,28 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
         !al8(n_tokens))
         return CSA_ERR_INVALID_ARG;
     if ((rc = check_cache(kv_raw, page_table_stride))) return rc;
-    const size_t need = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink);
+    LatArgs a = {};
+    int64_t items;
+    plan_window(B, H, total_q, max_q, window, n_sink, &a, &items);
+    const size_t need = parts_bytes(a);
     if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
     if (total_q == 0) return CSA_OK;
-    LatArgs a = {};
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
-    a.q = static_cast<const uint16_t*>(q);
     a.H = H;
-    a.scale = scale;
+    a.sl2 = scale * LP_LOG2E;
     a.kv = cache_of(kv_raw, page_table_stride);
     a.table_pages = page_table_stride;
+    a.B = B;
     a.q_offsets = q_offsets;
     a.n_tokens = n_tokens;
     a.total_q = total_q;
     a.max_q = max_q;
     a.window = window;
     a.n_sink = n_sink;
-    a.B = B;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    return from_cuda(launch_rows(a, total_q * H, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_pair(a, q, kv_raw, items, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -535,6 +535,23 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 // 3-D view of the index-key pool: [pages][rows per page][128 dims], box = 16 rows x
 // (64 bf16 | 128 fp8) = 16 x 128 B, 128-byte swizzle.
+bool make_bf16_map(void* map, const void* base, int nd, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box) {
+    auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], es[5];
+    for (int i = 0; i < nd; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < nd) st[i] = strides[i];
+    }
+    return enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)nd, const_cast<void*>(base),
+               d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_kidx_map(void* map, const HPaged& p, bool fp8, int64_t rows_per_page, int64_t n_pages) {
     CUtensorMap* m = static_cast<CUtensorMap*>(map);
     auto enc = encoder();
