@@ -15,16 +15,21 @@
 // dims would have to compute S twice).  Measured on GB300 with nothing but these products in flight: 2,056 cycles
 // a tile against 2,048 at the nominal rate.
 //
-// Roles (10 warps a CTA): warps 0-3 own the TMEM lanes (softmax, output); warps 4-7 load key rows; warp 8
-// issues the products (even CTA) or passes on that the odd CTA's rows have landed; warp 9 loads Q.
+// Roles (16 warps a CTA): warps 0-7 own the TMEM lanes, two to a lane quarter (softmax, output); warp 8 of
+// the even CTA issues the products; warp 9 works the items out for the others, looks up the tiles' pages, up to
+// four tiles ahead, and loads Q; warps 10-15 load key rows.  Both CTAs' copies report to the even CTA's
+// barriers.  The loops are kept short and, for the products, free of branches: with the items worked out in
+// every role and a wait before each slot's products, the kernel was 175 KB of code, every step of a role
+// cost some 200 cycles (the waits themselves were over at once), and a tile took 4,400 cycles.
 // Key rows come through a ring of 8 slots of 16 KB in the order in which the products take them: S of a tile
-// in four slots (128 dims each of the CTA's own keys), P V in up to four (32 keys each, the CTA's
-// half of the dims).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
-// Key rows are copied by TMA in the products' swizzle: boxes of 16 rows where 16 rows always share a page
-// (rows_per_page a multiple of 16), four-row gathers otherwise.  The list of key rows is made of
-// 16-row units; rows of a unit that no query sees are masked.
+// in four slots (128 dims each of the CTA's own keys), P V in four (32 keys each, the CTA's half of the
+// dims; empty ones in a short tile).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
+// Key rows are copied by TMA in the products' swizzle: where 16 rows always share a page (rows_per_page a
+// multiple of 16) in boxes of 64, 32 or 16 rows, as many as lie one behind the other in their page (issuing
+// a copy costs a warp some 60 cycles whatever its size); otherwise in four-row gathers.  The list of
+// key rows is made of 16-row units; rows of a unit that no query sees are masked.
 //
-// Softmax: a thread holds one row's logits of half of a tile; the row's two threads exchange their
+// Softmax: a thread holds one row's logits of a quarter of a tile; the row's four threads exchange their
 // maxima.  The running maximum moves only when a tile exceeds it by 2^8 (O is then rescaled in TMEM);
 // P is rounded to bf16 for the product, its sum is taken in fp32 before the rounding.
 //
@@ -41,7 +46,9 @@
 
 namespace csa {
 
-constexpr int LP_T = 320;
+constexpr int LP_T = 512;
+constexpr int LP_SOFT = 8;                                // softmax warps
+constexpr int LP_PROD = 6;                                // loading warps
 constexpr int LP_SLOTS = 8;
 constexpr int LP_PAIRS = 76;                              // pairs of SMs: sizes the splits (and so the workspace)
 constexpr uint32_t LP_SLOT = 16384;
@@ -49,13 +56,17 @@ constexpr uint32_t LP_QSLAB = 64 * 128;                   // 64 dims of the CTA'
 constexpr uint32_t LP_SM_RING = 8 * LP_QSLAB;             // behind Q
 constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 64 keys x 64 rows; output staging
 constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
-constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_QFULL = LP_EMPTY + 64, LP_QEMPTY = LP_QFULL + 8;
-constexpr uint32_t LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16, LP_PVDONE = LP_PREADY + 8;
-constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 256, LP_SM_DEAD = LP_SM_TMEM + 8;
-constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits
-constexpr uint32_t LP_SM_MAX = LP_SM_VALID + 128;         // [2][128] row maxima of the threads
-constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 1024;          // [128] row sums of the threads
-constexpr uint32_t LP_SMEM = LP_SM_SUM + 512 + 1024;      // + alignment slack
+constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
+constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
+constexpr uint32_t LP_PVDONE = LP_PREADY + 8, LP_VLAND = LP_PVDONE + 8, LP_ITEM = LP_VLAND + 8, LP_TAKEN = LP_ITEM + 32;
+static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
+constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
+constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits of the rows that are there
+constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row ids, or [8] units {page, row}, runs
+constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
+constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of the threads
+constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
+constexpr uint32_t LP_SMEM = LP_SM_ITEM + 4 * 128 + 1024; // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr float LP_LOG2E = 1.4426950408889634f;
 constexpr float LP_LN2 = 0.6931471805599453f;
@@ -66,6 +77,7 @@ struct LatArgs {
     float sl2;                 // scale * log2(e)
     DPaged kv;
     int64_t table_pages;       // entries of a request's page table
+    int rpp_shift;             // log2 of the rows per page, -1 where they are no power of two
     int B;
     // prefix: request b = row / H sees rows [0, n_rows[b]); rows below n_shared through table row 0
     const int64_t* n_rows;     // nullptr: window
@@ -87,7 +99,7 @@ struct LatArgs {
 };
 
 // An item: query rows [row0, row0 + nrows) against tiles [t0, t0 + T) of a list of 16-row units: units
-// [0, uA) of the request (sinks), then units uB, uB + 1, ..., nU in all.
+// [0, uA) of the request (sinks), then units uB, uB + 1, ..., nU in all.  T < 0: behind the last item.
 struct LatItem {
     int T, t0, nU, uA, uB;
     int row0, nrows;
@@ -96,9 +108,10 @@ struct LatItem {
     int a1, lo, hi;            // rows that a query of the item may see: [0, a1) and [lo, hi)
     int full_lo, full_hi;      // rows that every query of the item sees
     int rr0;                   // window: first query row within its sequence
+    int shared;                // prefix: the shared rows (else request trow's own)
     int64_t pos0;              // window: position of the sequence's first new token
-    bool shared;               // prefix: the shared rows (else request trow's own)
 };
+static_assert(sizeof(LatItem) <= 128, "an item's place in shared memory");
 
 // Sequences by row tiles, 32 at a time, one per lane; item indices ascend.
 struct SeqCursor {
@@ -203,7 +216,7 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.row0 = (int)q0 * a.H + x.rr0;
         x.trow = cur.c0 + src;
         x.part = split;
-        x.shared = false;
+        x.shared = 0;
         x.pos0 = (nt > 0 ? nt : 0) - ql;
         const int64_t p0 = x.pos0 + x.rr0 / a.H, p1 = x.pos0 + (x.rr0 + x.nrows - 1) / a.H;
         x.hi = p1 >= 0 ? (int)p1 + 1 : 0;
@@ -228,9 +241,12 @@ __device__ __forceinline__ int unit_row(const LatItem& x, int u) { return (u < x
 // Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
 // stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
 // further wait returning at once.
+// Lane i waits on the barrier at its own address: a warp can wait on several at once.
 __device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
         if (*dead) return false;
         if (i >= 32) __nanosleep(64);
     }
@@ -244,47 +260,26 @@ __device__ __forceinline__ float lat_ex2(float x) {  // ex2.approx.ftz: relative
     return y;
 }
 
-// The lookups of a tile, one lane's share.  Boxes: lane u's unit (page id, row within the page);
-// gathers: the page ids of rows 4 lane .. 4 lane + 3.  Loads only: nothing waits for them here.
-struct TileRef {
-    int pp[4];
-    int slot[4];
-    int need;  // bits of the rows (unit) that are looked up and inside the table
+// Row id of logical row j of the item's request, -1 where there is no page (or none inside the pool).
+__device__ __forceinline__ int lat_page(const LatArgs& a, const int32_t* pt, int j, int& slot) {
+    const uint32_t lp = a.rpp_shift >= 0 ? (uint32_t)j >> a.rpp_shift : (uint32_t)j / (uint32_t)a.kv.rpp;
+    slot = j - (int)lp * a.kv.rpp;
+    int pp = -1;
+    if ((int64_t)lp < a.table_pages) pp = __ldg(pt + lp);
+    if (pp < 0 || pp >= a.kv.n_pages) {
+        raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+        return -1;
+    }
+    return pp;
+}
+
+// The cache's tensor maps: [0] boxes of 16 rows x 64 dims (or of one row, for gathers), [1] of 32, [2] of 64.
+struct KeyMaps {
+    CUtensorMap m[3];
 };
 
 template <bool BOX>
-__device__ __forceinline__ TileRef tile_issue(const LatArgs& a, const LatItem& x, int i, int lane) {
-    TileRef r;
-    r.need = 0;
-    const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
-    const int u0 = (x.t0 + i) * 8;
-#pragma unroll
-    for (int e = 0; e < (BOX ? 1 : 4); ++e) {
-        r.pp[e] = r.slot[e] = 0;
-        const int k = lane * 4 + e;
-        const int u = u0 + (BOX ? lane : k >> 4);
-        if (BOX ? lane >= 8 : false) continue;
-        if (u >= x.nU) continue;
-        const int j = unit_row(x, u) + (BOX ? 0 : k & 15);
-        if (BOX) {
-            if (j >= x.hi) continue;                     // a unit behind the last row that is seen
-        } else if (!(j < x.a1 || (j >= x.lo && j < x.hi))) {
-            continue;                                    // a row of the unit that no query sees
-        }
-        const uint32_t lp = (uint32_t)j / (uint32_t)a.kv.rpp;
-        r.slot[e] = j - (int)lp * a.kv.rpp;
-        if ((int64_t)lp >= a.table_pages) {
-            raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-            continue;
-        }
-        r.need |= 1 << e;
-        r.pp[e] = __ldg(pt + lp);
-    }
-    return r;
-}
-
-template <bool BOX>
-__device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensorMap& kmap, const LatArgs& a) {
+__device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps& km, const LatArgs& a) {
     extern __shared__ uint8_t lp_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lp_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -299,15 +294,22 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
     }
     if (tid == 32) {
         for (int i = 0; i < LP_SLOTS; ++i) {
-            mbar_init(sb + LP_FULL + 8 * i, rank == 0 ? 2 : 1);  // this CTA's rows (and the other's)
+            mbar_init(sb + LP_FULL + 8 * i, 1);  // even CTA: both CTAs' rows
             mbar_init(sb + LP_EMPTY + 8 * i, 1);
+            mbar_init(sb + LP_LOOK + 8 * i, 1);
+            mbar_init(sb + LP_USED + 8 * i, LP_PROD);
         }
-        mbar_init(sb + LP_QFULL, rank == 0 ? 2 : 1);
+        mbar_init(sb + LP_QFULL, 1);
         mbar_init(sb + LP_QEMPTY, 1);
         mbar_init(sb + LP_SFULL, 1);
         mbar_init(sb + LP_SFULL + 8, 1);
-        mbar_init(sb + LP_PREADY, 8);  // the softmax warps of both CTAs
+        mbar_init(sb + LP_PREADY, 2 * LP_SOFT);  // the softmax warps of both CTAs
         mbar_init(sb + LP_PVDONE, 1);
+        mbar_init(sb + LP_VLAND, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(sb + LP_ITEM + 8 * i, 1);
+            mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_PROD + (rank == 0 ? 1 : 0));
+        }
         *dead = 0;
         fence_mbar_init();
     }
@@ -316,18 +318,27 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LP_SM_TMEM);
-    SeqCursor cur;
     LatItem x;
-    int sidx = 0, g = 0, n = 0;  // ring slots, tiles and items so far
+    int sidx = 0, g = 0, n = 0, q = 0;  // ring slots, tiles, items with tiles and items so far
     bool ok = true;
+    // The next item as warp 9 left it; false behind the last one, and when a wait has run out.
+    auto next_item = [&]() -> bool {
+        const bool in = lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
+        x = *reinterpret_cast<const LatItem*>(sm + LP_SM_ITEM + (q & 3) * 128);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
+        ++q;
+        ok = ok && in;
+        return in && x.T >= 0;
+    };
 
-    if (warp < 4) {
+    if (warp < LP_SOFT) {
         // ---------------------------------------------------------------- softmax and output
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const int r = tid & 63, half = tid >> 6;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const int r = tid & 63, half = (warp >> 1) & 1, ch = warp >> 2;
         float* mx = reinterpret_cast<float*>(sm + LP_SM_MAX);
         float* ls = reinterpret_cast<float*>(sm + LP_SM_SUM);
-        for (int it = pair; lat_item(a, cur, it, lane, warp == 0 && rank == 0, x); it += pairs) {
+        while (next_item()) {
             const int row = x.row0 + (int)rank * 64 + r;  // this thread's query row
             const bool mine = (int)rank * 64 + r < x.nrows;
             // rows that this query sees: [vlo, vhi) and [0, vs)
@@ -349,42 +360,43 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
             float m_run = -INFINITY, l_run = 0.f;
             for (int i = 0; i < x.T; ++i, ++g) {
                 const int nu = item_units(x, i), mu = (nu + 1) >> 1;  // units in all, and per half
-                const int u0 = (x.t0 + i) * 8;
+                const int c0 = ch ? (mu + 1) >> 1 : 0, nc = ch ? mu - c0 : (mu + 1) >> 1;  // this thread's
+                const int ub = half * mu + c0, u0 = (x.t0 + i) * 8;
+                ok = lat_wait(sb + LP_LOOK + 8 * (g & 7), (g >> 3) & 1, dead) && ok;
+                const uint4 vw = ld_shared_v4(sb + LP_SM_VALID + (g & 7) * 16);
+                // every row of the tile seen by every query of the item, and every page there
+                const bool plain = nu == 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && u0 >= x.uA &&
+                                   unit_row(x, u0) >= x.full_lo && unit_row(x, u0 + 7) + 16 <= x.full_hi;
                 ok = lat_wait(sb + LP_SFULL + 8 * (g & 1), (g >> 1) & 1, dead) && ok;
                 tc_fence_after();
-                const uint32_t* vw = reinterpret_cast<const uint32_t*>(sm + LP_SM_VALID) + (g & 7) * 4;
-                const uint32_t v0 = vw[0], v1 = vw[1], v2 = vw[2], v3 = vw[3];
-                // every row of the tile seen by every query of the item, and every page there
-                const bool plain = nu == 8 && (v0 & v1 & v2 & v3) == 0xffffffffu && u0 >= x.uA &&
-                                   unit_row(x, u0) >= x.full_lo && unit_row(x, u0 + 7) + 16 <= x.full_hi;
-                uint32_t sr[64];
-                const uint32_t ts = tmem + 256 + (uint32_t)(g & 1) * 64 + lane_off;
+                uint32_t sr[32];
+                const uint32_t ts = tmem + 256 + (uint32_t)((g & 1) * 64 + 16 * c0) + lane_off;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < mu) tc_ld16(ts + 16 * c, sr + 16 * c);
+                for (int c = 0; c < 2; ++c)
+                    if (c < nc) tc_ld16(ts + 16 * c, sr + 16 * c);
                 tc_wait_ld();
                 float mt = -INFINITY;
                 bool bad = false;
                 float* xs = reinterpret_cast<float*>(sr);
                 if (plain) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         xs[j] = __uint_as_float(sr[j]) * a.sl2;
                         mt = fmaxf(mt, xs[j]);
                     }
                 } else {
                     float z = 0.f;  // NaN where a logit of the tile is not finite
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c < mu) {
-                            const int u = half * mu + c;
+                    for (int c = 0; c < 2; ++c) {
+                        if (c < nc) {
+                            const int u = ub + c;
                             uint32_t bits = 0;
                             if (u < nu) {
                                 const int jb = unit_row(x, u0 + u);
                                 const int e0 = min(max(vlo - jb, 0), 16), e1 = min(max(vhi - jb, 0), 16);
                                 const int e2 = min(max(vs - jb, 0), 16);
                                 bits = (((1u << e1) - 1u) & ~((1u << e0) - 1u)) | ((1u << e2) - 1u);
-                                const uint32_t vv = u < 4 ? (u < 2 ? v0 : v1) : (u < 6 ? v2 : v3);
+                                const uint32_t vv = u < 4 ? (u < 2 ? vw.x : vw.y) : (u < 6 ? vw.z : vw.w);
                                 bits &= vv >> ((u & 1) * 16);
                             }
 #pragma unroll
@@ -398,11 +410,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                     }
                     bad = !(z == 0.f);
                 }
-                // the row's other half, and whether any logit of the tile is not finite
-                float* mb = mx + (g & 1) * 128;
+                // the row's other quarters, and whether any logit of the tile is not finite
+                float* mb = mx + (g & 1) * 256;
                 mb[tid] = mt;
-                const bool any_bad = named_bar_any(1, 128, bad);
-                mt = fmaxf(mt, mb[tid ^ 64]);
+                const bool any_bad = named_bar_any(1, 32 * LP_SOFT, bad);
+                mt = fmaxf(fmaxf(mt, mb[tid ^ 64]), fmaxf(mb[tid ^ 128], mb[tid ^ 192]));
                 float alpha = 1.f;
                 if (mt > -INFINITY) {
                     if (m_run == -INFINITY) {
@@ -415,8 +427,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < mu) {
+                for (int c = 0; c < 2; ++c) {
+                    if (c < nc) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float p0 = lat_ex2(xs[16 * c + j] - mref), p1 = lat_ex2(xs[16 * c + j + 1] - mref);
@@ -433,7 +445,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                     tc_fence_after();
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 32) {
+                        for (int c = 128 * ch; c < 128 * ch + 128; c += 32) {
                             uint32_t o[32];
                             tc_ld32(tmem + lane_off + c, o);
                             tc_wait_ld();
@@ -445,9 +457,9 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < mu) {
-                        const int u = half * mu + c;
+                for (int c = 0; c < 2; ++c) {
+                    if (c < nc) {
+                        const int u = ub + c;
                         const uint32_t pb = sb + LP_SM_P + (uint32_t)(u >> 2) * LP_QSLAB + (uint32_t)r * 128;
 #pragma unroll
                         for (int h2 = 0; h2 < 2; ++h2)
@@ -457,12 +469,14 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                     }
                 }
                 if (any_bad) {  // non-finite values of this CTA's V rows -> 0
-                    const int vs0 = sidx + 4 * min(i + 2, x.T) + 4 * i;
+                    ok = lat_wait(sb + LP_VLAND, g & 1, dead) && ok;
+                    const int vs0 = sidx + 4 * min(i + 2, x.T) + 4 * i;  // the tile's first V slot
+#pragma unroll 1
                     for (int s = 0; s < (nu + 1) >> 1; ++s) {
                         const int sl = (vs0 + s) & (LP_SLOTS - 1);
-                        ok = lat_wait(sb + LP_FULL + 8 * sl, ((vs0 + s) / LP_SLOTS) & 1, dead) && ok;
                         const uint32_t bytes = (uint32_t)min(2, nu - 2 * s) * 2048u;  // of each 4,096-byte slab
-                        for (uint32_t c = tid * 16; c < LP_SLOT; c += 128 * 16) {
+#pragma unroll 1
+                        for (uint32_t c = tid * 16; c < LP_SLOT; c += 32 * LP_SOFT * 16) {
                             if ((c & 4095u) >= bytes) continue;
                             const uint32_t ad = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT + c;
                             uint4 v = ld_shared_v4(ad);
@@ -482,55 +496,55 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                 if (lane == 0) mbar_arrive_rank(sb + LP_PREADY, 0);
             }
             if (x.T > 0) {
-                sidx += 8 * x.T - 4 + ((item_units(x, x.T - 1) + 1) >> 1);
+                sidx += 8 * x.T;
                 ls[tid] = l_run;
                 ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
                 tc_fence_after();
-                named_bar_sync(1, 128);
-                l_run += ls[tid ^ 64];
+                named_bar_sync(1, 32 * LP_SOFT);
+                l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
             }
-            // ---- rows [32 (warp & 1), + 32) of the CTA, dims [256 half, + 256): normalised, staged 128 bytes a row
-            //      in the P buffer, written 128 bytes a row
+            // ---- rows [32 (warp & 1), + 32) of the CTA, dims [256 half + 128 ch, + 128): normalised, staged 64 bytes a
+            //      row in the P buffer, written 64 bytes a row
             const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-            const uint32_t stg = sb + LP_SM_P + (uint32_t)warp * 4096;
+            const uint32_t stg = sb + LP_SM_P + (uint32_t)warp * 2048;
             const bool direct = a.parts == 1;
             const int wrow = (int)rank * 64 + (warp & 1) * 32;  // the warp's first row of the item
             if (direct || x.T > 0) {
+                const int64_t gr0 = x.row0 + wrow;
+                uint8_t* dst0 = direct ? reinterpret_cast<uint8_t*>(a.out + gr0 * D + half * 256 + ch * 128)
+                                       : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr0) * D +
+                                                                    half * 256 + ch * 128);
+                const int64_t pitch = direct ? D * 2 : D * 4;
 #pragma unroll 1
                 for (int c = 0; c < (direct ? 4 : 8); ++c) {
-                    uint32_t w[32];
+                    uint32_t w[16];
                     if (x.T == 0) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = 0;
+                        for (int e = 0; e < 16; ++e) w[e] = 0;
                     } else if (direct) {
-                        uint32_t o[64];
-                        tc_ld32(tmem + lane_off + 64 * c, *reinterpret_cast<uint32_t(*)[32]>(o));
-                        tc_ld32(tmem + lane_off + 64 * c + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+                        uint32_t o[32];
+                        tc_ld32(tmem + lane_off + 128 * ch + 32 * c, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                     } else {
-                        tc_ld32(tmem + lane_off + 32 * c, w);
+                        tc_ld16(tmem + lane_off + 128 * ch + 16 * c, w);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        st_shared_v4(stg + lane * 128 + ((uint32_t)(e ^ (lane & 7)) << 4),
+                    for (int e = 0; e < 4; ++e)
+                        st_shared_v4(stg + lane * 64 + ((uint32_t)(e ^ ((lane >> 1) & 3)) << 4),
                                      make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
                     __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = e * 4 + (lane >> 3);
+                    for (int e = 0; e < 4; ++e) {
+                        const int rr = e * 8 + (lane >> 2);
                         if (wrow + rr < x.nrows) {
-                            const uint4 v = ld_shared_v4(stg + rr * 128 + ((uint32_t)((lane & 7) ^ (rr & 7)) << 4));
-                            const int64_t gr = x.row0 + wrow + rr;
-                            uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out + gr * D + half * 256 + c * 64)
-                                                  : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr) * D +
-                                                                               half * 256 + c * 32);
-                            *reinterpret_cast<uint4*>(dst + (lane & 7) * 16) = v;
+                            const uint4 v = ld_shared_v4(stg + rr * 64 + ((uint32_t)((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                            *reinterpret_cast<uint4*>(dst0 + rr * pitch + c * 64 + (lane & 3) * 16) = v;
                         }
                     }
                     __syncwarp();
@@ -543,137 +557,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
                 else if (a.lse) a.lse[row] = e;
             }
         }
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- key rows
-        const int w = warp - 4;
-        auto claim = [&](uint32_t bytes) -> bool {  // slot sidx: free, and its bytes announced
-            const int sl = sidx & (LP_SLOTS - 1);
-            if (sidx >= LP_SLOTS && !lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)) return false;
-            if (lane == 0) {
-                if (bytes) mbar_arrive_expect_tx(sb + LP_FULL + 8 * sl, bytes);
-                else mbar_arrive(sb + LP_FULL + 8 * sl);
-            }
-            __syncwarp();
-            return true;
-        };
-        // ids of the tile's rows, checked: TMA coordinates (page, row) of lane u's unit, or four row ids
-        auto resolve = [&](TileRef& t) -> uint32_t {
-            uint32_t good = 0;
-#pragma unroll
-            for (int e = 0; e < (BOX ? 1 : 4); ++e) {
-                const bool in = (t.need >> e) & 1;
-                const bool there = in && t.pp[e] >= 0 && t.pp[e] < a.kv.n_pages;
-                if (in && !there) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-                if (there) good |= 1u << e;
-                if (BOX) {
-                    if (!there) t.pp[e] = 0;
-                    if (!there) t.slot[e] = 0;
-                } else {
-                    t.pp[e] = there ? t.pp[e] * (int)(a.kv.page_stride / ROW_BYTES) + t.slot[e] : 0;
-                }
-            }
-            return good;
-        };
-        auto emit_k = [&](TileRef& t, uint32_t good, int nu) -> bool {
-            const int mu = (nu + 1) >> 1, ku = min(max(nu - (int)rank * mu, 0), mu);
-            for (int kk = 0; kk < 4; ++kk, ++sidx) {
-                if ((sidx & 3) != w) continue;
-                if (kk == 0) {  // which rows are there, for the softmax
-                    uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + (g & 7) * 4;
-                    if (BOX) {
-                        const uint32_t b = __ballot_sync(0xffffffffu, good);
-                        if (lane < 4)
-                            vw[lane] = ((b >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((b >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
-                    } else {
-                        uint32_t v = good << (4 * (lane & 7));
-                        v |= __shfl_xor_sync(0xffffffffu, v, 1);
-                        v |= __shfl_xor_sync(0xffffffffu, v, 2);
-                        v |= __shfl_xor_sync(0xffffffffu, v, 4);
-                        if ((lane & 7) == 0) vw[lane >> 3] = v;
-                    }
-                    __syncwarp();
-                }
-                const int sl = sidx & (LP_SLOTS - 1);
-                const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = sb + LP_FULL + 8 * sl;
-                if (BOX) {
-                    const int slab = lane >> 2, i = lane & 3;
-                    const int pg = __shfl_sync(0xffffffffu, t.pp[0], ((int)rank * mu + i) & 7);
-                    const int rw = __shfl_sync(0xffffffffu, t.slot[0], ((int)rank * mu + i) & 7);
-                    if (!claim((uint32_t)ku * 4096u)) return false;
-                    if (lane < 8 && i < ku) tma_load_3d(dst + slab * 8192 + i * 2048, &kmap, (2 * kk + slab) * 64, rw, pg, bar);
-                } else {
-                    const int slab = lane >> 4, qd = lane & 15, from = ((int)rank * mu * 4 + qd) & 31;
-                    int4 id;
-                    id.x = __shfl_sync(0xffffffffu, t.pp[0], from);
-                    id.y = __shfl_sync(0xffffffffu, t.pp[1], from);
-                    id.z = __shfl_sync(0xffffffffu, t.pp[2], from);
-                    id.w = __shfl_sync(0xffffffffu, t.pp[3], from);
-                    if (!claim((uint32_t)ku * 4096u)) return false;
-                    if (qd < 4 * ku) tma_gather4(dst + slab * 8192 + qd * 512, &kmap, (2 * kk + slab) * 64, id, bar);
-                }
-            }
-            return true;
-        };
-        auto emit_v = [&](const TileRef& t, int nu) -> bool {
-            for (int v = 0; v < (nu + 1) >> 1; ++v, ++sidx) {
-                if ((sidx & 3) != w) continue;
-                const int vu = min(2, nu - 2 * v);
-                const int sl = sidx & (LP_SLOTS - 1);
-                const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = sb + LP_FULL + 8 * sl;
-                if (BOX) {
-                    const int i = lane & 1, s = (lane >> 1) & 3;
-                    const int pg = __shfl_sync(0xffffffffu, t.pp[0], 2 * v + i);
-                    const int rw = __shfl_sync(0xffffffffu, t.slot[0], 2 * v + i);
-                    if (!claim((uint32_t)vu * 8192u)) return false;
-                    if (lane < 8 && i < vu)
-                        tma_load_3d(dst + s * 4096 + i * 2048, &kmap, (int)rank * 256 + s * 64, rw, pg, bar);
-                } else {
-                    const int s = lane >> 3, qd = lane & 7, from = v * 8 + qd;
-                    int4 id;
-                    id.x = __shfl_sync(0xffffffffu, t.pp[0], from);
-                    id.y = __shfl_sync(0xffffffffu, t.pp[1], from);
-                    id.z = __shfl_sync(0xffffffffu, t.pp[2], from);
-                    id.w = __shfl_sync(0xffffffffu, t.pp[3], from);
-                    if (!claim((uint32_t)vu * 8192u)) return false;
-                    if (qd < 4 * vu) tma_gather4(dst + s * 4096 + qd * 512, &kmap, (int)rank * 256 + s * 64, id, bar);
-                }
-            }
-            return true;
-        };
-        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
-            if (x.T == 0) continue;
-            TileRef now = tile_issue<BOX>(a, x, 0, lane), next = now;
-            if (x.T > 1) next = tile_issue<BOX>(a, x, 1, lane);
-            uint32_t good = resolve(now);
-            ok = emit_k(now, good, item_units(x, 0));
-            for (int i = 0; ok && i < x.T; ++i) {
-                TileRef after = next;
-                ++g;
-                if (i + 1 < x.T) {
-                    good = resolve(next);
-                    ok = emit_k(next, good, item_units(x, i + 1));
-                    if (i + 2 < x.T) after = tile_issue<BOX>(a, x, i + 2, lane);  // in flight behind the V rows
-                }
-                ok = ok && emit_v(now, item_units(x, i));
-                now = next;
-                next = after;
-            }
-        }
-    } else if (warp == 8 && rank == 1) {
-        // ---------------------------------------------------------------- the odd CTA's rows have landed
-        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
-            if (x.T == 0) continue;
-            ok = lat_wait(sb + LP_QFULL, n & 1, dead);
-            if (ok && lane == 0) mbar_arrive_rank(sb + LP_QFULL, 0);
-            ++n;
-            const int end = sidx + 8 * x.T - 4 + ((item_units(x, x.T - 1) + 1) >> 1);
-            for (; ok && sidx < end; ++sidx) {
-                const uint32_t bar = sb + LP_FULL + 8 * (sidx & (LP_SLOTS - 1));
-                ok = lat_wait(bar, (sidx / LP_SLOTS) & 1, dead);
-                if (ok && lane == 0) mbar_arrive_rank(bar, 0);
-            }
-        }
-    } else if (warp == 8) {
+    } else if (warp == LP_SOFT && rank == 0) {
         // ---------------------------------------------------------------- the products
         const bool one = elect_one();
         const uint64_t dk = sdesc_sw128(sb, 16, 1024), dv = sdesc_sw128(sb, 4096, 1024);
@@ -681,89 +565,240 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
         auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
             return ((uint64_t)hi << 32) | (uint64_t)(lo + (off >> 4));
         };
-        auto do_s = [&](int gt, int nu) -> bool {  // S of tile gt
-            const uint32_t id = idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17), ids = id | ((uint32_t)(4 * ((nu + 1) >> 1)) << 17);
-            const uint32_t d = tmem + 256 + (uint32_t)(gt & 1) * 64;
-#pragma unroll 1
-            for (int kk = 0; kk < 4; ++kk, ++sidx) {
-                const int sl = sidx & (LP_SLOTS - 1);
-                if (!lat_wait(sb + LP_FULL + 8 * sl, (sidx / LP_SLOTS) & 1, dead)) return false;
-                tc_fence_after();
-                if (one) {
-                    const uint32_t ao = (uint32_t)(2 * kk) * LP_QSLAB, bo = LP_SM_RING + (uint32_t)sl * LP_SLOT;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_f16_pair(d, desc(klo, khi, ao + s * LP_QSLAB + k * 32), desc(klo, khi, bo + s * 8192 + k * 32),
-                                            ids, (kk | s | k) ? 1u : 0u);
-                    tc_commit_pair(sb + LP_EMPTY + 8 * sl);
-                }
-                __syncwarp();
-            }
-            if (one) tc_commit_pair(sb + LP_SFULL + 8 * (gt & 1));
-            __syncwarp();
-            return true;
-        };
-        auto do_pv = [&](int gt, int nu, bool first) -> bool {
-            if (!lat_wait(sb + LP_PREADY, gt & 1, dead)) return false;
-            constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
-#pragma unroll 1
-            for (int v = 0; v < (nu + 1) >> 1; ++v, ++sidx) {
-                const int sl = sidx & (LP_SLOTS - 1);
-                if (!lat_wait(sb + LP_FULL + 8 * sl, (sidx / LP_SLOTS) & 1, dead)) return false;
-                tc_fence_after();
-                if (one) {
-                    const uint32_t bo = LP_SM_RING + (uint32_t)sl * LP_SLOT;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int u = 2 * v + i;
-                        if (u < nu) {
-                            const uint32_t ao = LP_SM_P + (uint32_t)(u >> 2) * LP_QSLAB + (uint32_t)(u & 3) * 32;
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, ao), desc(vlo, vhi, bo + c * 8192 + i * 2048), idv,
-                                                first && u == 0 ? 0u : 1u);
-                        }
-                    }
-                    tc_commit_pair(sb + LP_EMPTY + 8 * sl);
-                }
-                __syncwarp();
-            }
-            if (one) tc_commit_pair(sb + LP_PVDONE);
-            __syncwarp();
-            return true;
-        };
-        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
+        while (next_item()) {
             if (x.T == 0) continue;
-            ok = lat_wait(sb + LP_QFULL, n & 1, dead) && do_s(g, item_units(x, 0));
+            ok = lat_wait(sb + LP_QFULL, n & 1, dead);
             ++n;
+            const int units = x.nU - x.t0 * 8;
+            // S of tile i, then P V of tile i - 1
+#pragma unroll 1
+            for (int i = 0; ok && i <= x.T; ++i) {
+                if (i < x.T) {
+                    const int mu = (min(8, units - 8 * i) + 1) >> 1;
+                    const uint32_t ids = (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17);
+                    const uint32_t d = tmem + 256 + (uint32_t)((g + i) & 1) * 64, reg = (uint32_t)(sidx >> 2) & 1;
+                    ok = __all_sync(0xffffffffu, lat_wait(sb + LP_FULL + 32 * reg + 8 * (lane & 3), (sidx >> 3) & 1, dead));
+                    tc_fence_after();
+                    if (ok && one) {
+                        const uint32_t bl = klo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc_mma_f16_pair(d, desc(klo, khi, (2 * kk + s) * LP_QSLAB + k * 32),
+                                                    desc(bl, khi, kk * LP_SLOT + s * 8192 + k * 32), ids, (kk | s | k) ? 1u : 0u);
+                            tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * kk);
+                        }
+                        tc_commit_pair(sb + LP_SFULL + 8 * ((g + i) & 1));
+                        if (i + 1 == x.T) tc_commit_pair(sb + LP_QEMPTY);
+                    }
+                    __syncwarp();
+                    sidx += 4;
+                }
+                if (i > 0 && ok) {
+                    const int nu = min(8, units - 8 * (i - 1));
+                    const uint32_t reg = (uint32_t)(sidx >> 2) & 1;
+                    ok = __all_sync(0xffffffffu, lat_wait(sb + LP_FULL + 32 * reg + 8 * (lane & 3), (sidx >> 3) & 1, dead));
+                    if (ok && one) tc_commit_pair(sb + LP_VLAND);
+                    __syncwarp();
+                    ok = ok && lat_wait(sb + LP_PREADY, (g + i - 1) & 1, dead);
+                    tc_fence_after();
+                    if (ok && one) {
+                        const uint32_t bl = vlo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4);
+                        constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            if (u < nu) {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, LP_SM_P + (u >> 2) * LP_QSLAB + (u & 3) * 32),
+                                                    desc(bl, vhi, (u >> 1) * LP_SLOT + c * 8192 + (u & 1) * 2048), idv,
+                                                    i == 1 && u == 0 ? 0u : 1u);
+                            }
+                            if (u & 1) tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * (u >> 1));
+                        }
+                        tc_commit_pair(sb + LP_PVDONE);
+                    }
+                    __syncwarp();
+                    sidx += 4;
+                }
+            }
+            g += x.T;
+        }
+    } else if (warp == LP_SOFT + 1) {
+        // ---------------------------------------------------------------- the tiles' pages, and Q
+        const uint32_t qfull = mapa(sb + LP_QFULL, 0);
+        SeqCursor cur;
+        for (int it = pair; ok; it += pairs, ++q) {
+            const bool there = lat_item(a, cur, it, lane, rank == 0, x);
+            if (!there) x.T = -1;
+            if (q >= 4) ok = lat_wait(sb + LP_TAKEN + 8 * (q & 3), ((q >> 2) - 1) & 1, dead);
+            if (lane == 0) {
+                *reinterpret_cast<LatItem*>(sm + LP_SM_ITEM + (q & 3) * 128) = x;
+                mbar_arrive(sb + LP_ITEM + 8 * (q & 3));
+            }
+            __syncwarp();
+            if (!there) break;
+            const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
             for (int i = 0; ok && i < x.T; ++i, ++g) {
-                if (i + 1 < x.T) ok = do_s(g + 1, item_units(x, i + 1));
-                else if (one) tc_commit_pair(sb + LP_QEMPTY);
+                const int u0 = (x.t0 + i) * 8, slot = g & 7;
+                // the tile's place in the ring: read by the loading warps eight tiles ago, and no further than
+                // four tiles ahead of them
+                if (g >= 4) ok = lat_wait(sb + LP_USED + 8 * ((g - 4) & 7), ((g - 4) >> 3) & 1, dead);
+                uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + slot * 4;
+                int* look = reinterpret_cast<int*>(sm + LP_SM_LOOK) + slot * 128;
+                if (BOX) {
+                    int pg = -1, rw = 0;
+                    const int j = u0 + lane < x.nU && lane < 8 ? unit_row(x, u0 + lane) : x.hi;
+                    if (j < x.hi) pg = lat_page(a, pt, j, rw);  // (a unit behind the last row that is seen: none)
+                    const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0);
+                    if (lane < 4) vw[lane] = ((b >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((b >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
+                    if (pg < 0) pg = rw = 0;
+                    // bit u: unit u + 1 lies right behind unit u
+                    const int pn = __shfl_down_sync(0xffffffffu, pg, 1), rn = __shfl_down_sync(0xffffffffu, rw, 1);
+                    const uint32_t runs = __ballot_sync(0xffffffffu, lane < 7 && pn == pg && rn == rw + 16);
+                    if (lane < 8) {
+                        look[2 * lane] = pg;
+                        look[2 * lane + 1] = rw;
+                    }
+                    if (lane == 0) look[16] = (int)runs;
+                } else {
+                    int id[4];
+                    uint32_t v = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // rows of a unit that no query sees are not looked up
+                        const int k = lane * 4 + e, u = u0 + (k >> 4);
+                        const int j = u < x.nU ? unit_row(x, u) + (k & 15) : -1;
+                        int rw, pg = -1;
+                        if (j >= 0 && (j < x.a1 || (j >= x.lo && j < x.hi))) pg = lat_page(a, pt, j, rw);
+                        id[e] = pg >= 0 ? pg * (int)(a.kv.page_stride / ROW_BYTES) + rw : 0;
+                        if (pg >= 0) v |= 1u << (4 * (lane & 7) + e);
+                    }
+                    *reinterpret_cast<int4*>(look + 4 * lane) = make_int4(id[0], id[1], id[2], id[3]);
+                    v |= __shfl_xor_sync(0xffffffffu, v, 1);
+                    v |= __shfl_xor_sync(0xffffffffu, v, 2);
+                    v |= __shfl_xor_sync(0xffffffffu, v, 4);
+                    if ((lane & 7) == 0) vw[lane >> 3] = v;
+                }
                 __syncwarp();
-                ok = ok && do_pv(g, item_units(x, i), i == 0);
+                if (lane == 0) mbar_arrive(sb + LP_LOOK + 8 * slot);
+                if (i == 0) {  // Q, behind the first tile's lookups
+                    if (n > 0) ok = lat_wait(sb + LP_QEMPTY, (n - 1) & 1, dead) && ok;
+                    ++n;
+                    if (ok && lane == 0) {
+                        if (rank == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            tma_load_2d_pair(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, qfull);
+                    }
+                    __syncwarp();
+                }
             }
         }
-    } else {
-        // ---------------------------------------------------------------- Q
-        for (int it = pair; ok && lat_item(a, cur, it, lane, false, x); it += pairs) {
-            if (x.T == 0) continue;
-            if (n > 0) ok = lat_wait(sb + LP_QEMPTY, (n - 1) & 1, dead);
-            ++n;
-            if (ok && lane == 0) {
-                mbar_arrive_expect_tx(sb + LP_QFULL, 8 * LP_QSLAB);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    tma_load_2d(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, sb + LP_QFULL);
+    } else if (warp >= LP_SOFT + 2) {
+        // ---------------------------------------------------------------- key rows
+        const uint32_t full0 = mapa(sb + LP_FULL, 0);  // the even CTA's barriers
+        int turn = warp - (LP_SOFT + 2);               // slots until this warp's next one
+        auto claim = [&](uint32_t pair_bytes) -> bool {  // slot sidx: free, and both CTAs' bytes announced
+            const int sl = sidx & (LP_SLOTS - 1);
+            if (sidx >= LP_SLOTS && !lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)) return false;
+            if (rank == 0 && lane == 0) {
+                if (pair_bytes) mbar_arrive_expect_tx(sb + LP_FULL + 8 * sl, pair_bytes);
+                else mbar_arrive(sb + LP_FULL + 8 * sl);
             }
             __syncwarp();
+            return true;
+        };
+        while (next_item()) {
+            const int units = x.nU - x.t0 * 8;
+            // K rows of tile i, then V rows of tile i - 1
+#pragma unroll 1
+            for (int i = 0; ok && i <= x.T && x.T > 0; ++i) {
+                if (i < x.T) {
+                    if (turn < 4) {  // (six warps: one slot of the four at most)
+                        const int kk = turn, gt = g + i, nu = min(8, units - 8 * i);
+                        const int mu = (nu + 1) >> 1, ku = min(max(nu - (int)rank * mu, 0), mu), first = (int)rank * mu;
+                        ok = lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead);
+                        const uint32_t look = sb + LP_SM_LOOK + (gt & 7) * 512;
+                        sidx += kk;
+                        const int sl = sidx & (LP_SLOTS - 1);
+                        const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = full0 + 8 * sl;
+                        if (BOX) {
+                            // lane: unit e of the CTA's own (at most 4), slab; the first unit of a run takes all of it
+                            const int slab = lane & 1, e = (lane >> 1) & 3;
+                            const uint2 at = ld_shared_v2(look + 8 * ((first + e) & 7));
+                            uint32_t runs;
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(runs) : "r"(look + 64));
+                            runs = (runs >> first) & ((1u << max(ku - 1, 0)) - 1u);  // bit e: unit e + 1 follows e
+                            // rows of this lane's copy: 0 where another unit's covers it
+                            const int big = runs == 7u ? (e == 0 ? 2 : -1) : ((runs >> (e & 2)) & 1u ? ((e & 1) ? -1 : 1) : 0);
+                            ok = ok && claim((uint32_t)nu * 4096u);
+                            if (ok && lane < 2 * ku && big >= 0)
+                                tma_load_3d_pair(dst + slab * 8192 + e * 2048, &km.m[big], (2 * kk + slab) * 64, (int)at.y,
+                                                 (int)at.x, bar);
+                        } else {
+                            const int slab = lane >> 4, qd = lane & 15;
+                            const uint4 id = ld_shared_v4(look + 16 * ((first * 4 + qd) & 31));
+                            ok = ok && claim((uint32_t)nu * 4096u);
+                            if (ok && qd < 4 * ku)
+                                tma_gather4_pair(dst + slab * 8192 + qd * 512, &km.m[0], (2 * kk + slab) * 64,
+                                                 make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
+                        }
+                        __syncwarp();
+                        sidx += 4 - kk;
+                        turn += LP_PROD - 4;
+                    } else {
+                        sidx += 4;
+                        turn -= 4;
+                    }
+                }
+                if (i > 0) {
+                    const int gt = g + i - 1;
+                    if (turn < 4) {
+                        const int v = turn, nu = min(8, units - 8 * (i - 1));
+                        ok = ok && lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead);
+                        const uint32_t look = sb + LP_SM_LOOK + (gt & 7) * 512;
+                        sidx += v;
+                        const int vu = min(max(nu - 2 * v, 0), 2), sl = sidx & (LP_SLOTS - 1);
+                        const uint32_t dst = sb + LP_SM_RING + (uint32_t)sl * LP_SLOT, bar = full0 + 8 * sl;
+                        if (BOX) {
+                            const int s = lane & 3, e = (lane >> 2) & 1;
+                            const uint2 at = ld_shared_v2(look + 8 * (2 * v + e));
+                            uint32_t runs;
+                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(runs) : "r"(look + 64));
+                            const int big = vu == 2 && ((runs >> (2 * v)) & 1u) ? (e ? -1 : 1) : 0;
+                            ok = ok && claim((uint32_t)vu * 16384u);
+                            if (ok && lane < 4 * vu && big >= 0)
+                                tma_load_3d_pair(dst + s * 4096 + e * 2048, &km.m[big], (int)rank * 256 + s * 64, (int)at.y,
+                                                 (int)at.x, bar);
+                        } else {
+                            const int s = lane >> 3, qd = lane & 7;
+                            const uint4 id = ld_shared_v4(look + 16 * ((v * 8 + qd) & 31));
+                            ok = ok && claim((uint32_t)vu * 16384u);
+                            if (ok && qd < 4 * vu)
+                                tma_gather4_pair(dst + s * 4096 + qd * 512, &km.m[0], (int)rank * 256 + s * 64,
+                                                 make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
+                        }
+                        __syncwarp();
+                        sidx += 4 - v;
+                        turn += LP_PROD - 4;
+                    } else {
+                        sidx += 4;
+                        turn -= 4;
+                    }
+                    if (lane == 0) mbar_arrive(sb + LP_USED + 8 * (gt & 7));  // done with the tile's lookups
+                }
+            }
+            g += x.T;
         }
     }
     __syncwarp();
     pdl_launch_dependents();
     if (!ok) {  // a wait ran out: leave the copies and products in flight some time to end
         if (lane == 0) raise_status(a.status, CSA_ERR_TIMEOUT);
+#pragma unroll 1
         for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
     tc_fence_before();
@@ -773,12 +808,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const CUtensor
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
-    lat_box_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, LatArgs a) {
-    lat_pair<true>(qmap, kmap, a);
+    lat_box_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps km, const __grid_constant__ LatArgs a) {
+    lat_pair<true>(qmap, km, a);
 }
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
-    lat_gather_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap, LatArgs a) {
-    lat_pair<false>(qmap, kmap, a);
+    lat_gather_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps km, const __grid_constant__ LatArgs a) {
+    lat_pair<false>(qmap, km, a);
 }
 
 // Log-sum-exp merge of a row's partial results, in their order: one CTA per row, thread t columns
@@ -918,24 +953,30 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     }
     const int sms = device_sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
-    CUtensorMap qm, km;
+    a.rpp_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (kv.rows_per_page == 1 << i) a.rpp_shift = i;
+    CUtensorMap qm;
+    KeyMaps km;
     const uint64_t qd[2] = {(uint64_t)D, (uint64_t)a.rows}, qs[1] = {ROW_BYTES};
     const uint32_t qb[2] = {64, 64};
     if (!make_bf16_map(&qm, q, 2, qd, qs, qb)) return cudaErrorInvalidValue;
     const bool box = kv.rows_per_page % 16 == 0;
-    if (box) {
-        const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
-        const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
-        const uint32_t b[3] = {64, 16, 1};
-        if (!make_bf16_map(&km, kv.base, 3, d, st, b)) return cudaErrorInvalidValue;
-    } else {
-        // rows behind the last page's own are not there: the extent ends with them
-        const uint64_t d[2] = {(uint64_t)D, (uint64_t)((kv.n_pages - 1) * (kv.page_stride_bytes / ROW_BYTES) + kv.rows_per_page)};
-        const uint64_t st[1] = {ROW_BYTES};
-        const uint32_t b[2] = {64, 1};
-        if (!make_bf16_map(&km, kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
+    for (int i = 0; i < 3; ++i) {
+        if (box) {  // a box never reaches behind its page: only runs of units are copied in larger ones
+            const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
+            const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
+            const uint32_t b[3] = {64, 16u << i, 1};
+            if (!make_bf16_map(&km.m[i], kv.base, 3, d, st, b)) return cudaErrorInvalidValue;
+        } else {  // the extent ends with the last page's own rows
+            const uint64_t per_page = (uint64_t)(kv.page_stride_bytes / ROW_BYTES);
+            const uint64_t d[2] = {(uint64_t)D, (uint64_t)(kv.n_pages - 1) * per_page + (uint64_t)kv.rows_per_page};
+            const uint64_t st[1] = {ROW_BYTES};
+            const uint32_t b[2] = {64, 1};
+            if (!make_bf16_map(&km.m[i], kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
+        }
     }
-    void (*kernel)(CUtensorMap, CUtensorMap, LatArgs) = box ? lat_box_kernel : lat_gather_kernel;
+    void (*kernel)(CUtensorMap, KeyMaps, LatArgs) = box ? lat_box_kernel : lat_gather_kernel;
     cudaError_t e = set_func_attr_once((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LP_SMEM);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, sms / 2));

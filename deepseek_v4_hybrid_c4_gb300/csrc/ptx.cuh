@@ -69,19 +69,28 @@ CSA_DEV void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
-// Tiled 2-D tensor copy, and a gather of four rows (a tensor map whose box is one row high) written one
-// behind the other; row ids have no alignment rule.
-CSA_DEV void tma_load_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
+// Tensor copies of one CTA of a pair (cta_group::2) into its own shared memory; bar may be an
+// mbarrier of either CTA of the pair, as a shared::cluster address.  2-D and 3-D boxes, and a gather of
+// four rows (a tensor map whose box is one row high) written one behind the other; row ids have no
+// alignment rule.
+CSA_DEV void tma_load_2d_pair(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            dst),
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-CSA_DEV void tma_gather4(uint32_t dst, const void* map, int c0, int4 rows, uint32_t bar) {
+CSA_DEV void tma_load_3d_pair(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4, %5, %6}], [%7];" ::"r"(dst),
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+CSA_DEV void tma_gather4_pair(uint32_t dst, const void* map, int c0, int4 rows, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar)
         : "memory");
 }
@@ -247,25 +256,13 @@ CSA_DEV void st_dsmem_u32(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
-// Arrive (once) on the mbarrier at the same shared-memory address in CTA `rank` of this cluster;
-// what this thread did and saw before is visible to a cluster-scope wait on it.
+// Arrive (once) on the mbarrier at the same shared-memory address in CTA `rank` of this cluster.
 CSA_DEV void mbar_arrive_rank(uint32_t bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
         : "memory");
-}
-CSA_DEV bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // ------------------------------------------------------------------ tcgen05 over a pair of CTAs
