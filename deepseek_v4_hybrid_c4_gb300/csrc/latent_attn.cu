@@ -54,7 +54,7 @@ constexpr int LP_PAIRS = 76;                              // pairs of SMs: sizes
 constexpr uint32_t LP_SLOT = 16384;
 constexpr uint32_t LP_QSLAB = 64 * 128;                   // 64 dims of the CTA's 64 query rows
 constexpr uint32_t LP_SM_RING = 8 * LP_QSLAB;             // behind Q
-constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 64 keys x 64 rows; output staging
+constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 64 keys x 64 rows
 constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
 constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
 constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
@@ -66,15 +66,31 @@ constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row 
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
 constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of the threads
 constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
-constexpr uint32_t LP_SMEM = LP_SM_ITEM + 4 * 128 + 1024; // + alignment slack
+constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] plain or not (tile_plain)
+constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr float LP_LOG2E = 1.4426950408889634f;
 constexpr float LP_LN2 = 0.6931471805599453f;
 constexpr float LP_RESCALE = 8.0f;                        // log2 units
 
+// n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and m = ceil(2^(31+s) / d) < 2^32,
+// m n / 2^(31+s) exceeds n / d by less than n / 2^31 / d < 1 / d.
+struct FastDiv {
+    uint32_t m, s;
+};
+static FastDiv fast_div(uint32_t d) {
+    FastDiv f = {0, 0};
+    while ((1u << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << (31 + f.s)) + d - 1) / d);
+    return f;
+}
+__device__ __forceinline__ int div_by(int n, FastDiv f) { return (int)(((uint64_t)(uint32_t)n * f.m) >> (31 + f.s)); }
+
 struct LatArgs {
     int H;
-    float sl2;                 // scale * log2(e)
+    FastDiv by_H;
+    float sl2;                 // |scale| * log2(e); the sign is in the products
+    uint32_t negate;           // instruction-descriptor bit that negates Q
     DPaged kv;
     int64_t table_pages;       // entries of a request's page table
     int rpp_shift;             // log2 of the rows per page, -1 where they are no power of two
@@ -94,6 +110,7 @@ struct LatArgs {
     float* part_o;             // [parts][rows][512] normalised
     float* part_lse;           // [parts][rows]
     uint16_t* out;
+    bool wide_out;             // out is 32-byte aligned
     float* lse;
     int32_t* status;
 };
@@ -111,7 +128,16 @@ struct LatItem {
     int shared;                // prefix: the shared rows (else request trow's own)
     int64_t pos0;              // window: position of the sequence's first new token
 };
-static_assert(sizeof(LatItem) <= 128, "an item's place in shared memory");
+static_assert(sizeof(LatItem) == 72, "an item's place in shared memory is read in 16-byte pieces");
+__device__ __forceinline__ LatItem load_item(uint32_t at) {
+    union {
+        LatItem x;
+        uint4 v[5];
+    } u;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) u.v[i] = ld_shared_v4(at + 16 * i);
+    return u.x;
+}
 
 // Sequences by row tiles, 32 at a time, one per lane; item indices ascend.
 struct SeqCursor {
@@ -143,7 +169,7 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
             x.trow = 0;
             x.part = split;
             // the shortest and the longest of the rows' requests
-            const int b0 = x.row0 / a.H, b1 = (x.row0 + x.nrows - 1) / a.H;
+            const int b0 = div_by(x.row0, a.by_H), b1 = div_by(x.row0 + x.nrows - 1, a.by_H);
             int mn = 0x7FFFFFFF, mx = 0;
             for (int b = b0 + lane; b <= b1; b += 32) {
                 const int64_t n = __ldg(a.n_rows + b);
@@ -218,7 +244,7 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.part = split;
         x.shared = 0;
         x.pos0 = (nt > 0 ? nt : 0) - ql;
-        const int64_t p0 = x.pos0 + x.rr0 / a.H, p1 = x.pos0 + (x.rr0 + x.nrows - 1) / a.H;
+        const int64_t p0 = x.pos0 + div_by(x.rr0, a.by_H), p1 = x.pos0 + div_by(x.rr0 + x.nrows - 1, a.by_H);
         x.hi = p1 >= 0 ? (int)p1 + 1 : 0;
         x.lo = p0 >= a.window ? (int)p0 - a.window + 1 : 0;
         x.a1 = min(a.n_sink, x.hi);
@@ -237,6 +263,13 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
 
 __device__ __forceinline__ int item_units(const LatItem& x, int i) { return min(8, x.nU - (x.t0 + i) * 8); }
 __device__ __forceinline__ int unit_row(const LatItem& x, int u) { return (u < x.uA ? u : u - x.uA + x.uB) * 16; }
+
+// Tile i of the item: every row seen by every query of the item, and every page there (vw: the rows that are).
+__device__ __forceinline__ bool tile_plain(const LatItem& x, int i, uint4 vw) {
+    const int u0 = (x.t0 + i) * 8;
+    return x.nU - u0 >= 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && u0 >= x.uA && unit_row(x, u0) >= x.full_lo &&
+           unit_row(x, u0 + 7) + 16 <= x.full_hi;
+}
 
 // Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
 // stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
@@ -258,6 +291,16 @@ __device__ __forceinline__ float lat_ex2(float x) {  // ex2.approx.ftz: relative
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 32 bytes to global memory; narrow: only 16-byte aligned.
+__device__ __forceinline__ void store_sector(uint8_t* p, const uint32_t* w, bool wide) {
+    if (wide) {
+        stg_v8(p, w);
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // Row id of logical row j of the item's request, -1 where there is no page (or none inside the pool).
@@ -324,7 +367,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     // The next item as warp 9 left it; false behind the last one, and when a wait has run out.
     auto next_item = [&]() -> bool {
         const bool in = lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
-        x = *reinterpret_cast<const LatItem*>(sm + LP_SM_ITEM + (q & 3) * 128);
+        x = load_item(sb + LP_SM_ITEM + (q & 3) * 128);
         __syncwarp();
         if (lane == 0) mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
         ++q;
@@ -345,12 +388,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             int vlo = 0, vhi = 0, vs = 0;
             if (mine) {
                 if (!a.n_rows) {
-                    const int64_t pos = x.pos0 + (x.rr0 + (int)rank * 64 + r) / a.H;
+                    const int64_t pos = x.pos0 + div_by(x.rr0 + (int)rank * 64 + r, a.by_H);
                     vhi = pos >= 0 ? (int)pos + 1 : 0;
                     vlo = max(0, vhi - a.window);
                     vs = min(a.n_sink, vhi);
                 } else if (x.shared) {
-                    const int64_t nr = __ldg(a.n_rows + row / a.H);
+                    const int64_t nr = __ldg(a.n_rows + div_by(row, a.by_H));
                     vhi = nr < 0 ? 0 : (nr > x.hi ? x.hi : (int)nr);
                 } else {
                     vlo = x.lo;
@@ -362,34 +405,30 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const int nu = item_units(x, i), mu = (nu + 1) >> 1;  // units in all, and per half
                 const int c0 = ch ? (mu + 1) >> 1 : 0, nc = ch ? mu - c0 : (mu + 1) >> 1;  // this thread's
                 const int ub = half * mu + c0, u0 = (x.t0 + i) * 8;
-                ok = lat_wait(sb + LP_LOOK + 8 * (g & 7), (g >> 3) & 1, dead) && ok;
-                const uint4 vw = ld_shared_v4(sb + LP_SM_VALID + (g & 7) * 16);
-                // every row of the tile seen by every query of the item, and every page there
-                const bool plain = nu == 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && u0 >= x.uA &&
-                                   unit_row(x, u0) >= x.full_lo && unit_row(x, u0 + 7) + 16 <= x.full_hi;
-                ok = lat_wait(sb + LP_SFULL + 8 * (g & 1), (g >> 1) & 1, dead) && ok;
+                // the tile's lookups and its S, waited for together (even and odd lanes)
+                ok = __all_sync(0xffffffffu, lane & 1 ? lat_wait(sb + LP_LOOK + 8 * (g & 7), (g >> 3) & 1, dead)
+                                                      : lat_wait(sb + LP_SFULL + 8 * (g & 1), (g >> 1) & 1, dead)) && ok;
                 tc_fence_after();
                 uint32_t sr[32];
                 const uint32_t ts = tmem + 256 + (uint32_t)((g & 1) * 64 + 16 * c0) + lane_off;
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (c < nc) tc_ld16(ts + 16 * c, sr + 16 * c);
+                const bool plain = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4) != 0;
                 tc_wait_ld();
-                float mt = -INFINITY;
+                float mt = -INFINITY;  // of the logits before scaling
                 bool bad = false;
                 float* xs = reinterpret_cast<float*>(sr);
                 if (plain) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        xs[j] = __uint_as_float(sr[j]) * a.sl2;
-                        mt = fmaxf(mt, xs[j]);
-                    }
+                    for (int j = 0; j < 32; ++j) mt = fmaxf(mt, xs[j]);
                 } else {
-                    float z = 0.f;  // NaN where a logit of the tile is not finite
+                    const uint4 vw = ld_shared_v4(sb + LP_SM_VALID + (g & 7) * 16);
+                    uint64_t z = 0;  // NaN where a logit of the tile is not finite
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+                        const int u = ub + c;
                         if (c < nc) {
-                            const int u = ub + c;
                             uint32_t bits = 0;
                             if (u < nu) {
                                 const int jb = unit_row(x, u0 + u);
@@ -398,18 +437,24 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                                 bits = (((1u << e1) - 1u) & ~((1u << e0) - 1u)) | ((1u << e2) - 1u);
                                 const uint32_t vv = u < 4 ? (u < 2 ? vw.x : vw.y) : (u < 6 ? vw.z : vw.w);
                                 bits &= vv >> ((u & 1) * 16);
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2)
+                                    z = f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), 0ull, z);
+                            }
+                            if (!__all_sync(0xffffffffu, bits == 0xFFFFu)) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (!((bits >> j) & 1u)) xs[16 * c + j] = -INFINITY;
                             }
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float s = __uint_as_float(sr[16 * c + j]);
-                                if (u < nu) z = fmaf(s, 0.f, z);
-                                xs[16 * c + j] = (bits >> j) & 1u ? s * a.sl2 : -INFINITY;
-                                mt = fmaxf(mt, xs[16 * c + j]);
-                            }
+                            for (int j = 0; j < 16; ++j) mt = fmaxf(mt, xs[16 * c + j]);
                         }
                     }
-                    bad = !(z == 0.f);
+                    const float2 zz = f32x2_split(z);
+                    bad = !(zz.x == 0.f) || !(zz.y == 0.f);
+                    ++n;  // tiles that are not plain so far
                 }
+                mt *= a.sl2;
                 // the row's other quarters, and whether any logit of the tile is not finite
                 float* mb = mx + (g & 1) * 256;
                 mb[tid] = mt;
@@ -425,20 +470,22 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
-                float sum0 = 0.f, sum1 = 0.f;
+                const uint64_t sl2 = f32x2(a.sl2, a.sl2), mneg = f32x2(-mref, -mref);
+                uint64_t sum = 0;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (c < nc) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float p0 = lat_ex2(xs[16 * c + j] - mref), p1 = lat_ex2(xs[16 * c + j + 1] - mref);
-                            sum0 += p0;
-                            sum1 += p1;
+                            const float2 e = f32x2_split(f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), sl2, mneg));
+                            const float p0 = lat_ex2(e.x), p1 = lat_ex2(e.y);
+                            sum = f32x2_add(sum, f32x2(p0, p1));
                             sr[8 * c + (j >> 1)] = pack_bf16x2(p0, p1);
                         }
                     }
                 }
-                l_run = l_run * alpha + (sum0 + sum1);
+                const float2 ss = f32x2_split(sum);
+                l_run = l_run * alpha + (ss.x + ss.y);
                 // P and O are free once the product before this one is done
                 if (i > 0) {
                     ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
@@ -469,7 +516,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 if (any_bad) {  // non-finite values of this CTA's V rows -> 0
-                    ok = lat_wait(sb + LP_VLAND, g & 1, dead) && ok;
+                    ok = lat_wait(sb + LP_VLAND, (n - 1) & 1, dead) && ok;
                     const int vs0 = sidx + 4 * min(i + 2, x.T) + 4 * i;  // the tile's first V slot
 #pragma unroll 1
                     for (int s = 0; s < (nu + 1) >> 1; ++s) {
@@ -503,51 +550,38 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 named_bar_sync(1, 32 * LP_SOFT);
                 l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
             }
-            // ---- rows [32 (warp & 1), + 32) of the CTA, dims [256 half + 128 ch, + 128): normalised, staged 64 bytes a
-            //      row in the P buffer, written 64 bytes a row
+            // ---- row r of the CTA, dims [256 half + 128 ch, + 128): normalised and written a sector (32 bytes) at
+            //      a time (through shared memory, for whole lines, the round trips cost more than the lines gain:
+            //      4,070 cycles an item)
             const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-            const uint32_t stg = sb + LP_SM_P + (uint32_t)warp * 2048;
             const bool direct = a.parts == 1;
-            const int wrow = (int)rank * 64 + (warp & 1) * 32;  // the warp's first row of the item
             if (direct || x.T > 0) {
-                const int64_t gr0 = x.row0 + wrow;
-                uint8_t* dst0 = direct ? reinterpret_cast<uint8_t*>(a.out + gr0 * D + half * 256 + ch * 128)
-                                       : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr0) * D +
-                                                                    half * 256 + ch * 128);
-                const int64_t pitch = direct ? D * 2 : D * 4;
+                const int at = half * 256 + ch * 128;
+                uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out + (int64_t)row * D + at)
+                                      : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + row) * D + at);
 #pragma unroll 1
-                for (int c = 0; c < (direct ? 4 : 8); ++c) {
-                    uint32_t w[16];
-                    if (x.T == 0) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = 0;
-                    } else if (direct) {
-                        uint32_t o[32];
-                        tc_ld32(tmem + lane_off + 128 * ch + 32 * c, o);
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32];
+                    if (x.T > 0) {
+                        tc_ld32(tmem + lane_off + 128 * ch + c, o);
                         tc_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+                    if (!mine) continue;
+                    if (direct) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                            o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        store_sector(dst + c * 2, o, a.wide_out);
+                        store_sector(dst + c * 2 + 32, o + 8, a.wide_out);
                     } else {
-                        tc_ld16(tmem + lane_off + 128 * ch + 16 * c, w);
-                        tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * inv);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) store_sector(dst + c * 4 + 32 * e, o + 8 * e, true);
                     }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        st_shared_v4(stg + lane * 64 + ((uint32_t)(e ^ ((lane >> 1) & 3)) << 4),
-                                     make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int rr = e * 8 + (lane >> 2);
-                        if (wrow + rr < x.nrows) {
-                            const uint4 v = ld_shared_v4(stg + rr * 64 + ((uint32_t)((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-                            *reinterpret_cast<uint4*>(dst0 + rr * pitch + c * 64 + (lane & 3) * 16) = v;
-                        }
-                    }
-                    __syncwarp();
                 }
                 tc_fence_before();
             }
@@ -558,31 +592,40 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             }
         }
     } else if (warp == LP_SOFT && rank == 0) {
-        // ---------------------------------------------------------------- the products
-        const bool one = elect_one();
-        const uint64_t dk = sdesc_sw128(sb, 16, 1024), dv = sdesc_sw128(sb, 4096, 1024);
-        const uint32_t klo = (uint32_t)dk, khi = (uint32_t)(dk >> 32), vlo = (uint32_t)dv, vhi = (uint32_t)(dv >> 32);
-        auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
-            return ((uint64_t)hi << 32) | (uint64_t)(lo + (off >> 4));
-        };
-        while (next_item()) {
-            if (x.T == 0) continue;
-            ok = lat_wait(sb + LP_QFULL, n & 1, dead);
-            ++n;
-            const int units = x.nU - x.t0 * 8;
-            // S of tile i, then P V of tile i - 1
+        // ---------------------------------------------------------------- the products (one thread)
+        if (elect_one()) {
+            const uint64_t dk = sdesc_sw128(sb, 16, 1024), dv = sdesc_sw128(sb, 4096, 1024);
+            const uint32_t klo = (uint32_t)dk, khi = (uint32_t)(dk >> 32), vlo = (uint32_t)dv, vhi = (uint32_t)(dv >> 32);
+            auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
+                return ((uint64_t)hi << 32) | (uint64_t)(lo + (off >> 4));
+            };
+            for (; ok; ++q) {
+                ok = lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
+                x = load_item(sb + LP_SM_ITEM + (q & 3) * 128);
+                const int T = x.T, units = x.nU - x.t0 * 8;
+                mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
+                if (T < 0) break;
+                if (T == 0) continue;
+                ok = ok && lat_wait(sb + LP_QFULL, n & 1, dead);
+                ++n;
+                // S of tile i, then P V of tile i - 1.  Each slot's barrier is tested while the products of the slot
+                // before it are issued: beside the copies and the products, a look at a barrier takes 150 cycles
+                // and more.
 #pragma unroll 1
-            for (int i = 0; ok && i <= x.T; ++i) {
-                if (i < x.T) {
-                    const int mu = (min(8, units - 8 * i) + 1) >> 1;
-                    const uint32_t ids = (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17);
-                    const uint32_t d = tmem + 256 + (uint32_t)((g + i) & 1) * 64, reg = (uint32_t)(sidx >> 2) & 1;
-                    ok = __all_sync(0xffffffffu, lat_wait(sb + LP_FULL + 32 * reg + 8 * (lane & 3), (sidx >> 3) & 1, dead));
-                    tc_fence_after();
-                    if (ok && one) {
-                        const uint32_t bl = klo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4);
+                for (int i = 0; ok && i <= T; ++i) {
+                    if (i < T) {
+                        const int mu = (min(8, units - 8 * i) + 1) >> 1;
+                        const uint32_t ids = (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17) | a.negate;
+                        const uint32_t d = tmem + 256 + (uint32_t)((g + i) & 1) * 64, reg = (uint32_t)(sidx >> 2) & 1;
+                        const uint32_t bl = klo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4), par = (uint32_t)(sidx >> 3) & 1;
+                        const uint32_t full = sb + LP_FULL + 32 * reg;
+                        bool there = mbar_test_wait(full, par);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
+                            if (!there) ok = ok && lat_wait(full + 8 * kk, par, dead);
+                            if (!ok) break;
+                            if (kk < 3) there = mbar_test_wait(full + 8 * kk + 8, par);
+                            tc_fence_after();
 #pragma unroll
                             for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -592,44 +635,56 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * kk);
                         }
                         tc_commit_pair(sb + LP_SFULL + 8 * ((g + i) & 1));
-                        if (i + 1 == x.T) tc_commit_pair(sb + LP_QEMPTY);
+                        if (i + 1 == T) tc_commit_pair(sb + LP_QEMPTY);
+                        sidx += 4;
                     }
-                    __syncwarp();
-                    sidx += 4;
-                }
-                if (i > 0 && ok) {
-                    const int nu = min(8, units - 8 * (i - 1));
-                    const uint32_t reg = (uint32_t)(sidx >> 2) & 1;
-                    ok = __all_sync(0xffffffffu, lat_wait(sb + LP_FULL + 32 * reg + 8 * (lane & 3), (sidx >> 3) & 1, dead));
-                    if (ok && one) tc_commit_pair(sb + LP_VLAND);
-                    __syncwarp();
-                    ok = ok && lat_wait(sb + LP_PREADY, (g + i - 1) & 1, dead);
-                    tc_fence_after();
-                    if (ok && one) {
+                    if (i > 0 && ok) {
+                        const int nu = min(8, units - 8 * (i - 1)), gt = g + i - 1;
+                        const uint32_t reg = (uint32_t)(sidx >> 2) & 1, par = (uint32_t)(sidx >> 3) & 1;
                         const uint32_t bl = vlo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4);
+                        const uint32_t full = sb + LP_FULL + 32 * reg;
                         constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
+                        bool there = mbar_test_wait(full, par);
+                        const uint32_t plain = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4);
+                        const bool ready = mbar_test_wait(sb + LP_PREADY, gt & 1);
+                        if (!plain) {
+                            // the softmax may have to look into the tile's V rows: tell both CTAs that they are there
+#pragma unroll 1
+                            for (int v = 0; v < 4; ++v) ok = ok && lat_wait(full + 8 * v, par, dead);
+                            if (ok) tc_commit_pair(sb + LP_VLAND);
+                        }
+                        if (!ready) ok = ok && lat_wait(sb + LP_PREADY, gt & 1, dead);
+                        tc_fence_after();
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            if (u < nu) {
+                        for (int v = 0; v < 4; ++v) {
+                            if (!there) ok = ok && lat_wait(full + 8 * v, par, dead);
+                            if (!ok) break;
+                            if (v < 3) there = mbar_test_wait(full + 8 * v + 8, par);
+                            tc_fence_after();
 #pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, LP_SM_P + (u >> 2) * LP_QSLAB + (u & 3) * 32),
-                                                    desc(bl, vhi, (u >> 1) * LP_SLOT + c * 8192 + (u & 1) * 2048), idv,
-                                                    i == 1 && u == 0 ? 0u : 1u);
+                            for (int e = 0; e < 2; ++e) {
+                                const int u = 2 * v + e;
+                                if (u < nu) {
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+                                        tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, LP_SM_P + (u >> 2) * LP_QSLAB + (u & 3) * 32),
+                                                        desc(bl, vhi, v * LP_SLOT + c * 8192 + e * 2048), idv,
+                                                        i == 1 && u == 0 ? 0u : 1u);
+                                }
                             }
-                            if (u & 1) tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * (u >> 1));
+                            tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * v);
                         }
                         tc_commit_pair(sb + LP_PVDONE);
+                        sidx += 4;
                     }
-                    __syncwarp();
-                    sidx += 4;
                 }
+                g += T;
             }
-            g += x.T;
         }
     } else if (warp == LP_SOFT + 1) {
         // ---------------------------------------------------------------- the tiles' pages, and Q
         const uint32_t qfull = mapa(sb + LP_QFULL, 0);
+        uint32_t* plain = reinterpret_cast<uint32_t*>(sm + LP_SM_PLAIN);
         SeqCursor cur;
         for (int it = pair; ok; it += pairs, ++q) {
             const bool there = lat_item(a, cur, it, lane, rank == 0, x);
@@ -683,7 +738,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     if ((lane & 7) == 0) vw[lane >> 3] = v;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sb + LP_LOOK + 8 * slot);
+                if (lane == 0) {
+                    plain[slot] = tile_plain(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u;
+                    mbar_arrive(sb + LP_LOOK + 8 * slot);
+                }
                 if (i == 0) {  // Q, behind the first tile's lookups
                     if (n > 0) ok = lat_wait(sb + LP_QEMPTY, (n - 1) & 1, dead) && ok;
                     ++n;
@@ -729,8 +787,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             // lane: unit e of the CTA's own (at most 4), slab; the first unit of a run takes all of it
                             const int slab = lane & 1, e = (lane >> 1) & 3;
                             const uint2 at = ld_shared_v2(look + 8 * ((first + e) & 7));
-                            uint32_t runs;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(runs) : "r"(look + 64));
+                            uint32_t runs = ld_shared_u32(look + 64);
                             runs = (runs >> first) & ((1u << max(ku - 1, 0)) - 1u);  // bit e: unit e + 1 follows e
                             // rows of this lane's copy: 0 where another unit's covers it
                             const int big = runs == 7u ? (e == 0 ? 2 : -1) : ((runs >> (e & 2)) & 1u ? ((e & 1) ? -1 : 1) : 0);
@@ -766,8 +823,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         if (BOX) {
                             const int s = lane & 3, e = (lane >> 2) & 1;
                             const uint2 at = ld_shared_v2(look + 8 * (2 * v + e));
-                            uint32_t runs;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(runs) : "r"(look + 64));
+                            uint32_t runs = ld_shared_u32(look + 64);
                             const int big = vu == 2 && ((runs >> (2 * v)) & 1u) ? (e ? -1 : 1) : 0;
                             ok = ok && claim((uint32_t)vu * 16384u);
                             if (ok && lane < 4 * vu && big >= 0)
@@ -832,27 +888,41 @@ __global__ void __launch_bounds__(128) lat_merge_kernel(LatArgs a) {
         const int64_t q0 = __ldg(a.q_offsets + l), q1 = __ldg(a.q_offsets + l + 1);
         if (q < q0 || q >= q1 || !seq_valid(a, q0, q1, __ldg(a.n_tokens + l))) return;
     }
+    // eight partial rows in flight at a time; their maximum so far is kept as a running one
     const float* lp = a.part_lse + row;
-    const float* op = a.part_o + (int64_t)row * D + t * 4;
+    const float4* op = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * D) + t;
     const int64_t step = (int64_t)a.rows;
-    float M = -INFINITY;
+    float M = -INFINITY, L = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
     bool nan = false;
-    for (int s = 0; s < a.parts; ++s) {
-        const float v = __ldcg(lp + s * step);
-        M = fmaxf(M, v);
-        nan = nan || v != v;
-    }
-    float L = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-    for (int s = 0; s < a.parts; ++s) {
-        const float v = __ldcg(lp + s * step);
-        if (v == -INFINITY) continue;
-        const float w = lat_ex2((v - M) * LP_LOG2E);
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(op + s * step * D));
-        L += w;
-        o0 = fmaf(w, f.x, o0);
-        o1 = fmaf(w, f.y, o1);
-        o2 = fmaf(w, f.z, o2);
-        o3 = fmaf(w, f.w, o3);
+    for (int s0 = 0; s0 < a.parts; s0 += 8) {
+        float v[8];
+        float4 f[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            v[s] = s0 + s < a.parts ? __ldcg(lp + (s0 + s) * step) : -INFINITY;
+            if (s0 + s < a.parts) f[s] = __ldcg(op + (s0 + s) * step * (D / 4));
+        }
+        float m = M;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            m = fmaxf(m, v[s]);
+            nan = nan || v[s] != v[s];
+        }
+        if (m > M) {
+            const float w = M == -INFINITY ? 0.f : lat_ex2((M - m) * LP_LOG2E);
+            L *= w, o0 *= w, o1 *= w, o2 *= w, o3 *= w;
+            M = m;
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (v[s] == -INFINITY) continue;  // (no keys: its row may hold anything)
+            const float w = lat_ex2((v[s] - M) * LP_LOG2E);
+            L += w;
+            o0 = fmaf(w, f[s].x, o0);
+            o1 = fmaf(w, f[s].y, o1);
+            o2 = fmaf(w, f[s].z, o2);
+            o3 = fmaf(w, f[s].w, o3);
+        }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     uint2 w;
@@ -896,6 +966,12 @@ static csa_status check_window(int32_t B, int32_t H, int64_t total_q, int64_t ma
     if (window < 1 || n_sink < 0 || total_q < 0 || max_q < 1) return CSA_ERR_INVALID_ARG;
     if (total_q > 0x7FFFFFFFLL / H || max_q > 0x7FFFFFFFLL) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
+}
+
+static void set_scale(LatArgs& a, float scale) {
+    a.sl2 = (scale < 0.f ? -scale : scale) * LP_LOG2E;
+    if (a.sl2 == 0.f) a.sl2 = 1e-30f;  // every weight 1, and a masked logit still -inf
+    a.negate = scale < 0.f ? 1u << 13 : 0u;
 }
 
 // Splits of the shared rows: the number that ends the row tiles soonest on LP_PAIRS pairs, where an
@@ -942,15 +1018,18 @@ static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window
 
 static size_t parts_bytes(const LatArgs& a) {
     if (a.parts <= 1) return 0;
-    return align_up((size_t)a.parts * a.rows * D * sizeof(float), 256) + align_up((size_t)a.parts * a.rows * sizeof(float), 256);
+    // (the partial rows start at a 256-byte boundary inside a workspace that is 16-byte aligned)
+    return 256 + align_up((size_t)a.parts * a.rows * D * sizeof(float), 256) +
+           align_up((size_t)a.parts * a.rows * sizeof(float), 256);
 }
 
 static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, int64_t items, void* ws, cudaStream_t s) {
     if (a.parts > 1) {
-        a.part_o = static_cast<float*>(ws);
-        a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                              align_up((size_t)a.parts * a.rows * D * sizeof(float), 256));
+        uint8_t* base = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
+        a.part_o = reinterpret_cast<float*>(base);
+        a.part_lse = reinterpret_cast<float*>(base + align_up((size_t)a.parts * a.rows * D * sizeof(float), 256));
     }
+    a.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     const int sms = device_sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
     a.rpp_shift = -1;
@@ -1024,7 +1103,8 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
-    a.sl2 = scale * LP_LOG2E;
+    set_scale(a, scale);
+    a.by_H = fast_div(H);
     a.kv = cache_of(kv, page_table_stride);
     a.table_pages = page_table_stride;
     a.B = B;
@@ -1064,7 +1144,8 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
-    a.sl2 = scale * LP_LOG2E;
+    set_scale(a, scale);
+    a.by_H = fast_div(H);
     a.kv = cache_of(kv_raw, page_table_stride);
     a.table_pages = page_table_stride;
     a.B = B;

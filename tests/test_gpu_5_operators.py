@@ -149,6 +149,38 @@ def test_prefix_attention_with_page_gaps_and_without_lse(m):
         check(out[b], w[1].float(), w, f"request {b}")
 
 
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1.5])
+def test_attention_with_other_scales(m, scale):
+    """A negative scale, a scale of zero (every row the same weight), logits of hundreds; outputs and
+    workspace at addresses that are 16-byte aligned and no more."""
+    g = gen(6)
+    n_rows, H, W, S = [300, 190], 20, 70, 3
+    c = Cache(g, n_rows, 32, 160)
+    q = randn(g, 2, H, D)
+    n = torch.tensor(n_rows, dtype=torch.int64, device="cuda")
+    off = torch.tensor([0, 1, 2], dtype=torch.int64, device="cuda")
+    need = max(m.csa_prefix_attn_workspace_size(2, H, 160, 300), m.csa_window_attn_workspace_size(2, H, 2, 1, W, S))
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")[16:]
+    for call in range(2):
+        out = torch.empty(2 * H * D + 8, dtype=torch.bfloat16, device="cuda")[8:].view(2, H, D)
+        assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+        lse = torch.empty(2, H, dtype=torch.float32, device="cuda")
+        if call == 0:
+            m.csa_prefix_attn(q, 2, H, scale, c.paged(m), c.width, 160, n, 300, out, lse, ws, need)
+        else:
+            m.csa_window_attn(q, H, scale, c.paged(m), c.width, 2, off, n, 2, 1, W, S, out, lse, ws, need)
+        for b in range(2):
+            keys = range(n_rows[b]) if call == 0 else list(range(S)) + list(range(n_rows[b] - W, n_rows[b]))
+            kv = c.rows(b, keys)
+            x = scale * (q[b].double() @ kv.t())
+            want_lse = torch.logsumexp(x, -1)
+            w = torch.exp(x - want_lse[:, None])
+            o, av = w @ kv, w @ kv.abs()
+            d = 2.0**-14 * abs(scale) * (q[b].double().abs() @ kv.abs().t()).amax(-1)
+            check(out[b], lse[b], (o, want_lse, 2.0**-8 * (av + o.abs()) + (2 * d[:, None] + 2.0**-20) * av,
+                                   d + 2.0**-20 * (1 + want_lse.abs())), f"call {call} request {b}")
+
+
 def test_prefix_attention_rising_logits(m):
     """Each tile's largest logit far above the ones before it: the running maximum moves at every tile."""
     g = gen(3)
