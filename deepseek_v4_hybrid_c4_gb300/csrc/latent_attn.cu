@@ -15,10 +15,9 @@
 // dims would have to compute S twice).  Measured on GB300 with nothing but these products in flight: 2,056 cycles
 // a tile against 2,048 at the nominal rate.
 //
-// Roles (20 warps a CTA): warps 0-7 do the softmax, two to a quarter of the TMEM lanes; warps 8-11 write the
-// output, beside the next item's softmax; warp 12 of the even CTA issues the products; warp 13 works the items
-// out for the others, looks up the tiles' pages, up to four tiles ahead, and loads Q; warps 14-19 load key
-// rows.  Both CTAs' copies report to the even CTA's
+// Roles (16 warps a CTA): warps 0-7 own the TMEM lanes, two to a lane quarter (softmax, output); warp 8 of
+// the even CTA issues the products; warp 9 works the items out for the others, looks up the tiles' pages, up to
+// four tiles ahead, and loads Q; warps 10-15 load key rows.  Both CTAs' copies report to the even CTA's
 // barriers.  The loops are kept short and, for the products, free of branches: with the items worked out in
 // every role and a wait before each slot's products, the kernel was 175 KB of code, every step of a role
 // cost some 200 cycles (the waits themselves were over at once), and a tile took 4,400 cycles.
@@ -47,12 +46,8 @@
 
 namespace csa {
 
-constexpr int LP_T = 640;
+constexpr int LP_T = 512;
 constexpr int LP_SOFT = 8;                                // softmax warps
-constexpr int LP_OUT = 4;                                 // output warps, behind them
-constexpr int LP_MMA = LP_SOFT + LP_OUT;                  // the warps of the other roles
-constexpr int LP_LOOKUP = LP_MMA + 1;
-constexpr int LP_LOAD = LP_LOOKUP + 1;
 constexpr int LP_PROD = 6;                                // loading warps
 constexpr int LP_SLOTS = 8;
 constexpr int LP_PAIRS = 76;                              // pairs of SMs: sizes the splits (and so the workspace)
@@ -64,15 +59,13 @@ constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
 constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
 constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
 constexpr uint32_t LP_PVDONE = LP_PREADY + 8, LP_VLAND = LP_PVDONE + 8, LP_ITEM = LP_VLAND + 8, LP_TAKEN = LP_ITEM + 32;
-constexpr uint32_t LP_SUMS = LP_TAKEN + 32, LP_OFREE = LP_SUMS + 16;
-static_assert(LP_OFREE + 8 <= LP_SM_BAR + 512, "barriers");
+static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
 constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
 constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits of the rows that are there
 constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row ids, or [8] units {page, row}, runs
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
-constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [2 items][256] row sums of the threads
-constexpr uint32_t LP_SM_ROWMAX = LP_SM_SUM + 2048;       // [2 items][64] the rows' maxima
-constexpr uint32_t LP_SM_ITEM = LP_SM_ROWMAX + 512;       // [4] items
+constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of the threads
+constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
 constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] plain or not (tile_plain)
 constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
@@ -358,11 +351,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         mbar_init(sb + LP_VLAND, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(sb + LP_ITEM + 8 * i, 1);
-            mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_OUT + LP_PROD + (rank == 0 ? 1 : 0));
+            mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_PROD + (rank == 0 ? 1 : 0));
         }
-        mbar_init(sb + LP_SUMS, LP_SOFT);  // of items in turn: the softmax may be an item ahead of the output
-        mbar_init(sb + LP_SUMS + 8, LP_SOFT);
-        mbar_init(sb + LP_OFREE, 2 * LP_OUT);  // the output warps of both CTAs
         *dead = 0;
         fence_mbar_init();
     }
@@ -386,11 +376,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     };
 
     if (warp < LP_SOFT) {
-        // ---------------------------------------------------------------- softmax
+        // ---------------------------------------------------------------- softmax and output
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int r = tid & 63, half = (warp >> 1) & 1, ch = warp >> 2;
         float* mx = reinterpret_cast<float*>(sm + LP_SM_MAX);
-        int done = 0;  // items with tiles so far
+        float* ls = reinterpret_cast<float*>(sm + LP_SM_SUM);
         while (next_item()) {
             const int row = x.row0 + (int)rank * 64 + r;  // this thread's query row
             const bool mine = (int)rank * 64 + r < x.nrows;
@@ -497,10 +487,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const float2 ss = f32x2_split(sum);
                 l_run = l_run * alpha + (ss.x + ss.y);
                 // P and O are free once the product before this one is done
-                if (g > 0) {
+                if (i > 0) {
                     ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
                     tc_fence_after();
-                    if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
                         for (int c = 128 * ch; c < 128 * ch + 128; c += 32) {
                             uint32_t o[32];
@@ -552,99 +542,56 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 __syncwarp();
                 if (lane == 0) mbar_arrive_rank(sb + LP_PREADY, 0);
             }
-            if (x.T > 0) {  // the row's sums and maximum, for the output warps
-                sidx += 8 * x.T;
-                reinterpret_cast<float*>(sm + LP_SM_SUM)[(done & 1) * 256 + tid] = l_run;
-                if (tid < 64) reinterpret_cast<float*>(sm + LP_SM_ROWMAX)[(done & 1) * 64 + tid] = m_run;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + LP_SUMS + 8 * (done & 1));
-                ++done;
-            }
-        }
-    } else if (warp < LP_MMA) {
-        // ---------------------------------------------------------------- output
-        // Warp w: rows [32 (w & 1), + 32) of the CTA, dims [256 (w >> 1), + 256), normalised.  Four lanes exchange
-        // their rows' sectors, so that a store covers 128 bytes of each of 8 rows: 1,524 cycles a 64 KB item,
-        // where a sector of each of 32 rows at a time takes 3,250 (the SM's path to the L2 takes 17 bytes
-        // a cycle of those, 43 of the former).
-        const int w = warp - LP_SOFT, r = (w & 1) * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(w * 32) << 16;
-        const bool direct = a.parts == 1;
-        while (next_item()) {
-            g += x.T;
-            float l = 0.f, m = -INFINITY;
             if (x.T > 0) {
-                ok = lat_wait(sb + LP_SUMS + 8 * (n & 1), (n >> 1) & 1, dead) && ok;
-                const float* ls = reinterpret_cast<const float*>(sm + LP_SM_SUM) + (n & 1) * 256 + r;
-                l = (ls[0] + ls[64]) + (ls[128] + ls[192]);
-                m = reinterpret_cast<const float*>(sm + LP_SM_ROWMAX)[(n & 1) * 64 + r];
-                ++n;
+                sidx += 8 * x.T;
+                ls[tid] = l_run;
                 ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
                 tc_fence_after();
+                named_bar_sync(1, 32 * LP_SOFT);
+                l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int row0 = (int)rank * 64 + (w & 1) * 32;  // the warp's first row of the item
+            // ---- row r of the CTA, dims [256 half + 128 ch, + 128): normalised and written a sector (32 bytes) at
+            //      a time (through shared memory, for whole lines, the round trips cost more than the lines gain:
+            //      4,070 cycles an item)
+            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const bool direct = a.parts == 1;
             if (direct || x.T > 0) {
-                const int64_t gr = x.row0 + row0 + (lane & ~3);
-                const int64_t pitch = direct ? D * 2 : D * 4;
-                uint8_t* dst = (direct ? reinterpret_cast<uint8_t*>(a.out + gr * D + (w >> 1) * 256)
-                                       : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr) * D + (w >> 1) * 256)) +
-                               (lane & 3) * 32;
-                const int left = x.nrows - row0 - (lane & ~3);  // rows of this group of four that there are
+                const int at = half * 256 + ch * 128;
+                uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out + (int64_t)row * D + at)
+                                      : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + row) * D + at);
 #pragma unroll 1
-                for (int c = 0; c < (direct ? 4 : 8); ++c) {
-                    uint32_t v[32];  // 128 bytes of this lane's row
-                    if (x.T == 0) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0;
-                    } else if (direct) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t o[32];
-                            tc_ld32(tmem + lane_off + 64 * c + 32 * h, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                v[16 * h + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                        }
-                    } else {
-                        tc_ld32(tmem + lane_off + 32 * c, v);
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t o[32];
+                    if (x.T > 0) {
+                        tc_ld32(tmem + lane_off + 128 * ch + c, o);
                         tc_wait_ld();
+                    } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
                     }
-                    // 4 x 4 transpose of sectors: lane j ends with sector j of rows 0 .. 3 of its group
+                    if (!mine) continue;
+                    if (direct) {
 #pragma unroll
-                    for (int s = 1; s < 4; s <<= 1) {
-                        const bool up = (lane & s) != 0;
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        store_sector(dst + c * 2, o, a.wide_out);
+                        store_sector(dst + c * 2 + 32, o + 8, a.wide_out);
+                    } else {
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            if (p & s) continue;
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t mine = up ? v[8 * p + e] : v[8 * (p | s) + e];
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, mine, s);
-                                if (up) v[8 * p + e] = got;
-                                else v[8 * (p | s) + e] = got;
-                            }
-                        }
+                        for (int e = 0; e < 4; ++e) store_sector(dst + c * 4 + 32 * e, o + 8 * e, true);
                     }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left) store_sector(dst + k * pitch + c * 128, v + 8 * k, a.wide_out || !direct);
                 }
                 tc_fence_before();
             }
-            __syncwarp();
-            if (x.T > 0 && lane == 0) mbar_arrive_rank(sb + LP_OFREE, 0);
-            if (w < 2 && row0 + lane < x.nrows) {
-                const int64_t row = x.row0 + row0 + lane;
-                const float e = l == 0.f ? -INFINITY : (m + log2f(l)) * LP_LN2;
+            if (tid < 64 && mine) {
+                const float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
                 if (!direct) a.part_lse[(int64_t)x.part * a.rows + row] = e;
                 else if (a.lse) a.lse[row] = e;
             }
         }
-    } else if (warp == LP_MMA && rank == 0) {
+    } else if (warp == LP_SOFT && rank == 0) {
         // ---------------------------------------------------------------- the products (one thread)
         if (elect_one()) {
             const uint64_t dk = sdesc_sw128(sb, 16, 1024), dv = sdesc_sw128(sb, 4096, 1024);
@@ -707,7 +654,6 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             if (ok) tc_commit_pair(sb + LP_VLAND);
                         }
                         if (!ready) ok = ok && lat_wait(sb + LP_PREADY, gt & 1, dead);
-                        if (i == 1 && n > 1) ok = ok && lat_wait(sb + LP_OFREE, n & 1, dead);  // the item before is written
                         tc_fence_after();
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
@@ -735,7 +681,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 g += T;
             }
         }
-    } else if (warp == LP_LOOKUP) {
+    } else if (warp == LP_SOFT + 1) {
         // ---------------------------------------------------------------- the tiles' pages, and Q
         const uint32_t qfull = mapa(sb + LP_QFULL, 0);
         uint32_t* plain = reinterpret_cast<uint32_t*>(sm + LP_SM_PLAIN);
@@ -809,10 +755,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
             }
         }
-    } else if (warp >= LP_LOAD) {
+    } else if (warp >= LP_SOFT + 2) {
         // ---------------------------------------------------------------- key rows
         const uint32_t full0 = mapa(sb + LP_FULL, 0);  // the even CTA's barriers
-        int turn = warp - LP_LOAD;               // slots until this warp's next one
+        int turn = warp - (LP_SOFT + 2);               // slots until this warp's next one
         auto claim = [&](uint32_t pair_bytes) -> bool {  // slot sidx: free, and both CTAs' bytes announced
             const int sl = sidx & (LP_SLOTS - 1);
             if (sidx >= LP_SLOTS && !lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)) return false;
