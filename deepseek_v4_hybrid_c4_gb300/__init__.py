@@ -158,10 +158,27 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_current_stream = None
+
+
+def _bind_current_stream():
+    """The current stream's handle as a function: the raw getter where torch has it (a Stream object
+    costs 3 us a call)."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:
+        device = torch.cuda.current_device
+        _current_stream = lambda: raw(device())  # noqa: E731
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _bind_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

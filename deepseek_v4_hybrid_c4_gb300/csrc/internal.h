@@ -41,6 +41,23 @@ inline csa_status check_paged(const csa_paged& p, int row_bytes) {
 int device_sm_count();
 cudaError_t set_func_attr_once(const void* func, cudaFuncAttribute attr, int value);
 
+// Launches a kernel that begins with griddepcontrol.wait, so that its launch and its prologue overlap
+// the end of the kernel before it in the stream (programmatic stream serialisation).
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+
 struct HWorkSet {          // HiSparse working set of a pool (see DWorkSet); table == nullptr: none
     const int32_t* table = nullptr;
     void* base = nullptr;

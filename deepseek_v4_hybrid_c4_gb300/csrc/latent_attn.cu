@@ -360,6 +360,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    pdl_wait();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LP_SM_TMEM);
     LatItem x;
     int sidx = 0, g = 0, n = 0, q = 0;  // ring slots, tiles, items with tiles and items so far
@@ -1042,6 +1043,7 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     if (!make_bf16_map(&qm, q, 2, qd, qs, qb)) return cudaErrorInvalidValue;
     const bool box = kv.rows_per_page % 16 == 0;
     for (int i = 0; i < 3; ++i) {
+        if (i > 0 && (!box || kv.rows_per_page < 16 << i)) break;  // no run of that many rows
         if (box) {  // a box never reaches behind its page: only runs of units are copied in larger ones
             const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
             const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
@@ -1059,19 +1061,9 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     cudaError_t e = set_func_attr_once((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LP_SMEM);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, sms / 2));
-    kernel<<<2 * pairs, LP_T, LP_SMEM, s>>>(qm, km, a);
-    e = cudaGetLastError();
+    e = launch_after(kernel, dim3(2 * pairs), LP_T, LP_SMEM, s, qm, km, a);
     if (e != cudaSuccess || a.parts == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)a.rows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, lat_merge_kernel, a);
+    return launch_after(lat_merge_kernel, dim3((unsigned)a.rows), 128, 0, s, a);
 }
 
 }  // namespace csa

@@ -3,8 +3,9 @@
 // physical pools, a page id standing for a page in every pool).
 //
 // refs[p] counts the table entries that name page p; a page is free where it is 0.  Every call that needs
-// free or used pages in order scans refs: a count per 4,096-page chunk, then each chunk's CTA adds the
-// counts before it to its own prefix sums and writes the pages' ranks and lists.  The lists make the
+// free or used pages in order scans refs in chunks of 4,096 pages: a chunk's CTA counts the pages in use before
+// it (up to 32,768 pages all of them by itself, beyond from counts that a kernel before it left), adds its own
+// prefix sums and writes the pages' ranks and lists.  The lists make the
 // results independent of timing: new pages are the lowest free ids, moved pages go in the order of
 // their ids.  Reference counts move by integer atomics, whose order does not show.
 #include "common.cuh"
@@ -63,6 +64,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
 // Pages of chunk blockIdx.x that are used (free: the rest).
 __global__ void __launch_bounds__(PG_T) pages_count_kernel(const int32_t* refs, int64_t n, int32_t* cnt) {
     __shared__ int64_t red[32];
+    pdl_wait();
     const int64_t base = (int64_t)blockIdx.x * PG_CHUNK;
     int c = 0;
 #pragma unroll
@@ -74,6 +76,9 @@ __global__ void __launch_bounds__(PG_T) pages_count_kernel(const int32_t* refs, 
     if (threadIdx.x == 0) cnt[blockIdx.x] = (int32_t)s;
     pdl_launch_dependents();
 }
+
+// Pools up to this size are counted by every scan CTA: a launch less (3 us), for up to 32 loads of a thread.
+constexpr int64_t kSelfCount = 8 * PG_CHUNK;
 
 // Ranks of chunk blockIdx.x.  COMPACT false: the free pages into list, hdr[0] = their number.
 // COMPACT true: U = used pages -> hdr[0]; used pages' ranks; free pages below U into hole; used pages of
@@ -88,10 +93,23 @@ __global__ void __launch_bounds__(PG_T) pages_scan_kernel(const int32_t* refs, i
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t chunks = gridDim.x, base = (int64_t)blockIdx.x * PG_CHUNK;
     int64_t before = 0, all = 0;  // used pages before this chunk, and in all
-    for (int64_t c = tid; c < chunks; c += PG_T) {
-        const int32_t x = w.cnt[c];
-        all += x;
-        if (c < (int64_t)blockIdx.x) before += x;
+    if (n <= kSelfCount) {
+        const int last = (int)n;
+        int b = 0, t = 0;
+#pragma unroll 8
+        for (int i = tid; i < last; i += PG_T) {
+            const int u = __ldcg(refs + i) > 0;
+            t += u;
+            if (i < (int)base) b += u;
+        }
+        before = b;
+        all = t;
+    } else {
+        for (int64_t c = tid; c < chunks; c += PG_T) {
+            const int32_t x = w.cnt[c];
+            all += x;
+            if (c < (int64_t)blockIdx.x) before += x;
+        }
     }
     before = block_sum(before, red);
     all = block_sum(all, red);
@@ -175,6 +193,7 @@ __global__ void __launch_bounds__(256) pages_alloc_kernel(int32_t* refs, int32_t
 // An entry gives its page back.  The exchange makes a row that is listed twice count once.
 __global__ void __launch_bounds__(256) pages_free_kernel(int32_t* refs, int64_t n_pages, int32_t* table, int64_t stride,
                                                          int B, const int32_t* rows, int32_t* status) {
+    pdl_wait();
     const int32_t b = rows[blockIdx.y];
     if (b < 0 || b >= B) {
         if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
@@ -317,6 +336,7 @@ __global__ void __launch_bounds__(256) pages_move_kernel(MoveArgs a) {
 
 __global__ void __launch_bounds__(256) pages_copy_kernel(PoolArgs a, const int32_t* src, const int32_t* dst, int n,
                                                          int32_t* status) {
+    pdl_wait();
     for (int k = blockIdx.x; k < n; k += gridDim.x) {
         const int32_t s = src[k], d = dst[k];
         if (s < 0 || d < 0 || s >= a.n_pages || d >= a.n_pages) {
@@ -359,29 +379,15 @@ static csa_status check_ws(const void* ws, size_t bytes, int64_t n_pages) {
     return ws && al16(ws) && bytes >= need ? CSA_OK : CSA_ERR_WORKSPACE;
 }
 
-// A launch that may start while the kernel before it in the stream ends (it waits for it by itself).
-template <typename... P, typename... A>
-static cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
-}
-
 static cudaError_t launch_scan(bool compact, const int32_t* refs, int32_t* refs_out, int64_t n, const PagesWs& w,
                                int64_t* n_used, cudaStream_t s) {
     const unsigned c = (unsigned)pages_chunks(n);
-    pages_count_kernel<<<c, PG_T, 0, s>>>(refs, n, w.cnt);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return compact ? launch_after(pages_scan_kernel<true>, dim3(c), PG_T, s, refs, refs_out, n, w, n_used)
-                   : launch_after(pages_scan_kernel<false>, dim3(c), PG_T, s, refs, refs_out, n, w, n_used);
+    if (n > kSelfCount) {
+        cudaError_t e = launch_after(pages_count_kernel, dim3(c), PG_T, 0, s, refs, n, w.cnt);
+        if (e != cudaSuccess) return e;
+    }
+    return compact ? launch_after(pages_scan_kernel<true>, dim3(c), PG_T, 0, s, refs, refs_out, n, w, n_used)
+                   : launch_after(pages_scan_kernel<false>, dim3(c), PG_T, 0, s, refs, refs_out, n, w, n_used);
 }
 
 }  // namespace csa
@@ -411,7 +417,7 @@ csa_status csa_pages_alloc(int32_t* refs, int64_t n_pages, int32_t* page_table, 
     const PagesWs w = pages_ws(workspace, n_pages, nullptr);
     cudaError_t e = launch_scan(false, refs, refs, n_pages, w, nullptr, s);
     if (e == cudaSuccess)
-        e = launch_after(pages_alloc_kernel, dim3(B), 256, s, refs, page_table, table_stride, B, first, count, w, st);
+        e = launch_after(pages_alloc_kernel, dim3(B), 256, 0, s, refs, page_table, table_stride, B, first, count, w, st);
     return from_cuda(e);
 }
 
@@ -426,9 +432,8 @@ csa_status csa_pages_free(int32_t* refs, int64_t n_pages, int32_t* page_table, i
     if (!st) return CSA_ERR_CUDA;
     int64_t x = (table_stride + 1023) / 1024;
     if (x > 64) x = 64;
-    pages_free_kernel<<<dim3((unsigned)x, (unsigned)R), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        refs, n_pages, page_table, table_stride, B, rows, st);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(launch_after(pages_free_kernel, dim3((unsigned)x, (unsigned)R), 256, 0,
+                                  static_cast<cudaStream_t>(stream), refs, n_pages, page_table, table_stride, B, rows, st));
 }
 
 csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* page_table, int64_t table_stride,
@@ -461,7 +466,7 @@ csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* p
     int64_t x = (table_stride + 1023) / 1024;
     if (x < 8) x = 8;
     if (x > 64) x = 64;
-    if (e == cudaSuccess) e = launch_after(pages_fork_kernel, dim3((unsigned)x, (unsigned)F), 256, s, a);
+    if (e == cudaSuccess) e = launch_after(pages_fork_kernel, dim3((unsigned)x, (unsigned)F), 256, 0, s, a);
     return from_cuda(e);
 }
 
@@ -487,7 +492,7 @@ csa_status csa_pages_compact(const csa_page_pools* pools, const int32_t* refs, i
     a.status = st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_scan(true, refs, refs_out, pools->n_pages, a.w, n_used, s);
-    if (e == cudaSuccess) e = launch_after(pages_move_kernel, dim3((unsigned)sms * 8), 256, s, a);
+    if (e == cudaSuccess) e = launch_after(pages_move_kernel, dim3((unsigned)sms * 8), 256, 0, s, a);
     return from_cuda(e);
 }
 
@@ -502,8 +507,7 @@ csa_status csa_pages_copy(const csa_page_pools* pools, const int32_t* src, const
     const int sms = device_sm_count();
     if (!st || !sms) return CSA_ERR_CUDA;
     const int g = n < sms * 8 ? n : sms * 8;
-    pages_copy_kernel<<<g, 256, 0, static_cast<cudaStream_t>(stream)>>>(a, src, dst, n, st);
-    return from_cuda(cudaGetLastError());
+    return from_cuda(launch_after(pages_copy_kernel, dim3(g), 256, 0, static_cast<cudaStream_t>(stream), a, src, dst, n, st));
 }
 
 }  // extern "C"
