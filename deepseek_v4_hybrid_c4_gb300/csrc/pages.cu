@@ -8,6 +8,8 @@
 // prefix sums and writes the pages' ranks and lists.  The lists make the
 // results independent of timing: new pages are the lowest free ids, moved pages go in the order of
 // their ids.  Reference counts move by integer atomics, whose order does not show.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -50,30 +52,40 @@ static PagesWs pages_ws(void* ws, int64_t n_pages, size_t* total) {
     return w;
 }
 
-// Sum of v over the CTA's warps, to every thread.  red: 32 words of shared memory.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
-    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
+// Sums of a and b over the CTA's warps, to every thread.  red: 2 x 32 words of shared memory.
+__device__ __forceinline__ void block_sum2(int& a, int& b, int32_t* red) {
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_down_sync(0xffffffffu, a, o);
+        b += __shfl_down_sync(0xffffffffu, b, o);
+    }
+    const int lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    if (lane == 0) {
+        red[threadIdx.x >> 5] = a;
+        red[32 + (threadIdx.x >> 5)] = b;
+    }
     __syncthreads();
-    int64_t s = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[w];
-    return s;
+    a = lane < warps ? red[lane] : 0;
+    b = lane < warps ? red[32 + lane] : 0;
+    for (int o = 16; o; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
 }
 
 // Pages of chunk blockIdx.x that are used (free: the rest).
 __global__ void __launch_bounds__(PG_T) pages_count_kernel(const int32_t* refs, int64_t n, int32_t* cnt) {
-    __shared__ int64_t red[32];
+    __shared__ int32_t red[64];
     pdl_wait();
     const int64_t base = (int64_t)blockIdx.x * PG_CHUNK;
-    int c = 0;
+    int c = 0, none = 0;
 #pragma unroll
     for (int v = 0; v < PG_V; ++v) {
         const int64_t i = base + v * PG_T + threadIdx.x;
         if (i < n) c += refs[i] > 0;
     }
-    const int64_t s = block_sum(c, red);
-    if (threadIdx.x == 0) cnt[blockIdx.x] = (int32_t)s;
+    block_sum2(c, none, red);
+    if (threadIdx.x == 0) cnt[blockIdx.x] = c;
     pdl_launch_dependents();
 }
 
@@ -86,58 +98,71 @@ constexpr int64_t kSelfCount = 8 * PG_CHUNK;
 template <bool COMPACT>
 __global__ void __launch_bounds__(PG_T) pages_scan_kernel(const int32_t* refs, int32_t* refs_out, int64_t n, PagesWs w,
                                                           int64_t* n_used) {
-    __shared__ int64_t red[32];
-    __shared__ int32_t wsum[PG_V][32];
+    __shared__ int32_t red[64];
+    __shared__ int32_t wsum[PG_V * 32];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t chunks = gridDim.x, base = (int64_t)blockIdx.x * PG_CHUNK;
-    int64_t before = 0, all = 0;  // used pages before this chunk, and in all
-    if (n <= kSelfCount) {
-        const int last = (int)n;
-        int b = 0, t = 0;
-#pragma unroll 8
-        for (int i = tid; i < last; i += PG_T) {
-            const int u = __ldcg(refs + i) > 0;
-            t += u;
-            if (i < (int)base) b += u;
-        }
-        before = b;
-        all = t;
-    } else {
-        for (int64_t c = tid; c < chunks; c += PG_T) {
-            const int32_t x = w.cnt[c];
-            all += x;
-            if (c < (int64_t)blockIdx.x) before += x;
-        }
-    }
-    before = block_sum(before, red);
-    all = block_sum(all, red);
+    const int chunks = (int)gridDim.x;
+    const int64_t base = (int64_t)blockIdx.x * PG_CHUNK;
+    // this thread's pages: base + 1024 v + tid; pre: used ones before it in its warp
     int32_t r[PG_V];
     int pre[PG_V];
 #pragma unroll
     for (int v = 0; v < PG_V; ++v) {
         const int64_t i = base + v * PG_T + tid;
-        r[v] = i < n ? refs[i] : 0;
-        const unsigned m = __ballot_sync(0xffffffffu, r[v] > 0);
-        pre[v] = __popc(m & ((1u << lane) - 1u));
-        if (lane == 0) wsum[v][warp] = __popc(m);
+        r[v] = i < n ? __ldcg(refs + i) : 0;
     }
-    __syncthreads();
-    int64_t at = before;  // used pages before thread 0's page of round v
+    int before = 0, all = 0;  // used pages before this chunk, and in all
+    if (n <= kSelfCount) {
+        const int last = (int)n;
+#pragma unroll 8
+        for (int i = tid; i < last; i += PG_T) {
+            const int u = __ldcg(refs + i) > 0;
+            all += u;
+            if (i < (int)base) before += u;
+        }
+    } else {
+        for (int c = tid; c < chunks; c += PG_T) {
+            const int32_t x = w.cnt[c];
+            all += x;
+            if (c < (int)blockIdx.x) before += x;
+        }
+    }
 #pragma unroll
     for (int v = 0; v < PG_V; ++v) {
-        int low = 0, tot = 0;
-        for (int x = 0; x < PG_T / 32; ++x) {
-            const int s = wsum[v][x];
-            tot += s;
-            if (x < warp) low += s;
+        const unsigned m = __ballot_sync(0xffffffffu, r[v] > 0);
+        pre[v] = __popc(m & ((1u << lane) - 1u));
+        if (lane == 0) wsum[v * 32 + warp] = __popc(m);
+    }
+    block_sum2(before, all, red);  // (its barriers publish wsum)
+    if (warp == 0) {  // exclusive prefix over the 128 (round, warp) counts, four a lane
+        int c[4], t = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            c[e] = wsum[lane * 4 + e];
+            t += c[e];
         }
+        int x = t;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        x -= t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            wsum[lane * 4 + e] = x;
+            x += c[e];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < PG_V; ++v) {
         const int64_t i = base + v * PG_T + tid;
-        const int64_t rk = at + low + pre[v];  // used pages of smaller id
+        const int rk = before + wsum[v * 32 + warp] + pre[v];  // used pages of smaller id
         if (i < n) {
             if (COMPACT) {
-                w.rank[i] = r[v] > 0 ? (int32_t)rk : -1;
+                w.rank[i] = r[v] > 0 ? rk : -1;
                 if (r[v] > 0 && i >= all) w.list[rk] = (int32_t)i;
                 if (r[v] <= 0 && i < all) w.hole[i - rk] = (int32_t)i;
                 if (i == all) w.hdr[1] = rk;
@@ -146,7 +171,6 @@ __global__ void __launch_bounds__(PG_T) pages_scan_kernel(const int32_t* refs, i
                 w.list[i - rk] = (int32_t)i;
             }
         }
-        at += tot;
     }
     if (blockIdx.x == 0 && tid == 0) {
         w.hdr[0] = COMPACT ? all : n - all;
@@ -161,17 +185,21 @@ __global__ void __launch_bounds__(PG_T) pages_scan_kernel(const int32_t* refs, i
 __global__ void __launch_bounds__(256) pages_alloc_kernel(int32_t* refs, int32_t* table, int64_t stride, int B,
                                                           const int32_t* first, const int32_t* count, PagesWs w,
                                                           int32_t* status) {
-    __shared__ int64_t red[32];
+    __shared__ int32_t red[64];
     pdl_wait();
     const int b = blockIdx.x;
     auto valid = [&](int g) {
         const int64_t f = first[g], c = count[g];
         return f >= 0 && c >= 0 && f + c <= stride;
     };
+    // entries of the requests before: in halves, as up to 4,096 rows of 2^31 - 1 entries do not fit 32 bits
     int64_t s = 0;
     for (int g = threadIdx.x; g < b; g += blockDim.x)
         if (valid(g)) s += count[g];
-    s = block_sum(s, red);
+    int lo = (int)(s & 0xFFFFF), mid = (int)((s >> 20) & 0xFFFFF), hi = (int)(s >> 40), none = 0;
+    block_sum2(lo, mid, red);
+    block_sum2(hi, none, red);
+    s = (int64_t)lo + ((int64_t)mid << 20) + ((int64_t)hi << 40);
     if (!valid(b)) {
         if (threadIdx.x == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
         return;
@@ -213,12 +241,31 @@ __global__ void __launch_bounds__(256) pages_free_kernel(int32_t* refs, int64_t 
     }
 }
 
-// 16-byte chunks t, t + n, ... of page src copied to page dst, the pools laid end to end.
-__device__ __forceinline__ void copy_page(const PoolArgs& a, int64_t src, int64_t dst, int64_t t, int64_t n) {
-    for (int p = 0; p < a.n_pools; ++p) {
-        const uint4* s = reinterpret_cast<const uint4*>(a.base[p] + src * a.stride[p]);
-        uint4* d = reinterpret_cast<uint4*>(a.base[p] + dst * a.stride[p]);
-        for (int64_t i = t; i < a.bytes[p] / 16; i += n) d[i] = s[i];
+// A page is copied in pieces of 8 KB (of one pool; the last one of a pool may be shorter), each by a CTA
+// of 256 threads with two 16-byte loads in flight per thread.
+constexpr int PG_PIECE = 512;  // in 16 bytes
+static int pieces_of(const PoolArgs& a) {
+    int64_t n = 0;
+    for (int p = 0; p < a.n_pools; ++p) n += (a.bytes[p] / 16 + PG_PIECE - 1) / PG_PIECE;
+    return n > 0x7FFFFFFF ? 0x7FFFFFFF : (int)n;
+}
+__device__ __forceinline__ void copy_piece(const PoolArgs& a, int64_t src, int64_t dst, int64_t piece) {
+#pragma unroll
+    for (int p = 0; p < CSA_POOLS_MAX; ++p) {
+        if (p >= a.n_pools) return;
+        const int64_t n16 = a.bytes[p] / 16, n = (n16 + PG_PIECE - 1) / PG_PIECE;
+        if (piece < n) {
+            const int64_t i = piece * PG_PIECE + threadIdx.x;
+            const uint4* s = reinterpret_cast<const uint4*>(a.base[p] + src * a.stride[p]) + i;
+            uint4* d = reinterpret_cast<uint4*>(a.base[p] + dst * a.stride[p]) + i;
+            uint4 v0, v1;
+            if (i < n16) v0 = __ldcs(s);
+            if (i + 256 < n16) v1 = __ldcs(s + 256);
+            if (i < n16) __stcs(d, v0);
+            if (i + 256 < n16) __stcs(d + 256, v1);
+            return;
+        }
+        piece -= n;
     }
 }
 
@@ -228,7 +275,7 @@ struct ForkArgs {
     int32_t* refs;
     int32_t* table;
     int64_t stride;
-    int B, F, rpp;
+    int B, F, rpp, pieces;
     const int32_t* src;
     const int32_t* dst;
     int64_t* n_tokens;
@@ -237,7 +284,7 @@ struct ForkArgs {
 };
 
 __global__ void __launch_bounds__(256) pages_fork_kernel(ForkArgs a) {
-    __shared__ int64_t red[32];
+    __shared__ int32_t red[64];
     pdl_wait();
     const int f = blockIdx.y, tid = threadIdx.x;
     const bool lead = blockIdx.x == 0 && tid == 0;
@@ -251,14 +298,13 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(ForkArgs a) {
         return p >= 0 && p < a.pools.n_pages ? p : -1;
     };
     const int32_t b = a.src[f], d = a.dst[f];
-    int64_t clash = 0, before = 0;
+    int clash = 0, before = 0;
     for (int g = tid; g < a.F; g += blockDim.x) {
         clash += d == a.src[g] || (g != f && d == a.dst[g]);
         int64_t n;
         if (g < f && last_page(g, &n) >= 0) ++before;
     }
-    clash = block_sum(clash, red);
-    before = block_sum(before, red);
+    block_sum2(clash, before, red);
     int64_t n = -1;
     const int64_t last = last_page(f, &n);
     if (b < 0 || b >= a.B || d < 0 || d >= a.B || clash || n < 0 || (n + a.rpp - 1) / a.rpp > a.stride) {
@@ -279,7 +325,8 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(ForkArgs a) {
         if (part && last < 0 && a.table[b * a.stride + full] >= 0) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
     }
     const int64_t t = (int64_t)blockIdx.x * blockDim.x + tid, nt = (int64_t)gridDim.x * blockDim.x;
-    if (fresh >= 0) copy_page(a.pools, last, fresh, t, nt);
+    if (fresh >= 0)
+        for (int p = blockIdx.x; p < a.pieces; p += gridDim.x) copy_piece(a.pools, last, fresh, p);
     const int32_t* from = a.table + b * a.stride;
     int32_t* to = a.table + d * a.stride;
     for (int64_t j = t; j < a.stride; j += nt) {
@@ -307,6 +354,7 @@ struct MoveArgs {
     int32_t* table_out;
     int64_t entries;
     PagesWs w;
+    int pieces;
     int32_t* status;
 };
 
@@ -330,20 +378,23 @@ __global__ void __launch_bounds__(256) pages_move_kernel(MoveArgs a) {
         }
         a.table_out[e] = p;
     }
-    for (int64_t k = blockIdx.x; k < moves; k += gridDim.x)
-        copy_page(a.pools, a.w.list[low + k], a.w.hole[k], threadIdx.x, blockDim.x);
+    for (int64_t u = blockIdx.x; u < moves * a.pieces; u += gridDim.x) {
+        const int64_t k = u / a.pieces;
+        copy_piece(a.pools, a.w.list[low + k], a.w.hole[k], u - k * a.pieces);
+    }
 }
 
-__global__ void __launch_bounds__(256) pages_copy_kernel(PoolArgs a, const int32_t* src, const int32_t* dst, int n,
-                                                         int32_t* status) {
+__global__ void __launch_bounds__(256) pages_copy_kernel(PoolArgs a, int pieces, const int32_t* src, const int32_t* dst,
+                                                         int n, int32_t* status) {
     pdl_wait();
-    for (int k = blockIdx.x; k < n; k += gridDim.x) {
+    for (int64_t u = blockIdx.x; u < (int64_t)n * pieces; u += gridDim.x) {
+        const int64_t k = u / pieces;
         const int32_t s = src[k], d = dst[k];
         if (s < 0 || d < 0 || s >= a.n_pages || d >= a.n_pages) {
             if (threadIdx.x == 0) raise_status(status, CSA_ERR_DEVICE_BOUNDS);
             continue;
         }
-        copy_page(a, s, d, threadIdx.x, blockDim.x);
+        copy_piece(a, s, d, u - k * pieces);
     }
 }
 
@@ -460,11 +511,12 @@ csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* p
     a.dst = dst;
     a.n_tokens = n_tokens;
     a.w = pages_ws(workspace, pools->n_pages, nullptr);
+    a.pieces = pieces_of(a.pools);
     a.status = st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_scan(false, refs, refs, pools->n_pages, a.w, nullptr, s);
-    int64_t x = (table_stride + 1023) / 1024;
-    if (x < 8) x = 8;
+    // CTAs of a child: one for each 1,024 entries of its row, and one for each piece of its page's copy
+    int64_t x = std::max<int64_t>((table_stride + 1023) / 1024, a.pieces);
     if (x > 64) x = 64;
     if (e == cudaSuccess) e = launch_after(pages_fork_kernel, dim3((unsigned)x, (unsigned)F), 256, 0, s, a);
     return from_cuda(e);
@@ -489,6 +541,7 @@ csa_status csa_pages_compact(const csa_page_pools* pools, const int32_t* refs, i
     a.table_out = page_table_out;
     a.entries = table_stride * B;
     a.w = pages_ws(workspace, pools->n_pages, nullptr);
+    a.pieces = pieces_of(a.pools);
     a.status = st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = launch_scan(true, refs, refs_out, pools->n_pages, a.w, n_used, s);
@@ -506,8 +559,10 @@ csa_status csa_pages_copy(const csa_page_pools* pools, const int32_t* src, const
     int32_t* st = device_status_ptr();
     const int sms = device_sm_count();
     if (!st || !sms) return CSA_ERR_CUDA;
-    const int g = n < sms * 8 ? n : sms * 8;
-    return from_cuda(launch_after(pages_copy_kernel, dim3(g), 256, 0, static_cast<cudaStream_t>(stream), a, src, dst, n, st));
+    const int pieces = pieces_of(a);
+    const int64_t g = std::min<int64_t>((int64_t)n * pieces, (int64_t)sms * 8);
+    return from_cuda(launch_after(pages_copy_kernel, dim3((unsigned)g), 256, 0, static_cast<cudaStream_t>(stream), a, pieces,
+                                  src, dst, n, st));
 }
 
 }  // extern "C"
