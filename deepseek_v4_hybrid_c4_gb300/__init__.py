@@ -229,11 +229,9 @@ def _scratch(nbytes: int, like):
     return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device if hasattr(like, "device") else "cuda")
 
 
-def _workspace(workspace, ws_bytes: int, need: int, like, stream):
-    """The caller's workspace, or a scratch tensor of `need` bytes that stays allocated until the work on
-    `stream` that uses it is done."""
-    if workspace is not None:
-        return workspace, ws_bytes
+def _workspace(need: int, like, stream):
+    """A scratch tensor of `need` bytes that stays allocated until the work on `stream` that uses it is
+    done, and its size."""
     ws = _scratch(need, like)
     if stream is not None and ws.is_cuda:
         import torch
@@ -313,7 +311,7 @@ def csa_prefix_attn(q, B: int, H: int, scale: float, kv: csa_paged, page_table_s
     """One token per request over a batch whose requests share their first n_shared rows (kv: the pool
     with the [B, page_table_stride] table).  workspace None: a scratch tensor is allocated."""
     if workspace is None:
-        workspace, ws_bytes = _workspace(None, 0, csa_prefix_attn_workspace_size(B, H, n_shared, max_rows), q, stream)
+        workspace, ws_bytes = _workspace(csa_prefix_attn_workspace_size(B, H, n_shared, max_rows), q, stream)
     _check(lib().csa_prefix_attn(_ptr(q), B, H, scale, kv, page_table_stride, n_shared, _ptr(n_rows), max_rows,
                                  _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), "csa_prefix_attn")
 
@@ -329,7 +327,7 @@ def csa_window_attn(q, H: int, scale: float, kv_raw: csa_paged, page_table_strid
     workspace None: a scratch tensor is allocated."""
     if workspace is None:
         need = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink)
-        workspace, ws_bytes = _workspace(None, 0, need, q, stream)
+        workspace, ws_bytes = _workspace(need, q, stream)
     _check(lib().csa_window_attn(_ptr(q), H, scale, kv_raw, page_table_stride, B, _ptr(q_offsets), _ptr(n_tokens),
                                  total_q, max_q, window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
                                  _stream(stream)), "csa_window_attn")
@@ -358,9 +356,10 @@ def csa_pages_workspace_size(n_pages: int) -> int:
 
 def csa_pages_alloc(refs, n_pages: int, page_table, table_stride: int, B: int, first, count, workspace=None,
                     ws_bytes: int = 0, stream=None) -> None:
-    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(n_pages), refs, stream)
+    if workspace is None:
+        workspace, ws_bytes = _workspace(csa_pages_workspace_size(n_pages), refs, stream)
     _check(lib().csa_pages_alloc(_ptr(refs), n_pages, _ptr(page_table), table_stride, B, _ptr(first), _ptr(count),
-                                 _ptr(ws), ws_bytes, _stream(stream)), "csa_pages_alloc")
+                                 _ptr(workspace), ws_bytes, _stream(stream)), "csa_pages_alloc")
 
 
 def csa_pages_free(refs, n_pages: int, page_table, table_stride: int, B: int, rows, R: int, stream=None) -> None:
@@ -370,17 +369,19 @@ def csa_pages_free(refs, n_pages: int, page_table, table_stride: int, B: int, ro
 
 def csa_pages_fork(pools: csa_page_pools, refs, page_table, table_stride: int, B: int, src, dst, F: int, n_tokens,
                    rows_per_page: int, workspace=None, ws_bytes: int = 0, stream=None) -> None:
-    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(pools.n_pages), refs, stream)
+    if workspace is None:
+        workspace, ws_bytes = _workspace(csa_pages_workspace_size(pools.n_pages), refs, stream)
     _check(lib().csa_pages_fork(ctypes.byref(pools), _ptr(refs), _ptr(page_table), table_stride, B, _ptr(src),
-                                _ptr(dst), F, _ptr(n_tokens), rows_per_page, _ptr(ws), ws_bytes, _stream(stream)),
+                                _ptr(dst), F, _ptr(n_tokens), rows_per_page, _ptr(workspace), ws_bytes, _stream(stream)),
            "csa_pages_fork")
 
 
 def csa_pages_compact(pools: csa_page_pools, refs, refs_out, page_table, page_table_out, table_stride: int, B: int,
                       n_used=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
-    ws, ws_bytes = _workspace(workspace, ws_bytes, csa_pages_workspace_size(pools.n_pages), refs, stream)
+    if workspace is None:
+        workspace, ws_bytes = _workspace(csa_pages_workspace_size(pools.n_pages), refs, stream)
     _check(lib().csa_pages_compact(ctypes.byref(pools), _ptr(refs), _ptr(refs_out), _ptr(page_table),
-                                   _ptr(page_table_out), table_stride, B, _ptr(n_used), _ptr(ws), ws_bytes,
+                                   _ptr(page_table_out), table_stride, B, _ptr(n_used), _ptr(workspace), ws_bytes,
                                    _stream(stream)), "csa_pages_compact")
 
 
