@@ -551,38 +551,60 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 named_bar_sync(1, 32 * LP_SOFT);
                 l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
             }
-            // ---- row r of the CTA, dims [256 half + 128 ch, + 128): normalised and written a sector (32 bytes) at
-            //      a time (through shared memory, for whole lines, the round trips cost more than the lines gain:
-            //      4,070 cycles an item)
+            // ---- row r of the CTA, dims [256 half + 128 ch, + 128), normalised.  Four lanes exchange their rows'
+            //      sectors, so that a store covers 128 bytes of each of 8 rows: an SM's stores leave at 43 bytes a
+            //      cycle so, and at 17 with a sector of each of 32 rows (a 64 KB item: 1,520 and 3,250 cycles).
             const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
             const bool direct = a.parts == 1;
             if (direct || x.T > 0) {
-                const int at = half * 256 + ch * 128;
-                uint8_t* dst = direct ? reinterpret_cast<uint8_t*>(a.out + (int64_t)row * D + at)
-                                      : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + row) * D + at);
+                const int at = half * 256 + ch * 128, j = lane & 3;
+                const int64_t gr = row - j;  // the group's first row
+                const int left = x.nrows - ((int)rank * 64 + r - j);
+                uint8_t* dst = (direct ? reinterpret_cast<uint8_t*>(a.out + gr * D + at)
+                                       : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr) * D + at)) +
+                               j * 32;
+                const int64_t pitch = direct ? D * 2 : D * 4;
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t o[32];
-                    if (x.T > 0) {
-                        tc_ld32(tmem + lane_off + 128 * ch + c, o);
+                for (int c = 0; c < (direct ? 2 : 4); ++c) {
+                    uint32_t v[32];  // 128 bytes of this lane's row
+                    if (x.T == 0) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0;
+                    } else if (direct) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t o[32];
+                            tc_ld32(tmem + lane_off + 128 * ch + 64 * c + 32 * h, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                v[16 * h + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        }
+                    } else {
+                        tc_ld32(tmem + lane_off + 128 * ch + 32 * c, v);
                         tc_wait_ld();
-                    } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
                     }
-                    if (!mine) continue;
-                    if (direct) {
+                    // 4 x 4 transpose of sectors: lane j of a group ends with sector j of the group's rows 0 .. 3
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                        store_sector(dst + c * 2, o, a.wide_out);
-                        store_sector(dst + c * 2 + 32, o + 8, a.wide_out);
-                    } else {
+                    for (int s = 1; s < 4; s <<= 1) {
+                        const bool up = (lane & s) != 0;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+                        for (int p = 0; p < 4; ++p) {
+                            if (p & s) continue;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) store_sector(dst + c * 4 + 32 * e, o + 8 * e, true);
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t give = up ? v[8 * p + e] : v[8 * (p | s) + e];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
+                                if (up) v[8 * p + e] = got;
+                                else v[8 * (p | s) + e] = got;
+                            }
+                        }
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left) store_sector(dst + k * pitch + c * 128, v + 8 * k, a.wide_out || !direct);
                 }
                 tc_fence_before();
             }
