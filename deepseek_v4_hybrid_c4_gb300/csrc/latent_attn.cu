@@ -325,8 +325,8 @@ template <bool BOX>
 __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps& km, const LatArgs& a) {
     extern __shared__ uint8_t lp_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lp_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sb = smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sb = (smem_u32(lp_raw) + 1023u) & ~1023u;  // (the same address, without a detour over generic ones)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(sm + LP_SM_DEAD);
@@ -334,6 +334,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     if (warp == 0) {
         tmem_alloc_pair(sb + LP_SM_TMEM, 512);
         tmem_relinquish_pair();
+    }
+    if (tid == 64) {
+        prefetch_tensormap(&qmap);
+        for (int i = 0; i < (BOX ? 3 : 1); ++i) prefetch_tensormap(&km.m[i]);
     }
     if (tid == 32) {
         for (int i = 0; i < LP_SLOTS; ++i) {
@@ -361,7 +365,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     cluster_sync();
     tc_fence_after();
     pdl_wait();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + LP_SM_TMEM);
+    const uint32_t tmem = 0;  // an allocation of all 512 columns
     LatItem x;
     int sidx = 0, g = 0, n = 0, q = 0;  // ring slots, tiles, items with tiles and items so far
     bool ok = true;
@@ -720,6 +724,17 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             __syncwarp();
             if (!there) break;
             const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
+            auto load_q = [&](int k) {
+                if (k > 0) ok = lat_wait(sb + LP_QEMPTY, (k - 1) & 1, dead) && ok;
+                if (ok && lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        tma_load_2d_pair(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, qfull);
+                }
+                __syncwarp();
+            };
+            if (x.T > 0 && n == 0) load_q(0);
             for (int i = 0; ok && i < x.T; ++i, ++g) {
                 const int u0 = (x.t0 + i) * 8, slot = g & 7;
                 // the tile's place in the ring: read by the loading warps eight tiles ago, and no further than
@@ -765,17 +780,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     plain[slot] = tile_plain(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u;
                     mbar_arrive(sb + LP_LOOK + 8 * slot);
                 }
-                if (i == 0) {  // Q, behind the first tile's lookups
-                    if (n > 0) ok = lat_wait(sb + LP_QEMPTY, (n - 1) & 1, dead) && ok;
-                    ++n;
-                    if (ok && lane == 0) {
-                        if (rank == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
-#pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            tma_load_2d_pair(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, qfull);
-                    }
-                    __syncwarp();
-                }
+                if (i == 0 && n > 0) load_q(n);  // behind the first tile's lookups, as it may have to wait
+                if (i == 0) ++n;
             }
         }
     } else if (warp >= LP_SOFT + 2) {
@@ -997,29 +1003,40 @@ static void set_scale(LatArgs& a, float scale) {
     a.negate = scale < 0.f ? 1u << 13 : 0u;
 }
 
-// Splits of the shared rows: the number that ends the row tiles soonest on LP_PAIRS pairs, where an
-// item costs its tiles of 128 keys and about three more (its Q, its first and last product, its output).
-static int plan_splits(int row_tiles, int tiles) {
-    int best = 1;
-    double cost = 1e30;
-    for (int s = 1; s <= tiles && s <= LP_PAIRS; ++s) {
-        const int waves = (row_tiles * s + LP_PAIRS - 1) / LP_PAIRS;
-        const double c = (double)waves * ((tiles + s - 1) / s + 3) + 0.05 * s;
-        if (c < cost) cost = c, best = s;
+// How long the slowest of LP_PAIRS pairs takes, in tiles of 128 keys, for n1 items of t1 tiles and n2 of t2 behind
+// them, dealt out in turn; an item costs about three tiles more (its Q, its first and last product, its output).
+static int64_t deal_cost(int64_t n1, int64_t t1, int64_t n2, int64_t t2) {
+    const int64_t P = LP_PAIRS, c1 = t1 + 3, c2 = t2 + 3;
+    int64_t worst = 0;
+    // pairs differ by whether they get one more of the first kind, and one more in all
+    const int64_t edges[3] = {0, n1 % P, (n1 + n2) % P};
+    for (int64_t p : edges) {
+        const int64_t a = n1 / P + (p < n1 % P), all = (n1 + n2) / P + (p < (n1 + n2) % P);
+        worst = std::max(worst, a * c1 + (all - a) * c2);
     }
-    return best;
+    return worst;
 }
 
+// The splits of the shared rows (SP) and of a request's own (OS) that end soonest; a partial result of every
+// row, written and read again, costs about 1.4 tiles for each 4,096 rows.
 static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArgs* a) {
     a->rows = B * H;
     a->RT = (a->rows + 127) / 128;
     const int tiles = (int)((n_shared + 127) / 128);
-    a->SP = tiles > 0 ? plan_splits(a->RT, tiles) : 0;
     const int own = max_rows > n_shared ? (int)((max_rows + 15) / 16 - n_shared / 16 + 7) / 8 : 0;
+    a->SP = 0;
     a->OS = 0;
-    if (own > 0) {  // a request's own rows in pieces no longer than the shared ones, or than fill the device
-        const int per = a->SP > 0 ? std::max(4, (tiles + a->SP - 1) / a->SP) : std::max(2, (own * B + LP_PAIRS - 1) / LP_PAIRS);
-        a->OS = std::min((own + per - 1) / per, std::max(1, 4 * LP_PAIRS / B));
+    double best = 1e30;
+    const int os_most = own ? std::min(own, std::max(1, 4 * LP_PAIRS / B)) : 0;
+    const int sp_most = std::min(tiles, LP_PAIRS);
+    for (int sp = std::min(1, tiles); sp <= sp_most; ++sp) {
+        // a request's own rows: whole, or in pieces as long as the shared ones
+        const int piece = sp ? std::max(4, (tiles + sp - 1) / sp) : std::max(2, (own * B + LP_PAIRS - 1) / LP_PAIRS);
+        const int os = own ? std::min((own + piece - 1) / piece, os_most) : 0;
+        const double c = (double)deal_cost((int64_t)a->RT * sp, sp ? (tiles + sp - 1) / sp : 0, (int64_t)B * os,
+                                           os ? (own + os - 1) / os : 0) +
+                         (sp + os > 1 ? 1.4 * (sp + os) * a->rows / 4096.0 + 0.02 * (sp + os) : 0.0);
+        if (c < best) best = c, a->SP = sp, a->OS = os;
     }
     if (a->SP + a->OS == 0) a->OS = 1;  // no rows at all: every request is empty
     a->parts = a->SP + a->OS;

@@ -81,6 +81,9 @@ CSA_DEV void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+CSA_DEV void prefetch_tensormap(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // Tensor copies of one CTA of a pair (cta_group::2) into its own shared memory; bar may be an
 // mbarrier of either CTA of the pair, as a shared::cluster address.  2-D and 3-D boxes, and a gather of
 // four rows (a tensor map whose box is one row high) written one behind the other; row ids have no
