@@ -26,7 +26,8 @@
 // dims; empty ones in a short tile).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
 // Key rows are copied by TMA in the products' swizzle: where 16 rows always share a page (rows_per_page a
 // multiple of 16) in boxes of 64, 32 or 16 rows, as many as lie one behind the other in their page (issuing
-// a copy costs a warp some 60 cycles whatever its size); otherwise in four-row gathers.  The list of
+// a copy costs a warp some 60 cycles whatever its size); otherwise in boxes of 16 rows where a unit's rows lie one
+// behind the other, and in four-row gathers where they do not.  The list of
 // key rows is made of 16-row units; rows of a unit that no query sees are masked.
 //
 // Softmax: a thread holds one row's logits of a quarter of a tile; the row's four threads exchange their
@@ -66,7 +67,8 @@ constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row 
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
 constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of the threads
 constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
-constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] plain or not (tile_plain)
+constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] bit 0: plain (tile_plain); bit 8 + u: unit u's
+                                                          // rows lie one behind the other (gathers)
 constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr float LP_LOG2E = 1.4426950408889634f;
@@ -316,7 +318,8 @@ __device__ __forceinline__ int lat_page(const LatArgs& a, const int32_t* pt, int
     return pp;
 }
 
-// The cache's tensor maps: [0] boxes of 16 rows x 64 dims (or of one row, for gathers), [1] of 32, [2] of 64.
+// The cache's tensor maps: boxes of 64 dims and [0] 16, [1] 32, [2] 64 rows of a page, or, over all rows of the
+// pool, [0] one row (gathers) and [1] 16 rows.
 struct KeyMaps {
     CUtensorMap m[3];
 };
@@ -337,7 +340,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     }
     if (tid == 64) {
         prefetch_tensormap(&qmap);
-        for (int i = 0; i < (BOX ? 3 : 1); ++i) prefetch_tensormap(&km.m[i]);
+        prefetch_tensormap(&km.m[0]);
     }
     if (tid == 32) {
         for (int i = 0; i < LP_SLOTS; ++i) {
@@ -419,7 +422,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (c < nc) tc_ld16(ts + 16 * c, sr + 16 * c);
-                const bool plain = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4) != 0;
+                const bool plain = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4) & 1u;
                 tc_wait_ld();
                 float mt = -INFINITY;  // of the logits before scaling
                 bool bad = false;
@@ -672,7 +675,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         const uint32_t full = sb + LP_FULL + 32 * reg;
                         constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
                         bool there = mbar_test_wait(full, par);
-                        const uint32_t plain = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4);
+                        const uint32_t plain = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) & 1u;
                         const bool ready = mbar_test_wait(sb + LP_PREADY, gt & 1);
                         if (!plain) {
                             // the softmax may have to look into the tile's V rows: tell both CTAs that they are there
@@ -742,6 +745,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 if (g >= 4) ok = lat_wait(sb + LP_USED + 8 * ((g - 4) & 7), ((g - 4) >> 3) & 1, dead);
                 uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + slot * 4;
                 int* look = reinterpret_cast<int*>(sm + LP_SM_LOOK) + slot * 128;
+                uint32_t whole = 0;  // bit u: unit u's rows lie one behind the other
                 if (BOX) {
                     int pg = -1, rw = 0;
                     const int j = u0 + lane < x.nU && lane < 8 ? unit_row(x, u0 + lane) : x.hi;
@@ -770,6 +774,14 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         if (pg >= 0) v |= 1u << (4 * (lane & 7) + e);
                     }
                     *reinterpret_cast<int4*>(look + 4 * lane) = make_int4(id[0], id[1], id[2], id[3]);
+                    const int behind = __shfl_down_sync(0xffffffffu, id[0], 1);
+                    const bool all4 = ((v >> (4 * (lane & 7))) & 15u) == 15u;
+                    const uint32_t b = __ballot_sync(0xffffffffu, all4 && id[1] == id[0] + 1 && id[2] == id[0] + 2 &&
+                                                                      id[3] == id[0] + 3 &&
+                                                                      ((lane & 3) == 3 || behind == id[0] + 4));
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (((b >> (4 * u)) & 15u) == 15u) whole |= 256u << u;
                     v |= __shfl_xor_sync(0xffffffffu, v, 1);
                     v |= __shfl_xor_sync(0xffffffffu, v, 2);
                     v |= __shfl_xor_sync(0xffffffffu, v, 4);
@@ -777,7 +789,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    plain[slot] = tile_plain(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u;
+                    plain[slot] = whole | (tile_plain(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u);
                     mbar_arrive(sb + LP_LOOK + 8 * slot);
                 }
                 if (i == 0 && n > 0) load_q(n);  // behind the first tile's lookups, as it may have to wait
@@ -827,8 +839,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         } else {
                             const int slab = lane >> 4, qd = lane & 15;
                             const uint4 id = ld_shared_v4(look + 16 * ((first * 4 + qd) & 31));
+                            const uint32_t whole = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) >> (8 + first);
                             ok = ok && claim((uint32_t)nu * 4096u);
-                            if (ok && qd < 4 * ku)
+                            const bool there = ok && qd < 4 * ku, box = (whole >> (qd >> 2)) & 1u;
+                            if (there && box && !(qd & 3))
+                                tma_load_2d_pair(dst + slab * 8192 + qd * 512, &km.m[1], (2 * kk + slab) * 64, (int)id.x, bar);
+                            if (there && !box)
                                 tma_gather4_pair(dst + slab * 8192 + qd * 512, &km.m[0], (2 * kk + slab) * 64,
                                                  make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
                         }
@@ -861,8 +877,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         } else {
                             const int s = lane >> 3, qd = lane & 7;
                             const uint4 id = ld_shared_v4(look + 16 * ((v * 8 + qd) & 31));
+                            const uint32_t whole = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) >> (8 + 2 * v);
                             ok = ok && claim((uint32_t)vu * 16384u);
-                            if (ok && qd < 4 * vu)
+                            const bool there = ok && qd < 4 * vu, box = (whole >> (qd >> 2)) & 1u;
+                            if (there && box && !(qd & 3))
+                                tma_load_2d_pair(dst + s * 4096 + qd * 512, &km.m[1], (int)rank * 256 + s * 64, (int)id.x, bar);
+                            if (there && !box)
                                 tma_gather4_pair(dst + s * 4096 + qd * 512, &km.m[0], (int)rank * 256 + s * 64,
                                                  make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
                         }
@@ -1076,23 +1096,24 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     for (int i = 0; i < 31; ++i)
         if (kv.rows_per_page == 1 << i) a.rpp_shift = i;
     CUtensorMap qm;
-    KeyMaps km;
+    KeyMaps km = {};
     const uint64_t qd[2] = {(uint64_t)D, (uint64_t)a.rows}, qs[1] = {ROW_BYTES};
     const uint32_t qb[2] = {64, 64};
     if (!make_bf16_map(&qm, q, 2, qd, qs, qb)) return cudaErrorInvalidValue;
     const bool box = kv.rows_per_page % 16 == 0;
-    for (int i = 0; i < 3; ++i) {
-        if (i > 0 && (!box || kv.rows_per_page < 16 << i)) break;  // no run of that many rows
-        if (box) {  // a box never reaches behind its page: only runs of units are copied in larger ones
-            const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
-            const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
+    if (box) {  // a box never reaches behind its page: only runs of units are copied in larger ones
+        const uint64_t d[3] = {(uint64_t)D, (uint64_t)kv.rows_per_page, (uint64_t)kv.n_pages};
+        const uint64_t st[2] = {ROW_BYTES, (uint64_t)kv.page_stride_bytes};
+        for (int i = 0; i < 3 && kv.rows_per_page >= 16 << i; ++i) {
             const uint32_t b[3] = {64, 16u << i, 1};
             if (!make_bf16_map(&km.m[i], kv.base, 3, d, st, b)) return cudaErrorInvalidValue;
-        } else {  // the extent ends with the last page's own rows
-            const uint64_t per_page = (uint64_t)(kv.page_stride_bytes / ROW_BYTES);
-            const uint64_t d[2] = {(uint64_t)D, (uint64_t)(kv.n_pages - 1) * per_page + (uint64_t)kv.rows_per_page};
-            const uint64_t st[1] = {ROW_BYTES};
-            const uint32_t b[2] = {64, 1};
+        }
+    } else {  // the extent ends with the last page's own rows
+        const uint64_t per_page = (uint64_t)(kv.page_stride_bytes / ROW_BYTES);
+        const uint64_t d[2] = {(uint64_t)D, (uint64_t)(kv.n_pages - 1) * per_page + (uint64_t)kv.rows_per_page};
+        const uint64_t st[1] = {ROW_BYTES};
+        for (int i = 0; i < 2 && (i == 0 || d[1] >= 16); ++i) {  // (fewer than 16 rows: no unit is copied as a box)
+            const uint32_t b[2] = {64, i == 0 ? 1u : 16u};
             if (!make_bf16_map(&km.m[i], kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
         }
     }

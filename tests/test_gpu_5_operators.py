@@ -282,6 +282,24 @@ def test_window_attention(m, H, seqs, W, S, rpp):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("rpp", [1, 3, 20, 24])
+def test_attention_over_pages_in_memory_order(m, rpp):
+    """Pages of any size one behind the other in memory, with one page elsewhere: rows of several pages are
+    neighbours in memory too."""
+    g = gen(18)
+    n = 333
+    c = Cache(g, [n], rpp)
+    first = (n + rpp - 1) // rpp
+    c.table[0, :first] = torch.arange(first, dtype=torch.int32, device="cuda")
+    c.table[0, 100 // rpp] = first  # one page elsewhere
+    q = randn(g, 7, 33, D)
+    out, lse = window(m, q, c, [7], [n], 200, 5)
+    check_window(q, c, [7], [n], 200, 5, out, lse)
+    out, lse = prefix(m, q[:1].contiguous(), c, n, [n])
+    check(out[0], lse[0], attend(q[0].double(), c.rows(0, range(n))), "prefix")
+    assert m.csa_read_device_status() == 0
+
+
 def test_window_attention_leaves_other_rows_alone(m):
     """Rows behind the last sequence and before the first, and sequences that leave their buffers."""
     g = gen(12)
