@@ -71,6 +71,7 @@ constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] bit 0: pl
                                                           // rows lie one behind the other (gathers)
 constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
+constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
 constexpr float LP_LOG2E = 1.4426950408889634f;
 constexpr float LP_LN2 = 0.6931471805599453f;
 constexpr float LP_RESCALE = 8.0f;                        // log2 units
@@ -107,6 +108,7 @@ struct LatArgs {
     int64_t total_q, max_q;
     int window, n_sink;
     int WS;                    // splits of a row tile's keys
+    int items;                 // at most, where the sequences do not overlap
     int rows;                  // query rows in all (B * H, total_q * H)
     int parts;                 // partial results of a row (1: written to out directly)
     float* part_o;             // [parts][rows][512] normalised
@@ -149,10 +151,10 @@ struct SeqCursor {
 };
 
 __device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t q1, int64_t nt) {
-    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q && nt <= 0x7FFFFFFF;
+    return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q && nt <= LP_MAX_ROWS;
 }
 
-__device__ __forceinline__ int ceil_div(int x, int y) { return (x + y - 1) / y; }
+__device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y); }
 
 // Item number `it` (warp-collective), or false behind the last one.
 __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
@@ -208,6 +210,7 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.lo = kb0;
         x.hi = kb1;
     } else {
+        if (it >= a.items) return false;  // (only offsets that fall and rise again would have more)
         while (it >= cur.base + cur.total) {
             cur.base += cur.total;
             cur.c0 += 32;
@@ -645,7 +648,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 for (int i = 0; ok && i <= T; ++i) {
                     if (i < T) {
                         const int mu = (min(8, units - 8 * i) + 1) >> 1;
-                        const uint32_t ids = (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17) | a.negate;
+                        const uint32_t ids =  // N = 32 mu
+                            (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17) | a.negate;
                         const uint32_t d = tmem + 256 + (uint32_t)((g + i) & 1) * 64, reg = (uint32_t)(sidx >> 2) & 1;
                         const uint32_t bl = klo + ((LP_SM_RING + reg * 4 * LP_SLOT) >> 4), par = (uint32_t)(sidx >> 3) & 1;
                         const uint32_t full = sb + LP_FULL + 32 * reg;
@@ -1005,7 +1009,7 @@ static DPaged cache_of(const csa_paged& kv, int64_t page_table_stride) {
 }
 
 static csa_status check_prefix(int32_t B, int32_t H, int64_t n_shared, int64_t max_rows) {
-    if (H < 1 || H > 128 || B < 1 || B > 65535 || max_rows > 0x7FFFFFFFLL) return CSA_ERR_UNSUPPORTED;
+    if (H < 1 || H > 128 || B < 1 || B > 65535 || max_rows > LP_MAX_ROWS) return CSA_ERR_UNSUPPORTED;
     if (n_shared < 0 || max_rows < n_shared) return CSA_ERR_INVALID_ARG;
     return CSA_OK;
 }
@@ -1204,6 +1208,7 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
     a.q_offsets = q_offsets;
     a.n_tokens = n_tokens;
     a.total_q = total_q;
+    a.items = (int)items;
     a.max_q = max_q;
     a.window = window;
     a.n_sink = n_sink;

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(ForkArgs a) {
         const int32_t b = a.src[g];
         if (b < 0 || b >= a.B) return -1;
         *n = a.n_tokens[b];
-        if (*n <= 0 || *n % a.rpp == 0 || (*n + a.rpp - 1) / a.rpp > a.stride) return -1;
+        if (*n <= 0 || *n % a.rpp == 0 || *n / a.rpp >= a.stride) return -1;
         const int32_t p = a.table[b * a.stride + *n / a.rpp];
         return p >= 0 && p < a.pools.n_pages ? p : -1;
     };
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(ForkArgs a) {
     block_sum2(clash, before, red);
     int64_t n = -1;
     const int64_t last = last_page(f, &n);
-    if (b < 0 || b >= a.B || d < 0 || d >= a.B || clash || n < 0 || (n + a.rpp - 1) / a.rpp > a.stride) {
+    if (b < 0 || b >= a.B || d < 0 || d >= a.B || clash || n < 0 || n / a.rpp + (n % a.rpp != 0) > a.stride) {
         if (lead) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
         return;
     }

@@ -533,8 +533,6 @@ static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return g_encode;
 }
 
-// 3-D view of the index-key pool: [pages][rows per page][128 dims], box = 16 rows x
-// (64 bf16 | 128 fp8) = 16 x 128 B, 128-byte swizzle.
 bool make_bf16_map(void* map, const void* base, int nd, const uint64_t* dims, const uint64_t* strides,
                    const uint32_t* box) {
     auto enc = encoder();
@@ -552,6 +550,8 @@ bool make_bf16_map(void* map, const void* base, int nd, const uint64_t* dims, co
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D view of the index-key pool: [pages][rows per page][128 dims], box = 16 rows x
+// (64 bf16 | 128 fp8) = 16 x 128 B, 128-byte swizzle.
 bool make_kidx_map(void* map, const HPaged& p, bool fp8, int64_t rows_per_page, int64_t n_pages) {
     CUtensorMap* m = static_cast<CUtensorMap*>(map);
     auto enc = encoder();

@@ -257,7 +257,7 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * infinity reaches only the requests that attend it.
  * B * H rows are padded to 128-row tensor-core tiles; key ranges are split and merged by
  * log-sum-exp, in a fixed order: the same inputs give the same bits.
- * 1 <= H <= 128, 1 <= B <= 65535, 0 <= n_shared <= max_rows <= 2^31 - 1; page_stride_bytes a
+ * 1 <= H <= 128, 1 <= B <= 65535, 0 <= n_shared <= max_rows <= 2^31 - 128; page_stride_bytes a
  * multiple of 1024 and n_pages * page_stride_bytes / 1024 < 2^31 (else CSA_ERR_UNSUPPORTED);
  * page_table_stride * rows_per_page >= max_rows.  workspace: 16-byte aligned, at least
  * csa_prefix_attn_workspace_size(B, H, n_shared, max_rows) bytes, contents overwritten.  Graph
@@ -278,8 +278,8 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
  *   l_j = scale * q_h . K_j,  o_h = softmax(l) . V   (K = V = the row)
  * q bf16 [total_q, H, 512]; out bf16 [total_q, H, 512]; lse fp32 [total_q, H] (nullable).  Rows of
  * out and lse that no sequence covers are left as they were.  total_q and max_q are host bounds: the
- * rows of the buffers, and the most new tokens of a sequence; a sequence whose offsets leave them is
- * skipped (CSA_ERR_DEVICE_BOUNDS).  A token before position 0 (more new tokens than n_tokens)
+ * rows of the buffers, and the most new tokens of a sequence; a sequence whose offsets leave them, or
+ * whose n_tokens is above 2^31 - 128, is skipped (CSA_ERR_DEVICE_BOUNDS).  A token before position 0 (more new tokens than n_tokens)
  * sees nothing: out 0, lse -inf.  Pages that hold only positions no new token sees are not read and
  * their table entries may be anything (a cache that gives the pages behind the window back).  A page
  * id outside the pool, or a position behind page_table_stride pages, leaves its rows out
@@ -337,7 +337,8 @@ csa_status csa_pages_free(int32_t* refs, int64_t n_pages, int32_t* page_table, i
  * n_tokens[src[f]] tokens (device int64 [B]; rows_per_page tokens to a page).  Whole pages are shared
  * (their refs go up by one); a last, partly filled page is copied, in every pool, to a new page,
  * so that parent and children can each write on; entries behind it become -1 and n_tokens[dst[f]]
- * = n_tokens[src[f]].  New pages go to the children in the order of f.  Entries of the parent without a
+ * = n_tokens[src[f]].  New pages go to the children in the order of f (the one that a skipped child would
+ * have had stays free).  Entries of the parent without a
  * page (pages behind a window, given back) are -1 in the child too.  A child whose last page finds no
  * free page keeps the whole pages and the tokens in them (CSA_ERR_NO_PAGES).  Entries that row dst[f] held
  * before are overwritten: give them back first (csa_pages_free).  A child is skipped

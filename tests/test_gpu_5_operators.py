@@ -452,6 +452,90 @@ def test_attention_on_a_side_stream_and_in_graphs(m):
     assert m.csa_read_device_status() == 0
 
 
+def test_attention_calls_on_two_streams_at_once(m):
+    """Both calls, each on its own stream with its own workspace, in flight together: the same bits as alone."""
+    g = gen(22)
+    n_rows = [5000 + 70 * b for b in range(8)]
+    c = Cache(g, n_rows, 64, 4500)
+    q, qw = randn(g, 8, 128, D), randn(g, 600, 24, D)
+    kv, n = c.paged(m), torch.tensor(n_rows, dtype=torch.int64, device="cuda")
+    off = torch.tensor([0, 100, 101, 101, 400, 401, 402, 500, 600], dtype=torch.int64, device="cuda")
+    sizes = (m.csa_prefix_attn_workspace_size(8, 128, 4500, 5500), m.csa_window_attn_workspace_size(8, 24, 600, 300, 2000, 9))
+    ws = [torch.empty(max(x, 16), dtype=torch.uint8, device="cuda") for x in sizes]
+    outs = [torch.zeros_like(q), torch.zeros_like(qw)]
+
+    def one():
+        m.csa_prefix_attn(q, 8, 128, SCALE, kv, c.width, 4500, n, 5500, outs[0], None, ws[0], ws[0].numel())
+
+    def two():
+        m.csa_window_attn(qw, 24, SCALE, kv, c.width, 8, off, n, 600, 300, 2000, 9, outs[1], None, ws[1], ws[1].numel())
+
+    one()
+    two()
+    torch.cuda.synchronize()
+    alone = [o.clone() for o in outs]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for f, s in zip((one, two), streams):
+            with torch.cuda.stream(s):
+                f()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, a) for o, a in zip(outs, alone)) and m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("rpp", [64, 24])
+def test_attention_beyond_4_gb(m, rpp):
+    """A pool of 6 GB whose used pages are its last ones: row offsets that pass 32 bits."""
+    g = gen(23)
+    n = 700
+    pages = -(-n // rpp)
+    n_pages = (6 << 30) // (rpp * 1024)
+    c = Cache.__new__(Cache)
+    c.rpp, c.pitch, c.width, c.B, c.n_pages = rpp, rpp, pages, 1, n_pages
+    c.pool = torch.zeros(n_pages * rpp, D, dtype=torch.bfloat16, device="cuda")
+    c.table = (n_pages - 1 - torch.arange(pages, dtype=torch.int32, device="cuda")).view(1, -1)
+    c.pool[c.at(0, range(n))] = randn(g, n, D)
+    q = randn(g, 5, 24, D)
+    out, lse = window(m, q, c, [5], [n], 600, 3)
+    check_window(q, c, [5], [n], 600, 3, out, lse)
+    out, lse = prefix(m, q[:1].contiguous(), c, 650, [n])
+    check(out[0], lse[0], attend(q[0].double(), c.rows(0, range(n))), "prefix")
+    assert m.csa_read_device_status() == 0
+
+
+def test_window_attention_offsets_that_fall_and_rise(m):
+    """Offsets that are not non-decreasing are reported, and the call ends: sequences that overlap because of
+    them are not all computed."""
+    g = gen(24)
+    B = 300
+    c = Cache(g, [40] * B, 64)
+    q = randn(g, 64, 128, D)
+    off = torch.tensor([0, 32] * (B // 2) + [0], dtype=torch.int64, device="cuda")
+    n = torch.full((B,), 40, dtype=torch.int64, device="cuda")
+    out = torch.full_like(q, 7.0)
+    m.csa_window_attn(q, 128, SCALE, c.paged(m), c.width, B, off, n, 64, 32, 8, 0, out)
+    torch.cuda.synchronize()
+    assert (out[32:] == 7).all() and m.csa_read_device_status() == BOUNDS
+
+
+def test_window_attention_lengths_out_of_range(m):
+    """A token count behind the largest is reported and its sequence skipped; the others are as if alone."""
+    g = gen(25)
+    c = Cache(g, [50, 60, 70], 64)
+    q = randn(g, 9, 16, D)
+    for n in ((1 << 31) - 1, 1 << 31, (1 << 63) - 1):
+        out, lse = window(m, q, c, [3, 3, 3], [50, n, 70], 32, 2)
+        assert m.csa_read_device_status() == BOUNDS
+        assert (out[3:6] == 7).all() and (lse[3:6] == 7).all()
+        check_window(q[:3], c, [3], [50], 32, 2, out[:3], lse[:3])
+        for i in range(3):
+            p = 67 + i
+            check(out[6 + i], lse[6 + i], attend(q[6 + i].double(), c.rows(2, [0, 1] + list(range(p - 31, p + 1)))), f"{p}")
+
+
 # ------------------------------------------------------------------ pages
 class Model:
     """The page calls on Python integers."""
@@ -618,6 +702,44 @@ def test_pages_fork_refusals_on_the_device(m):
         [2, 1, 1] + [0] * 9, [[0, 50, 1], [0, -1, 2], e, e], [9, 9, 0, 0], BOUNDS)
     full = [1] * 12
     assert go(full, base, [0], [1], n) == ([2] + [1] * 11, [[0, 1, -1], [0, -1, -1], e, e], [6, 4, -7, -7], NO_PAGES)
+
+
+def test_pages_fork_token_counts_out_of_range(m):
+    """Token counts that no table row holds, up to the largest integer: skipped and reported."""
+    pools = pools_of(8)
+    d = m.page_pools(pools, 8)
+    for n in (12, 13, (1 << 40) + 1, (1 << 63) - 1, (1 << 63) - 4, -1, -(1 << 63)):
+        r, t, nt = i32([1, 1, 1, 0, 0, 0, 0, 0]), i32([[0, 1, 2], [-1] * 3]), torch.tensor([n, 5], device="cuda")
+        m.csa_pages_fork(d, r, t, 3, 2, i32([0]), i32([1]), 1, nt, 4)
+        if n == 12:
+            assert t.tolist() == [[0, 1, 2]] * 2 and nt.tolist() == [12, 12] and m.csa_read_device_status() == 0
+        else:
+            assert t.tolist() == [[0, 1, 2], [-1] * 3] and nt.tolist() == [n, 5]
+            assert r.tolist() == [1, 1, 1, 0, 0, 0, 0, 0] and m.csa_read_device_status() == BOUNDS
+
+
+def test_pages_beyond_4_gb(m):
+    """A pool of 6 GB: a fork copies into its last page, a compaction moves pages from its end to its front."""
+    n_pages, words = 400000, 2048
+    pool = torch.zeros(n_pages, words, dtype=torch.int64, device="cuda")
+    d = m.page_pools([pool], n_pages)
+    refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    refs[-1] = 0
+    table = i32([[5, n_pages - 2, -1], [-1] * 3])
+    pool[n_pages - 2] = 77
+    nt = torch.tensor([7, 0], dtype=torch.int64, device="cuda")
+    m.csa_pages_fork(d, refs, table, 3, 2, i32([0]), i32([1]), 1, nt, 4)
+    assert table.tolist() == [[5, n_pages - 2, -1], [5, n_pages - 1, -1]] and nt.tolist() == [7, 7]
+    assert bool((pool[n_pages - 1] == 77).all()) and int(refs[5]) == 2 and int(refs.sum()) == n_pages + 1
+    pool[n_pages - 1] = 78
+    refs.zero_()
+    refs[5], refs[n_pages - 2:] = 2, 1
+    used = torch.zeros(1, dtype=torch.int64, device="cuda")
+    pool[5] = 76
+    m.csa_pages_compact(d, refs, refs, table, table, 3, 2, used)
+    assert used.item() == 3 and table.tolist() == [[0, 1, -1], [0, 2, -1]] and refs[:3].tolist() == [2, 1, 1]
+    assert bool((pool[:3] == torch.tensor([[76], [77], [78]], device="cuda")).all())
+    assert int(refs.sum()) == 4 and m.csa_read_device_status() == 0
 
 
 @pytest.mark.parametrize("in_place", [False, True])

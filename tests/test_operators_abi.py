@@ -44,6 +44,11 @@ def test_prefix_attn_refusals(csa):
     assert csa.csa_prefix_attn_workspace_size(2, 16, 300, 200) == 0
 
 
+def test_prefix_attn_longest_context(csa):
+    assert csa.csa_prefix_attn_workspace_size(2, 16, 100, (1 << 31) - 128) > 0
+    assert csa.csa_prefix_attn_workspace_size(2, 16, 100, (1 << 31) - 127) == 0
+
+
 def test_window_attn_refusals(csa):
     f = csa.lib().csa_window_attn
 
