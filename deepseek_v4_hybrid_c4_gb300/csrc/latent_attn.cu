@@ -59,9 +59,11 @@ constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 6
 constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
 constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
 constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
-constexpr uint32_t LP_PVDONE = LP_PREADY + 8, LP_VLAND = LP_PVDONE + 8, LP_ITEM = LP_VLAND + 8, LP_TAKEN = LP_ITEM + 32;
+constexpr uint32_t LP_PVDONE = LP_PREADY + 8, LP_ITEM = LP_PVDONE + 8, LP_TAKEN = LP_ITEM + 32;
 static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
 constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
+constexpr uint32_t LP_SM_WANT = LP_SM_TMEM + 16, LP_SM_LAND = LP_SM_TMEM + 20;  // the last tile whose V rows a softmax
+                                                          // warp asked for (even CTA), and that are there (both)
 constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits of the rows that are there
 constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row ids, or [8] units {page, row}, runs
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
@@ -292,6 +294,39 @@ __device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile
     return false;
 }
 
+// The same for a word of shared memory.
+__device__ __forceinline__ bool lat_word(uint32_t at, uint32_t want, volatile uint32_t* dead) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
+        if (ld_shared_u32(at) == want) return true;
+        if (*dead) return false;
+        if (i >= 32) __nanosleep(64);
+    }
+    *dead = 1;
+    return false;
+}
+
+// The products' thread: a bounded wait for P of tile t.  A softmax warp that has to look into the tile's V rows
+// (full, par: their barriers) asks for them meanwhile: both CTAs are told when they are there.  Out of line, as the
+// wait is over at the first look as a rule.
+__device__ __forceinline__ bool lat_wait_p(uint32_t sb, uint32_t full, uint32_t par, uint32_t t, volatile uint32_t* dead) {
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
+        if (mbar_try_wait(sb + LP_PREADY, t & 1)) return true;
+        if (ld_shared_u32(sb + LP_SM_WANT) == t + 1 && ld_shared_u32(sb + LP_SM_LAND) != t + 1) {
+#pragma unroll 1
+            for (int v = 0; v < 4; ++v) ok = ok && lat_wait(full + 8 * v, par, dead);
+            fence_cluster();
+#pragma unroll 1
+            for (int c = 0; ok && c < 2; ++c) st_dsmem_u32(mapa(sb + LP_SM_LAND, c), t + 1);
+        }
+        if (*dead || !ok) break;
+    }
+    *dead = 1;
+    return false;
+}
+
 __device__ __forceinline__ float lat_ex2(float x) {  // ex2.approx.ftz: relative error below 2^-22
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -358,12 +393,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         mbar_init(sb + LP_SFULL + 8, 1);
         mbar_init(sb + LP_PREADY, 2 * LP_SOFT);  // the softmax warps of both CTAs
         mbar_init(sb + LP_PVDONE, 1);
-        mbar_init(sb + LP_VLAND, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(sb + LP_ITEM + 8 * i, 1);
             mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_PROD + (rank == 0 ? 1 : 0));
         }
         *dead = 0;
+        *reinterpret_cast<uint32_t*>(sm + LP_SM_WANT) = *reinterpret_cast<uint32_t*>(sm + LP_SM_LAND) = 0;
         fence_mbar_init();
     }
     tc_fence_before();
@@ -463,7 +498,6 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                     const float2 zz = f32x2_split(z);
                     bad = !(zz.x == 0.f) || !(zz.y == 0.f);
-                    ++n;  // tiles that are not plain so far
                 }
                 mt *= a.sl2;
                 // the row's other quarters, and whether any logit of the tile is not finite
@@ -527,7 +561,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 if (any_bad) {  // non-finite values of this CTA's V rows -> 0
-                    ok = lat_wait(sb + LP_VLAND, (n - 1) & 1, dead) && ok;
+                    // (the products' thread, waiting for P, answers; a warp that gave up lets its own wait run out)
+                    if (lane == 0) st_dsmem_u32(mapa(sb + LP_SM_WANT, 0), (uint32_t)g + 1);
+                    ok = lat_word(sb + LP_SM_LAND, (uint32_t)g + 1, dead) && ok;
+                    fence_cluster();
                     const int vs0 = sidx + 4 * min(i + 2, x.T) + 4 * i;  // the tile's first V slot
 #pragma unroll 1
                     for (int s = 0; s < (nu + 1) >> 1; ++s) {
@@ -632,21 +669,29 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
                 return ((uint64_t)hi << 32) | (uint64_t)(lo + (off >> 4));
             };
-            for (; ok; ++q) {
-                ok = lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
-                x = load_item(sb + LP_SM_ITEM + (q & 3) * 128);
-                const int T = x.T, units = x.nU - x.t0 * 8;
-                mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
-                if (T < 0) break;
-                if (T == 0) continue;
-                ok = ok && lat_wait(sb + LP_QFULL, n & 1, dead);
+            int T = 0, units = 0;
+            auto take = [&]() {  // the next item that has tiles, or T < 0
+                do {
+                    ok = ok && lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
+                    const uint32_t at = sb + LP_SM_ITEM + (q & 3) * 128;
+                    const uint2 tt = ld_shared_v2(at);  // T, t0
+                    T = ok ? (int)tt.x : -1;
+                    units = (int)ld_shared_u32(at + 8) - (int)tt.y * 8;
+                    mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
+                    ++q;
+                } while (T == 0);
+            };
+            take();
+            while (ok && T > 0) {
+                const int T0 = T;
+                ok = lat_wait(sb + LP_QFULL, n & 1, dead);
                 ++n;
                 // S of tile i, then P V of tile i - 1.  Each slot's barrier is tested while the products of the slot
                 // before it are issued: beside the copies and the products, a look at a barrier takes 150 cycles
                 // and more.
 #pragma unroll 1
-                for (int i = 0; ok && i <= T; ++i) {
-                    if (i < T) {
+                for (int i = 0; ok && i <= T0; ++i) {
+                    if (i < T0) {
                         const int mu = (min(8, units - 8 * i) + 1) >> 1;
                         const uint32_t ids =  // N = 32 mu
                             (idesc_bf16_f32(128, 32, false) & ~(0x3Fu << 17)) | ((uint32_t)(4 * mu) << 17) | a.negate;
@@ -669,7 +714,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * kk);
                         }
                         tc_commit_pair(sb + LP_SFULL + 8 * ((g + i) & 1));
-                        if (i + 1 == T) tc_commit_pair(sb + LP_QEMPTY);
+                        if (i + 1 == T0) tc_commit_pair(sb + LP_QEMPTY);
                         sidx += 4;
                     }
                     if (i > 0 && ok) {
@@ -679,15 +724,9 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         const uint32_t full = sb + LP_FULL + 32 * reg;
                         constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
                         bool there = mbar_test_wait(full, par);
-                        const uint32_t plain = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) & 1u;
                         const bool ready = mbar_test_wait(sb + LP_PREADY, gt & 1);
-                        if (!plain) {
-                            // the softmax may have to look into the tile's V rows: tell both CTAs that they are there
-#pragma unroll 1
-                            for (int v = 0; v < 4; ++v) ok = ok && lat_wait(full + 8 * v, par, dead);
-                            if (ok) tc_commit_pair(sb + LP_VLAND);
-                        }
-                        if (!ready) ok = ok && lat_wait(sb + LP_PREADY, gt & 1, dead);
+                        if (!ready)
+                            ok = ok && lat_wait_p(sb, full, par, (uint32_t)gt, dead);
                         tc_fence_after();
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
@@ -712,7 +751,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         sidx += 4;
                     }
                 }
-                g += T;
+                g += T0;
+                take();
             }
         }
     } else if (warp == LP_SOFT + 1) {

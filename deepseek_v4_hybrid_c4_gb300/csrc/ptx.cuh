@@ -304,6 +304,8 @@ CSA_DEV void st_dsmem_u32(uint32_t cluster_addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
+CSA_DEV void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 // Arrive (once) on the mbarrier at the same shared-memory address in CTA `rank` of this cluster.
 CSA_DEV void mbar_arrive_rank(uint32_t bar, uint32_t rank) {
     asm volatile(
