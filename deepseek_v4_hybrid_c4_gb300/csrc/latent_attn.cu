@@ -55,11 +55,12 @@ constexpr int LP_PAIRS = 76;                              // pairs of SMs: sizes
 constexpr uint32_t LP_SLOT = 16384;
 constexpr uint32_t LP_QSLAB = 64 * 128;                   // 64 dims of the CTA's 64 query rows
 constexpr uint32_t LP_SM_RING = 8 * LP_QSLAB;             // behind Q
-constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // two slabs of 64 keys x 64 rows
-constexpr uint32_t LP_SM_BAR = LP_SM_P + 2 * LP_QSLAB;
+constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // slabs of 64 keys x 64 rows: two, and
+                                                          // one for tiles of up to 4 units (the last of an item)
+constexpr uint32_t LP_SM_BAR = LP_SM_P + 3 * LP_QSLAB;
 constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
 constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
-constexpr uint32_t LP_PVDONE = LP_PREADY + 8, LP_ITEM = LP_PVDONE + 8, LP_TAKEN = LP_ITEM + 32;
+constexpr uint32_t LP_PVDONE = LP_PREADY + 16, LP_ITEM = LP_PVDONE + 16, LP_TAKEN = LP_ITEM + 32;
 static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
 constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
 constexpr uint32_t LP_SM_WANT = LP_SM_TMEM + 16, LP_SM_LAND = LP_SM_TMEM + 20;  // the last tile whose V rows a softmax
@@ -159,9 +160,10 @@ __device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t 
 __device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y); }
 
 // Item number `it` (warp-collective), or false behind the last one.
+template <bool WINDOW>
 __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
     int split, splits;
-    if (a.n_rows) {
+    if (!WINDOW) {
         if (it >= a.RT * a.SP + a.B * a.OS) return false;
         int kb0, kb1;
         x.shared = it < a.RT * a.SP;
@@ -269,13 +271,17 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
 }
 
 __device__ __forceinline__ int item_units(const LatItem& x, int i) { return min(8, x.nU - (x.t0 + i) * 8); }
-__device__ __forceinline__ int unit_row(const LatItem& x, int u) { return (u < x.uA ? u : u - x.uA + x.uB) * 16; }
+template <bool WINDOW>
+__device__ __forceinline__ int unit_row(const LatItem& x, int u) {
+    return (!WINDOW ? u + x.uB : u < x.uA ? u : u - x.uA + x.uB) * 16;
+}
 
 // Tile i of the item: every row seen by every query of the item, and every page there (vw: the rows that are).
+template <bool WINDOW>
 __device__ __forceinline__ bool tile_plain(const LatItem& x, int i, uint4 vw) {
     const int u0 = (x.t0 + i) * 8;
-    return x.nU - u0 >= 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && u0 >= x.uA && unit_row(x, u0) >= x.full_lo &&
-           unit_row(x, u0 + 7) + 16 <= x.full_hi;
+    return x.nU - u0 >= 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && (!WINDOW || u0 >= x.uA) && unit_row<WINDOW>(x, u0) >= x.full_lo &&
+           unit_row<WINDOW>(x, u0 + 7) + 16 <= x.full_hi;
 }
 
 // Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
@@ -313,7 +319,7 @@ __device__ __forceinline__ bool lat_wait_p(uint32_t sb, uint32_t full, uint32_t 
     bool ok = true;
 #pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
-        if (mbar_try_wait(sb + LP_PREADY, t & 1)) return true;
+        if (mbar_try_wait(sb + LP_PREADY + 8 * (t & 1), (t >> 1) & 1)) return true;
         if (ld_shared_u32(sb + LP_SM_WANT) == t + 1 && ld_shared_u32(sb + LP_SM_LAND) != t + 1) {
 #pragma unroll 1
             for (int v = 0; v < 4; ++v) ok = ok && lat_wait(full + 8 * v, par, dead);
@@ -362,7 +368,7 @@ struct KeyMaps {
     CUtensorMap m[3];
 };
 
-template <bool BOX>
+template <bool BOX, bool WINDOW>
 __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps& km, const LatArgs& a) {
     extern __shared__ uint8_t lp_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lp_raw) + 1023) & ~uintptr_t(1023));
@@ -392,7 +398,9 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         mbar_init(sb + LP_SFULL, 1);
         mbar_init(sb + LP_SFULL + 8, 1);
         mbar_init(sb + LP_PREADY, 2 * LP_SOFT);  // the softmax warps of both CTAs
+        mbar_init(sb + LP_PREADY + 8, 2 * LP_SOFT);
         mbar_init(sb + LP_PVDONE, 1);
+        mbar_init(sb + LP_PVDONE + 8, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(sb + LP_ITEM + 8 * i, 1);
             mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_PROD + (rank == 0 ? 1 : 0));
@@ -433,7 +441,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             // rows that this query sees: [vlo, vhi) and [0, vs)
             int vlo = 0, vhi = 0, vs = 0;
             if (mine) {
-                if (!a.n_rows) {
+                if (WINDOW) {
                     const int64_t pos = x.pos0 + div_by(x.rr0 + (int)rank * 64 + r, a.by_H);
                     vhi = pos >= 0 ? (int)pos + 1 : 0;
                     vlo = max(0, vhi - a.window);
@@ -477,7 +485,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         if (c < nc) {
                             uint32_t bits = 0;
                             if (u < nu) {
-                                const int jb = unit_row(x, u0 + u);
+                                const int jb = unit_row<WINDOW>(x, u0 + u);
                                 const int e0 = min(max(vlo - jb, 0), 16), e1 = min(max(vhi - jb, 0), 16);
                                 const int e2 = min(max(vs - jb, 0), 16);
                                 bits = (((1u << e1) - 1u) & ~((1u << e0) - 1u)) | ((1u << e2) - 1u);
@@ -531,9 +539,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 const float2 ss = f32x2_split(sum);
                 l_run = l_run * alpha + (ss.x + ss.y);
-                // P and O are free once the product before this one is done
-                if (i > 0) {
-                    ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
+                // P and O are free once the product before this one is done; a short tile, the item's last, has a
+                // slab of its own for P, and as a rule leaves O alone
+                const bool tail = WINDOW && nu <= 4;
+                if (i > 0 && (!tail || any_bad || __any_sync(0xffffffffu, alpha != 1.f))) {
+                    ok = lat_wait(sb + LP_PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, dead) && ok;
                     tc_fence_after();
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -552,7 +562,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 for (int c = 0; c < 2; ++c) {
                     if (c < nc) {
                         const int u = ub + c;
-                        const uint32_t pb = sb + LP_SM_P + (uint32_t)(u >> 2) * LP_QSLAB + (uint32_t)r * 128;
+                        const uint32_t pb = sb + LP_SM_P + (uint32_t)(tail ? 2 : u >> 2) * LP_QSLAB + (uint32_t)r * 128;
 #pragma unroll
                         for (int h2 = 0; h2 < 2; ++h2)
                             st_shared_v4(pb + ((uint32_t)(((u & 3) * 2 + h2) ^ (r & 7)) << 4),
@@ -588,12 +598,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_rank(sb + LP_PREADY, 0);
+                if (lane == 0) mbar_arrive_rank(sb + LP_PREADY + 8 * (g & 1), 0);
             }
             if (x.T > 0) {
                 sidx += 8 * x.T;
                 ls[tid] = l_run;
-                ok = lat_wait(sb + LP_PVDONE, (g - 1) & 1, dead) && ok;
+                ok = lat_wait(sb + LP_PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, dead) && ok;
                 tc_fence_after();
                 named_bar_sync(1, 32 * LP_SOFT);
                 l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
@@ -724,10 +734,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         const uint32_t full = sb + LP_FULL + 32 * reg;
                         constexpr uint32_t idv = idesc_bf16_f32(128, 256, true);
                         bool there = mbar_test_wait(full, par);
-                        const bool ready = mbar_test_wait(sb + LP_PREADY, gt & 1);
+                        const bool ready = mbar_test_wait(sb + LP_PREADY + 8 * (gt & 1), (gt >> 1) & 1);
                         if (!ready)
                             ok = ok && lat_wait_p(sb, full, par, (uint32_t)gt, dead);
                         tc_fence_after();
+                        // (an operand whose place is no constant costs the products 5 percent: prefixes have one P)
+                        const uint32_t pl = klo + ((LP_SM_P + (WINDOW && nu <= 4 ? 2 * LP_QSLAB : 0u)) >> 4);
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             if (!there) ok = ok && lat_wait(full + 8 * v, par, dead);
@@ -735,19 +747,17 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             if (v < 3) there = mbar_test_wait(full + 8 * v + 8, par);
                             tc_fence_after();
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int u = 2 * v + e;
-                                if (u < nu) {
+                            for (int u = 2 * v; u < 2 * v + 2; ++u) {
+                                if (u >= nu) continue;
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c)
-                                        tc_mma_f16_pair(tmem + c * 128, desc(klo, khi, LP_SM_P + (u >> 2) * LP_QSLAB + (u & 3) * 32),
-                                                        desc(bl, vhi, v * LP_SLOT + c * 8192 + e * 2048), idv,
-                                                        i == 1 && u == 0 ? 0u : 1u);
-                                }
+                                for (int c = 0; c < 2; ++c)
+                                    tc_mma_f16_pair(tmem + c * 128, desc(pl, khi, (u >> 2) * LP_QSLAB + (u & 3) * 32),
+                                                    desc(bl, vhi, v * LP_SLOT + c * 8192 + (u & 1) * 2048), idv,
+                                                    i == 1 && u == 0 ? 0u : 1u);
                             }
                             tc_commit_pair(sb + LP_EMPTY + 32 * reg + 8 * v);
                         }
-                        tc_commit_pair(sb + LP_PVDONE);
+                        tc_commit_pair(sb + LP_PVDONE + 8 * (gt & 1));
                         sidx += 4;
                     }
                 }
@@ -761,7 +771,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         uint32_t* plain = reinterpret_cast<uint32_t*>(sm + LP_SM_PLAIN);
         SeqCursor cur;
         for (int it = pair; ok; it += pairs, ++q) {
-            const bool there = lat_item(a, cur, it, lane, rank == 0, x);
+            const bool there = lat_item<WINDOW>(a, cur, it, lane, rank == 0, x);
             if (!there) x.T = -1;
             if (q >= 4) ok = lat_wait(sb + LP_TAKEN + 8 * (q & 3), ((q >> 2) - 1) & 1, dead);
             if (lane == 0) {
@@ -792,7 +802,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 uint32_t whole = 0;  // bit u: unit u's rows lie one behind the other
                 if (BOX) {
                     int pg = -1, rw = 0;
-                    const int j = u0 + lane < x.nU && lane < 8 ? unit_row(x, u0 + lane) : x.hi;
+                    const int j = u0 + lane < x.nU && lane < 8 ? unit_row<WINDOW>(x, u0 + lane) : x.hi;
                     if (j < x.hi) pg = lat_page(a, pt, j, rw);  // (a unit behind the last row that is seen: none)
                     const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0);
                     if (lane < 4) vw[lane] = ((b >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((b >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
@@ -811,9 +821,9 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // rows of a unit that no query sees are not looked up
                         const int k = lane * 4 + e, u = u0 + (k >> 4);
-                        const int j = u < x.nU ? unit_row(x, u) + (k & 15) : -1;
+                        const int j = u < x.nU ? unit_row<WINDOW>(x, u) + (k & 15) : -1;
                         int rw, pg = -1;
-                        if (j >= 0 && (j < x.a1 || (j >= x.lo && j < x.hi))) pg = lat_page(a, pt, j, rw);
+                        if (j >= 0 && ((WINDOW && j < x.a1) || (j >= x.lo && j < x.hi))) pg = lat_page(a, pt, j, rw);
                         id[e] = pg >= 0 ? pg * (int)(a.kv.page_stride / ROW_BYTES) + rw : 0;
                         if (pg >= 0) v |= 1u << (4 * (lane & 7) + e);
                     }
@@ -833,7 +843,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    plain[slot] = whole | (tile_plain(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u);
+                    plain[slot] = whole | (tile_plain<WINDOW>(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u);
                     mbar_arrive(sb + LP_LOOK + 8 * slot);
                 }
                 if (i == 0 && n > 0) load_q(n);  // behind the first tile's lookups, as it may have to wait
@@ -956,13 +966,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     if (warp == 0) tmem_dealloc_pair(tmem, 512);
 }
 
+template <bool BOX, bool WINDOW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
-    lat_box_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps km, const __grid_constant__ LatArgs a) {
-    lat_pair<true>(qmap, km, a);
-}
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
-    lat_gather_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps km, const __grid_constant__ LatArgs a) {
-    lat_pair<false>(qmap, km, a);
+    lat_pair_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ KeyMaps km,
+                    const __grid_constant__ LatArgs a) {
+    lat_pair<BOX, WINDOW>(qmap, km, a);
 }
 
 // Log-sum-exp merge of a row's partial results, in their order: one CTA per row, thread t columns
@@ -1161,7 +1169,9 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
             if (!make_bf16_map(&km.m[i], kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
         }
     }
-    void (*kernel)(CUtensorMap, KeyMaps, LatArgs) = box ? lat_box_kernel : lat_gather_kernel;
+    void (*kernel)(CUtensorMap, KeyMaps, LatArgs) =
+        a.n_rows ? (box ? lat_pair_kernel<true, false> : lat_pair_kernel<false, false>)
+                 : (box ? lat_pair_kernel<true, true> : lat_pair_kernel<false, true>);
     cudaError_t e = set_func_attr_once((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LP_SMEM);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, sms / 2));
