@@ -264,8 +264,8 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.full_hi = p0 >= 0 ? (int)p0 + 1 : 0;
     }
     const int tiles = ceil_div(x.nU, 8);
-    x.t0 = (int)((int64_t)tiles * split / splits);
-    x.T = (int)((int64_t)tiles * (split + 1) / splits) - x.t0;
+    x.t0 = (int)((uint32_t)(tiles * split) / (uint32_t)splits);  // (fewer than 2^24 tiles, up to 76 splits)
+    x.T = (int)((uint32_t)(tiles * (split + 1)) / (uint32_t)splits) - x.t0;
     if (x.shared && x.t0 * 128 >= x.hi) x.T = 0;
     return true;
 }
@@ -284,12 +284,7 @@ __device__ __forceinline__ bool tile_plain(const LatItem& x, int i, uint4 vw) {
            unit_row<WINDOW>(x, u0 + 7) + 16 <= x.full_hi;
 }
 
-// Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
-// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
-// further wait returning at once.
-// Lane i waits on the barrier at its own address: a warp can wait on several at once.
-__device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool lat_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
 #pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -298,6 +293,13 @@ __device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile
     }
     *dead = 1;
     return false;
+}
+// Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
+// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
+// further wait returning at once.
+// Lane i waits on the barrier at its own address: a warp can wait on several at once.
+__device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
+    return mbar_try_wait(bar, parity) || lat_wait_on(bar, parity, dead);
 }
 
 // The same for a word of shared memory.
@@ -652,10 +654,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             if (p & s) continue;
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                const uint32_t give = up ? v[8 * p + e] : v[8 * (p | s) + e];
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, s);
-                                if (up) v[8 * p + e] = got;
-                                else v[8 * (p | s) + e] = got;
+                                const uint32_t lo = v[8 * p + e], hi = v[8 * (p | s) + e];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                                v[8 * p + e] = up ? got : lo;
+                                v[8 * (p | s) + e] = up ? hi : got;
                             }
                         }
                     }
@@ -783,12 +785,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
             auto load_q = [&](int k) {
                 if (k > 0) ok = lat_wait(sb + LP_QEMPTY, (k - 1) & 1, dead) && ok;
-                if (ok && lane == 0) {
-                    if (rank == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        tma_load_2d_pair(sb + s * LP_QSLAB, &qmap, s * 64, x.row0 + (int)rank * 64, qfull);
-                }
+                if (ok && rank == 0 && lane == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
+                __syncwarp();
+                if (ok && lane < 8)
+                    tma_load_2d_pair(sb + lane * LP_QSLAB, &qmap, lane * 64, x.row0 + (int)rank * 64, qfull);
                 __syncwarp();
             };
             if (x.T > 0 && n == 0) load_q(0);
