@@ -602,19 +602,23 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 __syncwarp();
                 if (lane == 0) mbar_arrive_rank(sb + LP_PREADY + 8 * (g & 1), 0);
             }
+            // while the last product runs: the row's sum, its lse and where its output goes
             if (x.T > 0) {
                 sidx += 8 * x.T;
                 ls[tid] = l_run;
-                ok = lat_wait(sb + LP_PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, dead) && ok;
-                tc_fence_after();
                 named_bar_sync(1, 32 * LP_SOFT);
                 l_run = (ls[r] + ls[r + 64]) + (ls[r + 128] + ls[r + 192]);
+            }
+            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const bool direct = a.parts == 1;
+            if (tid < 64 && mine) {
+                const float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
+                if (!direct) a.part_lse[(int64_t)x.part * a.rows + row] = e;
+                else if (a.lse) a.lse[row] = e;
             }
             // ---- row r of the CTA, dims [256 half + 128 ch, + 128), normalised.  Four lanes exchange their rows'
             //      sectors, so that a store covers 128 bytes of each of 8 rows: an SM's stores leave at 43 bytes a
             //      cycle so, and at 17 with a sector of each of 32 rows (a 64 KB item: 1,520 and 3,250 cycles).
-            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-            const bool direct = a.parts == 1;
             if (direct || x.T > 0) {
                 const int at = half * 256 + ch * 128, j = lane & 3;
                 const int64_t gr = row - j;  // the group's first row
@@ -623,6 +627,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                                        : reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)x.part * a.rows + gr) * D + at)) +
                                j * 32;
                 const int64_t pitch = direct ? D * 2 : D * 4;
+                if (x.T > 0) {
+                    ok = lat_wait(sb + LP_PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, dead) && ok;
+                    tc_fence_after();
+                }
 #pragma unroll 1
                 for (int c = 0; c < (direct ? 2 : 4); ++c) {
                     uint32_t v[32];  // 128 bytes of this lane's row
@@ -646,31 +654,27 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
                     }
                     // 4 x 4 transpose of sectors: lane j of a group ends with sector j of the group's rows 0 .. 3
-#pragma unroll
-                    for (int s = 1; s < 4; s <<= 1) {
+                    auto exchange = [&](int p, int s) {
                         const bool up = (lane & s) != 0;
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            if (p & s) continue;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t lo = v[8 * p + e], hi = v[8 * (p | s) + e];
-                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
-                                v[8 * p + e] = up ? got : lo;
-                                v[8 * (p | s) + e] = up ? hi : got;
-                            }
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t lo = v[8 * p + e], hi = v[8 * (p | s) + e];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                            v[8 * p + e] = up ? got : lo;
+                            v[8 * (p | s) + e] = up ? hi : got;
                         }
-                    }
+                    };
+                    exchange(0, 2);
+                    exchange(1, 2);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left) store_sector(dst + k * pitch + c * 128, v + 8 * k, a.wide_out || !direct);
+                    for (int p = 0; p < 4; p += 2) {
+                        exchange(p, 1);
+#pragma unroll
+                        for (int k = p; k < p + 2; ++k)
+                            if (k < left) store_sector(dst + k * pitch + c * 128, v + 8 * k, a.wide_out || !direct);
+                    }
                 }
                 tc_fence_before();
-            }
-            if (tid < 64 && mine) {
-                const float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
-                if (!direct) a.part_lse[(int64_t)x.part * a.rows + row] = e;
-                else if (a.lse) a.lse[row] = e;
             }
         }
     } else if (warp == LP_SOFT && rank == 0) {
