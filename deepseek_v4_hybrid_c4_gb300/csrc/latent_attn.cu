@@ -641,11 +641,15 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             uint32_t o[32];
+                            const uint64_t inv2 = f32x2(inv, inv);
                             tc_ld32(tmem + lane_off + 128 * ch + 64 * c + 32 * h, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                v[16 * h + e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 f = f32x2_split(
+                                    f32x2_mul(f32x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2));
+                                v[16 * h + e] = pack_bf16x2(f.x, f.y);
+                            }
                         }
                     } else {
                         tc_ld32(tmem + lane_off + 128 * ch + 32 * c, v);

@@ -163,7 +163,7 @@ CSA_DEV void stg_v8(void* p, const uint32_t* w) {
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-// Pairs of floats in one register pair: a * b + c and a + b on both halves.
+// Pairs of floats in one register pair: a * b + c, a + b and a * b on both halves.
 CSA_DEV uint64_t f32x2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -182,6 +182,11 @@ CSA_DEV uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
 CSA_DEV uint64_t f32x2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+CSA_DEV uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
