@@ -15,12 +15,19 @@
 // dims would have to compute S twice).  Measured on GB300 with nothing but these products in flight: 2,056 cycles
 // a tile against 2,048 at the nominal rate.
 //
+// What bounds it.  Many query rows over a long prefix: the tensor cores under the power limit (4,096 rows over
+// 32K keys, 276 GFLOP: 172 us, 1.6 PFLOP/s; fewer cycles a tile only lowered the clock).  A prompt under a
+// short window: the softmax warps' chain through an item (8,192 tokens of 128 heads, window 128: 459 us, 4.7 TB/s
+// of queries and outputs; 40 percent of an item is its output).  Single tokens: one chain of dependent loads,
+// products and stores, 9 to 11 us.
+//
 // Roles (16 warps a CTA): warps 0-7 own the TMEM lanes, two to a lane quarter (softmax, output); warp 8 of
 // the even CTA issues the products; warp 9 works the items out for the others, looks up the tiles' pages, up to
 // four tiles ahead, and loads Q; warps 10-15 load key rows.  Both CTAs' copies report to the even CTA's
-// barriers.  The loops are kept short and, for the products, free of branches: with the items worked out in
+// barriers.  The code is kept small and, for the products, free of branches: with the items worked out in
 // every role and a wait before each slot's products, the kernel was 175 KB of code, every step of a role
-// cost some 200 cycles (the waits themselves were over at once), and a tile took 4,400 cycles.
+// cost some 200 cycles (the waits themselves were over at once), and a tile took 4,400 cycles.  Windows and
+// prefixes are separate kernels (a shared one: prefixes 2 to 5 percent slower), 63 to 67 KB each.
 // Key rows come through a ring of 8 slots of 16 KB in the order in which the products take them: S of a tile
 // in four slots (128 dims each of the CTA's own keys), P V in four (32 keys each, the CTA's half of the
 // dims; empty ones in a short tile).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
@@ -32,12 +39,15 @@
 //
 // Softmax: a thread holds one row's logits of a quarter of a tile; the row's four threads exchange their
 // maxima.  The running maximum moves only when a tile exceeds it by 2^8 (O is then rescaled in TMEM);
-// P is rounded to bf16 for the product, its sum is taken in fp32 before the rounding.
+// P is rounded to bf16 for the product, its sum is taken in fp32 before the rounding.  P and O wait for the
+// product before; the last tile of a window item, when it is short, has a place of its own for P and waits only to
+// rescale O (a prompt of 8K tokens: 524 -> 503 us).
 //
 // A masked weight is exactly 0, but 0 * NaN is NaN, and the products see every row of a unit.  In
 // a tile with masked rows a NaN or an infinity in any row makes that row's logits of all 128 query rows
 // non-finite; where a thread finds one, its CTA replaces the non-finite values of the tile's V rows by 0 before the
-// product.  Query rows that do attend such a key have a NaN weight from its logit and stay NaN.
+// product, once the products' thread has told it that they are there (waiting for them in every tile with masked rows
+// cost a prompt 6 percent).  Query rows that do attend such a key have a NaN weight from its logit and stay NaN.
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,8 +69,9 @@ constexpr uint32_t LP_SM_P = LP_SM_RING + LP_SLOTS * LP_SLOT;  // slabs of 64 ke
                                                           // one for tiles of up to 4 units (the last of an item)
 constexpr uint32_t LP_SM_BAR = LP_SM_P + 3 * LP_QSLAB;
 constexpr uint32_t LP_FULL = LP_SM_BAR, LP_EMPTY = LP_FULL + 64, LP_LOOK = LP_EMPTY + 64, LP_USED = LP_LOOK + 64;
-constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8, LP_PREADY = LP_SFULL + 16;
-constexpr uint32_t LP_PVDONE = LP_PREADY + 16, LP_ITEM = LP_PVDONE + 16, LP_TAKEN = LP_ITEM + 32;
+constexpr uint32_t LP_QFULL = LP_USED + 64, LP_QEMPTY = LP_QFULL + 8, LP_SFULL = LP_QEMPTY + 8;
+constexpr uint32_t LP_PREADY = LP_SFULL + 16, LP_PVDONE = LP_PREADY + 16, LP_ITEM = LP_PVDONE + 16;
+constexpr uint32_t LP_TAKEN = LP_ITEM + 32;
 static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
 constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
 constexpr uint32_t LP_SM_WANT = LP_SM_TMEM + 16, LP_SM_LAND = LP_SM_TMEM + 20;  // the last tile whose V rows a softmax
@@ -203,7 +214,8 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
             x.trow = b;
             x.part = a.SP + split;
             const int64_t n = __ldg(a.n_rows + b);
-            if (report && lane == 0 && split == 0 && (n < 0 || n > a.max_rows)) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
+            if (report && lane == 0 && split == 0 && (n < 0 || n > a.max_rows))
+                raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
             kb0 = a.n_shared;
             kb1 = n < 0 ? 0 : (n > a.max_rows ? a.max_rows : (int)n);
             x.full_lo = kb0;
@@ -280,10 +292,15 @@ __device__ __forceinline__ int unit_row(const LatItem& x, int u) {
 template <bool WINDOW>
 __device__ __forceinline__ bool tile_plain(const LatItem& x, int i, uint4 vw) {
     const int u0 = (x.t0 + i) * 8;
-    return x.nU - u0 >= 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && (!WINDOW || u0 >= x.uA) && unit_row<WINDOW>(x, u0) >= x.full_lo &&
-           unit_row<WINDOW>(x, u0 + 7) + 16 <= x.full_hi;
+    return x.nU - u0 >= 8 && (vw.x & vw.y & vw.z & vw.w) == 0xffffffffu && (!WINDOW || u0 >= x.uA) &&
+           unit_row<WINDOW>(x, u0) >= x.full_lo && unit_row<WINDOW>(x, u0 + 7) + 16 <= x.full_hi;
 }
 
+// Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
+// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
+// further wait returning at once.
+// Lane i waits on the barrier at its own address: a warp can wait on several at once.  A wait that is not over at
+// the first look goes on out of line (the code of all roles goes through one instruction cache).
 __device__ __noinline__ bool lat_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
 #pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
@@ -294,10 +311,6 @@ __device__ __noinline__ bool lat_wait_on(uint32_t bar, uint32_t parity, volatile
     *dead = 1;
     return false;
 }
-// Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
-// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
-// further wait returning at once.
-// Lane i waits on the barrier at its own address: a warp can wait on several at once.
 __device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
     return mbar_try_wait(bar, parity) || lat_wait_on(bar, parity, dead);
 }
@@ -315,9 +328,9 @@ __device__ __forceinline__ bool lat_word(uint32_t at, uint32_t want, volatile ui
 }
 
 // The products' thread: a bounded wait for P of tile t.  A softmax warp that has to look into the tile's V rows
-// (full, par: their barriers) asks for them meanwhile: both CTAs are told when they are there.  Out of line, as the
-// wait is over at the first look as a rule.
-__device__ __forceinline__ bool lat_wait_p(uint32_t sb, uint32_t full, uint32_t par, uint32_t t, volatile uint32_t* dead) {
+// (full, par: their barriers) asks for them meanwhile: both CTAs are told when they are there.
+__device__ __forceinline__ bool lat_wait_p(uint32_t sb, uint32_t full, uint32_t par, uint32_t t,
+                                            volatile uint32_t* dead) {
     bool ok = true;
 #pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
@@ -351,7 +364,7 @@ __device__ __forceinline__ void store_sector(uint8_t* p, const uint32_t* w, bool
     }
 }
 
-// Row id of logical row j of the item's request, -1 where there is no page (or none inside the pool).
+// Page of logical row j of the item's request and j's row in it; -1 where there is no page (or none inside the pool).
 __device__ __forceinline__ int lat_page(const LatArgs& a, const int32_t* pt, int j, int& slot) {
     const uint32_t lp = a.rpp_shift >= 0 ? (uint32_t)j >> a.rpp_shift : (uint32_t)j / (uint32_t)a.kv.rpp;
     slot = j - (int)lp * a.kv.rpp;
@@ -813,7 +826,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     const int j = u0 + lane < x.nU && lane < 8 ? unit_row<WINDOW>(x, u0 + lane) : x.hi;
                     if (j < x.hi) pg = lat_page(a, pt, j, rw);  // (a unit behind the last row that is seen: none)
                     const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0);
-                    if (lane < 4) vw[lane] = ((b >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((b >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
+                    const uint32_t b2 = b >> (2 * lane);
+                    if (lane < 4) vw[lane] = (b2 & 1 ? 0xFFFFu : 0u) | (b2 & 2 ? 0xFFFF0000u : 0u);
                     if (pg < 0) pg = rw = 0;
                     // bit u: unit u + 1 lies right behind unit u
                     const int pn = __shfl_down_sync(0xffffffffu, pg, 1), rn = __shfl_down_sync(0xffffffffu, rw, 1);
@@ -1122,7 +1136,8 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
     a->parts = a->SP + a->OS;
 }
 
-static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, LatArgs* a, int64_t* items) {
+static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, LatArgs* a,
+                        int64_t* items) {
     a->rows = (int)(total_q * H);
     const int64_t per_seq = (max_q * H + 127) / 128;
     const int64_t tiles_q = std::min((int64_t)B * per_seq, (total_q * H + 127) / 128 + B);
