@@ -86,6 +86,9 @@ constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] bit 0: pl
 constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
+// Tiles of a split at most: O takes eight additions a tile in the tensor cores, each of which may lose 2^-23 of the
+// sum so far, in all no more than the 2^-8 that a rounded weight may be off.
+constexpr int LP_MAX_TILES = 4096;
 constexpr float LP_LOG2E = 1.4426950408889634f;
 constexpr float LP_LN2 = 0.6931471805599453f;
 constexpr float LP_RESCALE = 8.0f;                        // log2 units
@@ -116,6 +119,7 @@ struct LatArgs {
     const int64_t* n_rows;     // nullptr: window
     int n_shared, max_rows;
     int RT, SP, OS;            // row tiles over the batch; splits of the shared rows, of a request's own rows
+    FastDiv by_RT, by_SP, by_OS, by_WS;
     // window: B sequences
     const int64_t* q_offsets;
     const int64_t* n_tokens;
@@ -174,6 +178,7 @@ __device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)
 template <bool WINDOW>
 __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
     int split, splits;
+    FastDiv by;
     if (!WINDOW) {
         if (it >= a.RT * a.SP + a.B * a.OS) return false;
         int kb0, kb1;
@@ -181,8 +186,9 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.a1 = x.uA = x.rr0 = 0;
         x.pos0 = 0;
         if (x.shared) {  // neighbouring items read the same keys
-            split = it / a.RT;
+            split = div_by(it, a.by_RT);
             splits = a.SP;
+            by = a.by_SP;
             x.row0 = (it - split * a.RT) * 128;
             x.nrows = min(128, a.rows - x.row0);
             x.trow = 0;
@@ -206,9 +212,10 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
             x.full_hi = mn;
             x.nU = ceil_div(a.n_shared, 16);  // the same split of the keys for every row tile
         } else {
-            const int j = it - a.RT * a.SP, b = j / a.OS;
+            const int j = it - a.RT * a.SP, b = div_by(j, a.by_OS);
             split = j - b * a.OS;
             splits = a.OS;
+            by = a.by_OS;
             x.row0 = b * a.H;
             x.nrows = a.H;
             x.trow = b;
@@ -256,9 +263,11 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         const int d = at - __shfl_sync(0xffffffffu, cur.incl - cur.tiles, src);
         const int ql = __shfl_sync(0xffffffffu, cur.ql, src);
         const int64_t q0 = __shfl_sync(0xffffffffu, cur.q0, src), nt = __shfl_sync(0xffffffffu, cur.nt, src);
+        const int tile = div_by(d, a.by_WS);
         splits = a.WS;
-        split = d % a.WS;
-        x.rr0 = d / a.WS * 128;
+        by = a.by_WS;
+        split = d - tile * a.WS;
+        x.rr0 = tile * 128;
         x.nrows = min(128, ql * a.H - x.rr0);
         x.row0 = (int)q0 * a.H + x.rr0;
         x.trow = cur.c0 + src;
@@ -276,8 +285,9 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.full_hi = p0 >= 0 ? (int)p0 + 1 : 0;
     }
     const int tiles = ceil_div(x.nU, 8);
-    x.t0 = (int)((uint32_t)(tiles * split) / (uint32_t)splits);  // (fewer than 2^24 tiles, up to 76 splits)
-    x.T = (int)((uint32_t)(tiles * (split + 1)) / (uint32_t)splits) - x.t0;
+    const int each = div_by(tiles, by), more = tiles - each * splits;  // the first `more` splits take one more
+    x.t0 = split * each + min(split, more);
+    x.T = each + (split < more ? 1 : 0);
     if (x.shared && x.t0 * 128 >= x.hi) x.T = 0;
     return true;
 }
@@ -1121,12 +1131,13 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
     a->SP = 0;
     a->OS = 0;
     double best = 1e30;
+    const int os_least = (own + LP_MAX_TILES - 1) / LP_MAX_TILES, sp_least = (tiles + LP_MAX_TILES - 1) / LP_MAX_TILES;
     const int os_most = own ? std::min(own, std::max(1, 4 * LP_PAIRS / B)) : 0;
-    const int sp_most = std::min(tiles, LP_PAIRS);
-    for (int sp = std::min(1, tiles); sp <= sp_most; ++sp) {
+    const int sp_most = std::max(sp_least, std::min(tiles, LP_PAIRS));
+    for (int sp = sp_least; sp <= sp_most; ++sp) {
         // a request's own rows: whole, or in pieces as long as the shared ones
-        const int piece = sp ? std::max(4, (tiles + sp - 1) / sp) : std::max(2, (own * B + LP_PAIRS - 1) / LP_PAIRS);
-        const int os = own ? std::min((own + piece - 1) / piece, os_most) : 0;
+        const int piece = sp ? std::max(4, (tiles + sp - 1) / sp) : (int)std::max<int64_t>(2, ((int64_t)own * B + LP_PAIRS - 1) / LP_PAIRS);
+        const int os = std::max(os_least, own ? std::min((own + piece - 1) / piece, os_most) : 0);
         const double c = (double)deal_cost((int64_t)a->RT * sp, sp ? (tiles + sp - 1) / sp : 0, (int64_t)B * os,
                                            os ? (own + os - 1) / os : 0) +
                          (sp + os > 1 ? 1.4 * (sp + os) * a->rows / 4096.0 + 0.02 * (sp + os) : 0.0);
@@ -1146,7 +1157,7 @@ static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window
     const int64_t tiles = (keys + 127) / 128;
     int64_t s = 1;
     if (tiles >= 4 && tiles_q <= LP_PAIRS / 2) s = std::min(tiles / 2, LP_PAIRS / std::max<int64_t>(tiles_q, 1));
-    a->WS = (int)std::max<int64_t>(1, s);
+    a->WS = (int)std::max(s, (tiles + LP_MAX_TILES - 1) / LP_MAX_TILES);
     a->parts = a->WS;
     if (items) *items = tiles_q * a->WS;
 }
@@ -1165,6 +1176,11 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
         a.part_lse = reinterpret_cast<float*>(base + align_up((size_t)a.parts * a.rows * D * sizeof(float), 256));
     }
     a.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
+    a.by_H = fast_div(a.H);
+    a.by_RT = fast_div(std::max(a.RT, 1));
+    a.by_SP = fast_div(std::max(a.SP, 1));
+    a.by_OS = fast_div(std::max(a.OS, 1));
+    a.by_WS = fast_div(std::max(a.WS, 1));
     const int sms = device_sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
     a.rpp_shift = -1;
@@ -1229,11 +1245,11 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
     plan_prefix(B, H, n_shared, max_rows, &a);
     const size_t need = parts_bytes(a);
     if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
+    if ((int64_t)a.RT * a.SP + (int64_t)B * a.OS > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
     set_scale(a, scale);
-    a.by_H = fast_div(H);
     a.kv = cache_of(kv, page_table_stride);
     a.table_pages = page_table_stride;
     a.B = B;
@@ -1270,11 +1286,11 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
     const size_t need = parts_bytes(a);
     if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
     if (total_q == 0) return CSA_OK;
+    if (items > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
     set_scale(a, scale);
-    a.by_H = fast_div(H);
     a.kv = cache_of(kv_raw, page_table_stride);
     a.table_pages = page_table_stride;
     a.B = B;

@@ -256,7 +256,8 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
  * infinity reaches only the requests that attend it.
  * B * H rows are padded to 128-row tensor-core tiles; key ranges are split and merged by
- * log-sum-exp, in a fixed order: the same inputs give the same bits.
+ * log-sum-exp, in a fixed order: the same inputs give the same bits.  A range holds up to 524,288
+ * rows, so that the workspace grows with max_rows beyond that.
  * 1 <= H <= 128, 1 <= B <= 65535, 0 <= n_shared <= max_rows <= 2^31 - 128; page_stride_bytes a
  * multiple of 1024 and n_pages * page_stride_bytes / 1024 < 2^31 (else CSA_ERR_UNSUPPORTED);
  * page_table_stride * rows_per_page >= max_rows.  workspace: 16-byte aligned, at least

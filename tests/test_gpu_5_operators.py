@@ -506,6 +506,45 @@ def test_attention_beyond_4_gb(m, rpp):
     assert m.csa_read_device_status() == 0
 
 
+@pytest.mark.parametrize("call", ["prefix", "window"])
+def test_attention_over_the_longest_context(m, call):
+    """2^31 - 128 rows over three pages of 4,096 rows, named again and again; all rows, and a window of 2^30.  Beside
+    the bounds of attend(): a split of 4,096 tiles adds eight times a tile to its output, each losing up to
+    2^-23 of the sum (2^-8 in all), and once a tile to its row sums, and up to 4,096 splits are merged in fp32 (2^-24 an
+    addition: 2^-11 for both)."""
+    g = gen(26)
+    n, rpp, H = (1 << 31) - 128, 4096, 16
+    pages = -(-n // rpp)
+    c = Cache.__new__(Cache)
+    c.rpp, c.pitch, c.width, c.B, c.n_pages = rpp, rpp, pages, 1, 3
+    c.pool = (randn(g, 3 * rpp, D).float() + 0.5).to(torch.bfloat16)
+    c.table = (torch.arange(pages, dtype=torch.int32, device="cuda") % 3).view(1, -1).contiguous()
+    q = randn(g, 1, H, D)
+    if call == "prefix":
+        first = 0
+        out, lse = prefix(m, q, c, 64, [n])
+    else:
+        first = n - (1 << 30)
+        out, lse = window(m, q, c, [1], [n], 1 << 30, 0)
+    assert m.csa_read_device_status() == 0
+    count = torch.zeros(3 * rpp, dtype=torch.float64, device="cuda")  # how often a row is attended
+    whole, last = first // rpp + 1, pages - 1                         # pages attended as a whole: [whole, last)
+    for p in range(3):
+        count[p * rpp:(p + 1) * rpp] = (last - p + 2) // 3 - (whole - p + 2) // 3
+    count[whole % 3 * rpp - rpp + first % rpp if whole % 3 else 2 * rpp + first % rpp:
+          whole % 3 * rpp if whole % 3 else 3 * rpp] += 1             # page whole - 1 from `first` on
+    count[last % 3 * rpp:last % 3 * rpp + (n - last * rpp)] += 1
+    assert int(count.sum()) == n - first
+    kv, qd = c.pool.double(), q[0].double()
+    x = SCALE * (qd @ kv.t()) + torch.log(count)
+    want = torch.logsumexp(x, -1)
+    w = torch.exp(x - want[:, None])
+    o, a = w @ kv, w @ kv.abs()
+    d = 2.0**-14 * SCALE * (qd.abs() @ kv.abs().t()).amax(-1)
+    check(out[0], lse[0], (o, want, 2.0**-8 * (2 * a + o.abs()) + (2 * d[:, None] + 2.0**-11) * a,
+                           d + 2.0**-20 * (1 + want.abs()) + 2.0**-11), call)
+
+
 def test_window_attention_offsets_that_fall_and_rise(m):
     """Offsets that are not non-decreasing are reported, and the call ends: sequences that overlap because of
     them are not all computed."""
