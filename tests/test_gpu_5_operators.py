@@ -718,6 +718,36 @@ def test_pages_fork(m, n_pages, tokens, src, rpp):
     assert m.csa_read_device_status() == 0
 
 
+@pytest.mark.parametrize("n_pages,F", [(64, 1), (64, 8), (500, 9), (500, 16), (500, 17), (3000, 100), (32768, 3),
+                                       (32769, 3), (40000, 16)])
+def test_pages_fork_of_any_number(m, n_pages, F):
+    """Pools that every scan CTA counts by itself (up to 32,768 pages) and larger ones, one child and many."""
+    test_pages_fork(m, n_pages, [40, 33], [i % 2 for i in range(F)], 16)
+
+
+@pytest.mark.parametrize("n_pages,free", [(32768, 3), (32768, 2), (20000, 16), (8193, 1), (70000, 5), (31, 0)])
+def test_pages_fork_in_a_pool_almost_full(m, n_pages, free):
+    """The free pages are the last ones of the pool, and there are as many as children, fewer, or more."""
+    F = 4
+    refs = [1] * (n_pages - free) + [0] * free
+    mod = Model(refs, [[0, 1, -1]] + [[-1] * 3 for _ in range(F)])
+    n = [6] + [0] * F
+    r, t, nt = i32(mod.refs), i32(mod.table), torch.tensor(n, dtype=torch.int64, device="cuda")
+    pools = pools_of(n_pages)
+    m.csa_pages_fork(m.page_pools(pools, n_pages), r, t, 3, F + 1, i32([0] * F), i32([1, 2, 3, 4]), F, nt, 4)
+    for f in range(F):
+        mod.refs[0] += 1
+        if f < free:
+            mod.refs[n_pages - free + f] = 1
+        mod.table[1 + f] = [0, n_pages - free + f if f < free else -1, -1]
+        n[1 + f] = 6 if f < free else 4
+    assert r.tolist() == mod.refs and t.tolist() == mod.table and nt.tolist() == n
+    for p in pools:
+        for f in range(min(free, F)):
+            assert torch.equal(p[n_pages - free + f], p[1])
+    assert m.csa_read_device_status() == (0 if free >= F else NO_PAGES)
+
+
 def test_pages_fork_refusals_on_the_device(m):
     """Rows outside the table, a child that is a parent, a row twice, tokens that do not fit, a page id
     outside the pool, no free page: reported, and the other children are as if alone."""
