@@ -1276,8 +1276,8 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
                            size_t ws_bytes, void* stream) {
     csa_status rc = check_window(B, H, total_q, max_q, window, n_sink);
     if (rc) return rc;
-    if (!q || !al16(q) || !out || !al16(out) || (lse && !al4(lse)) || !q_offsets || !al8(q_offsets) || !n_tokens ||
-        !al8(n_tokens))
+    if ((total_q > 0 && (!q || !out)) || !al16(q) || !al16(out) || (lse && !al4(lse)) || !q_offsets || !al8(q_offsets) ||
+        !n_tokens || !al8(n_tokens))
         return CSA_ERR_INVALID_ARG;
     if ((rc = check_cache(kv_raw, page_table_stride))) return rc;
     LatArgs a = {};

@@ -476,7 +476,7 @@ csa_status csa_pages_free(int32_t* refs, int64_t n_pages, int32_t* page_table, i
                           const int32_t* rows, int32_t R, void* stream) {
     csa_status rc = check_table(refs, n_pages, page_table, table_stride, B);
     if (rc) return rc;
-    if (!rows || !al4(rows) || R < 0) return CSA_ERR_INVALID_ARG;
+    if (R < 0 || (R > 0 && !rows) || !al4(rows)) return CSA_ERR_INVALID_ARG;
     if (R > 65535) return CSA_ERR_UNSUPPORTED;
     if (R == 0) return CSA_OK;
     int32_t* st = device_status_ptr();
@@ -496,7 +496,7 @@ csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* p
     csa_status rc = check_pools(pools, &a.pools);
     if (rc) return rc;
     if ((rc = check_table(refs, pools->n_pages, page_table, table_stride, B))) return rc;
-    if (!src || !al4(src) || !dst || !al4(dst) || !n_tokens || !al8(n_tokens) || rows_per_page < 1 || F < 0)
+    if (F < 0 || (F > 0 && (!src || !dst)) || !al4(src) || !al4(dst) || !n_tokens || !al8(n_tokens) || rows_per_page < 1)
         return CSA_ERR_INVALID_ARG;
     if (F > 1024) return CSA_ERR_UNSUPPORTED;
     if ((rc = check_ws(workspace, ws_bytes, pools->n_pages))) return rc;

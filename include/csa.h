@@ -289,7 +289,7 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
  * 1 <= H <= 128, 1 <= B <= 65535, 1 <= window <= 2^30, 0 <= n_sink <= 2^30, 0 <= total_q,
  * total_q * H < 2^31 (else CSA_ERR_UNSUPPORTED), 1 <= max_q; the limits of csa_prefix_attn on kv.
  * workspace: 16-byte aligned, csa_window_attn_workspace_size(...) bytes, contents overwritten
- * (0 bytes where no key range is split).  Graph capture: yes.
+ * (0 bytes where no key range is split).  With total_q = 0 q and out may be null.  Graph capture: yes.
  */
 size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
                                       int32_t n_sink);
@@ -306,7 +306,7 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
  * lowest ids.  Nothing here waits for the host; every result is the same from run to run.  Calls on
  * one refs array belong on one stream, or need events between them.
  * workspace (alloc, fork, compact): 16-byte aligned, at least csa_pages_workspace_size(n_pages) bytes,
- * contents overwritten.  1 <= n_pages <= 2^28, 1 <= B <= 65535, 1 <= table_stride <= 2^31 - 1 and
+ * contents overwritten.  Lists of no entries may be null.  1 <= n_pages <= 2^28, 1 <= B <= 65535, 1 <= table_stride <= 2^31 - 1 and
  * B * table_stride <= 2^40.  Graph capture: yes.
  */
 #define CSA_POOLS_MAX 4
@@ -345,7 +345,7 @@ csa_status csa_pages_free(int32_t* refs, int64_t n_pages, int32_t* page_table, i
  * before are overwritten: give them back first (csa_pages_free).  A child is skipped
  * (CSA_ERR_DEVICE_BOUNDS) where a row is outside the table, dst[f] is a parent of this call or another
  * child's row, or the parent's tokens do not fit its row; a page id outside the pool becomes -1
- * (CSA_ERR_DEVICE_BOUNDS).  1 <= F <= 1024. */
+ * (CSA_ERR_DEVICE_BOUNDS).  0 <= F <= 1024. */
 csa_status csa_pages_fork(const csa_page_pools* pools, int32_t* refs, int32_t* page_table, int64_t table_stride,
                           int32_t B, const int32_t* src, const int32_t* dst, int32_t F, int64_t* n_tokens,
                           int32_t rows_per_page, void* workspace, size_t ws_bytes, void* stream);

@@ -135,6 +135,21 @@ def test_prefix_attention(m, H, shared, n_rows, rpp):
     assert torch.equal(out, again) and torch.equal(lse, lse2)  # the same bits
 
 
+def test_attention_over_nothing(m):
+    """No rows at all: outputs of zero and lse -inf; no new tokens: nothing is written."""
+    g = gen(7)
+    c = Cache(g, [10, 10], 16)
+    q = randn(g, 2, 5, D)
+    out, lse = prefix(m, q, c, 0, [0, 0])
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    out, lse = prefix(m, q, c, 9, [0, 0])
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    out, lse = window(m, q[:0], c, [0, 0], [10, 0], 16, 2)
+    out, lse = window(m, q, c, [0, 0], [10, 0], 16, 2)
+    assert bool((out == 7).all()) and bool((lse == 7).all())
+    assert m.csa_read_device_status() == 0
+
+
 def test_prefix_attention_with_page_gaps_and_without_lse(m):
     """Pages 1.25 rows' pitch apart; no lse wanted; large logits (weights close to one-hot)."""
     g = gen(2)

@@ -127,6 +127,17 @@ def test_pages_refusals(csa):
     assert cp(None, A4, A4, 1, None) == inv and cp(ctypes.byref(pools(csa)), None, None, 0, None) == csa.CSA_OK
 
 
+def test_calls_of_nothing(csa):
+    """Empty tensors have null pointers: nothing to do is no error."""
+    L = csa.lib()
+    pools = csa.csa_page_pools(1, 10, (0x10000,), (1024,), (1024,))
+    assert L.csa_window_attn(None, 16, 0.04, kv(csa), 10, 2, A16, A16, 0, 1, 128, 4, None, None, None, 0, None) == 0
+    assert L.csa_pages_free(A16, 10, A16, 5, 2, None, 0, None) == 0
+    assert L.csa_pages_fork(ctypes.byref(pools), A16, A16, 5, 2, None, None, 0, A16, 64, A16, 1 << 20, None) == 0
+    assert L.csa_pages_copy(ctypes.byref(pools), None, None, 0, None) == 0
+    assert L.csa_pages_free(A16, 10, A16, 5, 2, None, 1, None) == csa.CSA_ERR_INVALID_ARG
+
+
 def test_page_pools_struct_matches_the_header(csa, tmp_path):
     import os
     import shutil
