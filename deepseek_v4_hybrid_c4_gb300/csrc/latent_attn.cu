@@ -120,6 +120,10 @@ struct LatArgs {
     int n_shared, max_rows;
     int RT, SP, OS;            // row tiles over the batch; splits of the shared rows, of a request's own rows
     FastDiv by_RT, by_SP, by_OS, by_WS;
+    // prefix, in runs (run > 0): the row tiles' shared tiles, the first tS of every gS places, and the requests' own ones,
+    // tO of every gO, are each laid end to end and cut every `run` places: NS runs of the first, then those of the second
+    int run, NS, tS, gS, tO, gO;
+    FastDiv by_run, by_gS, by_gO;
     // window: B sequences
     const int64_t* q_offsets;
     const int64_t* n_tokens;
@@ -166,6 +170,7 @@ struct SeqCursor {
     int c0 = -32, base = 0, total = 0;
     int incl = 0, tiles = 0, ql = 0;
     int64_t q0 = 0, nt = 0;
+    int pos = -1, end = 0, run = 0;  // a run: the next place, the end, its number among the runs of its kind
 };
 
 __device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t q1, int64_t nt) {
@@ -179,17 +184,49 @@ template <bool WINDOW>
 __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
     int split, splits;
     FastDiv by;
+    int first = 0, last = 0;  // tiles of a run's item
     if (!WINDOW) {
-        if (it >= a.RT * a.SP + a.B * a.OS) return false;
-        int kb0, kb1;
-        x.shared = it < a.RT * a.SP;
+        int kb0, kb1, seg;
+        if (a.run) {
+            if (cur.pos < 0) {
+                cur.run = it < a.NS ? it : it - a.NS;
+                cur.pos = cur.run * a.run;
+                cur.end = min(cur.pos + a.run, it < a.NS ? a.RT * a.gS : a.B * a.gO);
+                cur.total = it < a.NS;
+            }
+            x.shared = cur.total;
+            const int g = x.shared ? a.gS : a.gO, t = x.shared ? a.tS : a.tO;
+            const FastDiv by_g = x.shared ? a.by_gS : a.by_gO;
+            seg = div_by(cur.pos, by_g);
+            if (cur.pos - seg * g >= t) cur.pos = ++seg * g;
+            if (cur.pos >= cur.end) return false;
+            first = cur.pos - seg * g;
+            last = min(first + cur.end - cur.pos, t);
+            cur.pos += last - first;
+            split = cur.run - div_by(seg * g, a.by_run);
+            splits = 0;
+            by = a.by_run;
+        } else {
+            if (it >= a.RT * a.SP + a.B * a.OS) return false;
+            x.shared = it < a.RT * a.SP;
+            if (x.shared) {  // neighbouring items read the same keys
+                split = div_by(it, a.by_RT);
+                splits = a.SP;
+                by = a.by_SP;
+                seg = it - split * a.RT;
+            } else {
+                const int j = it - a.RT * a.SP;
+                seg = div_by(j, a.by_OS);
+                split = j - seg * a.OS;
+                splits = a.OS;
+                by = a.by_OS;
+            }
+            first = split;  // (0 once a request)
+        }
         x.a1 = x.uA = x.rr0 = 0;
         x.pos0 = 0;
-        if (x.shared) {  // neighbouring items read the same keys
-            split = div_by(it, a.by_RT);
-            splits = a.SP;
-            by = a.by_SP;
-            x.row0 = (it - split * a.RT) * 128;
+        if (x.shared) {
+            x.row0 = seg * 128;
             x.nrows = min(128, a.rows - x.row0);
             x.trow = 0;
             x.part = split;
@@ -212,16 +249,13 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
             x.full_hi = mn;
             x.nU = ceil_div(a.n_shared, 16);  // the same split of the keys for every row tile
         } else {
-            const int j = it - a.RT * a.SP, b = div_by(j, a.by_OS);
-            split = j - b * a.OS;
-            splits = a.OS;
-            by = a.by_OS;
+            const int b = seg;
             x.row0 = b * a.H;
             x.nrows = a.H;
             x.trow = b;
             x.part = a.SP + split;
             const int64_t n = __ldg(a.n_rows + b);
-            if (report && lane == 0 && split == 0 && (n < 0 || n > a.max_rows))
+            if (report && lane == 0 && first == 0 && (n < 0 || n > a.max_rows))
                 raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
             kb0 = a.n_shared;
             kb1 = n < 0 ? 0 : (n > a.max_rows ? a.max_rows : (int)n);
@@ -285,9 +319,14 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
         x.full_hi = p0 >= 0 ? (int)p0 + 1 : 0;
     }
     const int tiles = ceil_div(x.nU, 8);
-    const int each = div_by(tiles, by), more = tiles - each * splits;  // the first `more` splits take one more
-    x.t0 = split * each + min(split, more);
-    x.T = each + (split < more ? 1 : 0);
+    if (!WINDOW && a.run) {
+        x.t0 = first;
+        x.T = max(min(last, tiles) - first, 0);
+    } else {
+        const int each = div_by(tiles, by), more = tiles - each * splits;  // the first `more` splits take one more
+        x.t0 = split * each + min(split, more);
+        x.T = each + (split < more ? 1 : 0);
+    }
     if (x.shared && x.t0 * 128 >= x.hi) x.T = 0;
     return true;
 }
@@ -1006,11 +1045,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LP_T, 1)
 }
 
 // Log-sum-exp merge of a row's partial results, in their order: one CTA per row, thread t columns
-// 4t .. 4t+3, IN partial rows in flight: 8, or 16 where there are more (32 requests of 16 heads, 30 partial results of a
-// row: 70.1 -> 66.0 us in all; 16 for everyone costs 4,096 rows of 8 partial results 3 percent, as fewer CTAs
+// 4t .. 4t+3, IN partial rows in flight: 8, or 16 where there may be more (32 requests of 16 heads, 30 partial results
+// of a row: 70.1 -> 66.0 us in all; 16 for everyone costs 4,096 rows of 8 partial results 3 percent, as fewer CTAs
 // fit an SM).  Window: rows that no sequence covers are left alone.
 template <int IN>
-__global__ void __launch_bounds__(128) lat_merge_kernel(LatArgs a) {
+__global__ void __launch_bounds__(128, IN > 8 ? 4 : 8) lat_merge_kernel(LatArgs a) {
     pdl_wait();
     const int row = blockIdx.x, t = threadIdx.x;
     if (!a.n_rows) {
@@ -1024,19 +1063,28 @@ __global__ void __launch_bounds__(128) lat_merge_kernel(LatArgs a) {
         const int64_t q0 = __ldg(a.q_offsets + l), q1 = __ldg(a.q_offsets + l + 1);
         if (q < q0 || q >= q1 || !seq_valid(a, q0, q1, __ldg(a.n_tokens + l))) return;
     }
+    // the row's partial results: all, or those of the runs that its row tile and its request lie in
+    int n = a.parts, n_first = a.parts, skip = 0;
+    if (a.run) {
+        const int p = (row >> 7) * a.gS, o = div_by(row, a.by_H) * a.gO;
+        n_first = a.tS ? div_by(p + a.tS - 1, a.by_run) - div_by(p, a.by_run) + 1 : 0;
+        n = n_first + (a.tO ? div_by(o + a.tO - 1, a.by_run) - div_by(o, a.by_run) + 1 : 0);
+        skip = a.SP - n_first;
+    }
     // (the maximum so far is kept as a running one)
     const float* lp = a.part_lse + row;
     const float4* op = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * D) + t;
     const int64_t step = (int64_t)a.rows;
     float M = -INFINITY, L = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
     bool nan = false;
-    for (int s0 = 0; s0 < a.parts; s0 += IN) {
+    for (int s0 = 0; s0 < n; s0 += IN) {
         float v[IN];
         float4 f[IN];
 #pragma unroll
         for (int s = 0; s < IN; ++s) {
-            v[s] = s0 + s < a.parts ? __ldcg(lp + (s0 + s) * step) : -INFINITY;
-            if (s0 + s < a.parts) f[s] = __ldcg(op + (s0 + s) * step * (D / 4));
+            const int64_t at = (s0 + s < n_first ? s0 + s : s0 + s + skip) * step;
+            v[s] = s0 + s < n ? __ldcg(lp + at) : -INFINITY;
+            if (s0 + s < n) f[s] = __ldcg(op + at * (D / 4));
         }
         float m = M;
 #pragma unroll
@@ -1124,8 +1172,9 @@ static int64_t deal_cost(int64_t n1, int64_t t1, int64_t n2, int64_t t2) {
     return worst;
 }
 
-// The splits of the shared rows (SP) and of a request's own (OS) that end soonest; a partial result of every
-// row, written and read again, costs about 1.4 tiles for each 4,096 rows.
+// How the tiles are dealt to the pairs: the splits of the shared rows (SP) and of a request's own (OS) that end
+// soonest, or runs (then SP and OS are the most partial results that a row has of each); a partial result of every row,
+// written and read again, costs about 1.4 tiles for each 4,096 rows.
 static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArgs* a) {
     a->rows = B * H;
     a->RT = (a->rows + 127) / 128;
@@ -1139,12 +1188,37 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
     const int sp_most = std::max(sp_least, std::min(tiles, LP_PAIRS));
     for (int sp = sp_least; sp <= sp_most; ++sp) {
         // a request's own rows: whole, or in pieces as long as the shared ones
-        const int piece = sp ? std::max(4, (tiles + sp - 1) / sp) : (int)std::max<int64_t>(2, ((int64_t)own * B + LP_PAIRS - 1) / LP_PAIRS);
+        const int piece = sp ? std::max(4, (tiles + sp - 1) / sp)
+                             : (int)std::max<int64_t>(2, ((int64_t)own * B + LP_PAIRS - 1) / LP_PAIRS);
         const int os = std::max(os_least, own ? std::min((own + piece - 1) / piece, os_most) : 0);
         const double c = (double)deal_cost((int64_t)a->RT * sp, sp ? (tiles + sp - 1) / sp : 0, (int64_t)B * os,
                                            os ? (own + os - 1) / os : 0) +
                          (sp + os > 1 ? 1.4 * (sp + os) * a->rows / 4096.0 + 0.02 * (sp + os) : 0.0);
         if (c < best) best = c, a->SP = sp, a->OS = os;
+    }
+    // Or in runs, one for each pair: all of one length and with fewer partial results a row, at the price of items that
+    // end in a run's midst and of row tiles that read the same keys at different times.  Behind each row tile's or
+    // request's tiles are places that stand for an item's cost beside its tiles (three and two: 158 and 60.6 us for
+    // the two cases below; three and three 158 and 62.4, two and two 159 and 61.3, one and one 171 and 62.3).
+    // 32 requests of 128 heads over 32K rows + 300: 171.6 us in splits, 158.0 in runs; of 16 heads over 64K + 2K: 65.3
+    // and 60.6; where the splits come out even (8 x 128 over 8K + 512, one item a pair) they are the faster by the same rule.
+    const int64_t gS = tiles ? tiles + 3 : 0, gO = own ? own + 2 : 0, inS = a->RT * gS, inO = B * gO;
+    if (inS + inO >= 4 * LP_PAIRS && std::max(inS, inO) < 1 << 30) {
+        int64_t C = (inS + inO + LP_PAIRS - 1) / LP_PAIRS;
+        while ((inS + C - 1) / C + (inO + C - 1) / C > LP_PAIRS) C += 1 + C / 256;
+        const int PS = tiles ? (int)((tiles + C - 2) / C) + 1 : 0, PO = own ? (int)((own + C - 2) / C) + 1 : 0;
+        const double c = C + 3 + 1.4 * ((tiles + own) / (double)C + (tiles > 0) + (own > 0)) * a->rows / 4096.0 +
+                         0.02 * (PS + PO);
+        if (C <= LP_MAX_TILES && c < best) {
+            a->SP = PS;
+            a->OS = PO;
+            a->run = (int)C;
+            a->NS = (int)((inS + C - 1) / C);
+            a->tS = tiles;
+            a->gS = (int)gS;
+            a->tO = own;
+            a->gO = (int)gO;
+        }
     }
     if (a->SP + a->OS == 0) a->OS = 1;  // no rows at all: every request is empty
     a->parts = a->SP + a->OS;
@@ -1184,6 +1258,9 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     a.by_SP = fast_div(std::max(a.SP, 1));
     a.by_OS = fast_div(std::max(a.OS, 1));
     a.by_WS = fast_div(std::max(a.WS, 1));
+    a.by_run = fast_div(std::max(a.run, 1));
+    a.by_gS = fast_div(std::max(a.gS, 1));
+    a.by_gO = fast_div(std::max(a.gO, 1));
     const int sms = device_sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
     a.rpp_shift = -1;
@@ -1249,7 +1326,9 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
     plan_prefix(B, H, n_shared, max_rows, &a);
     const size_t need = parts_bytes(a);
     if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
-    if ((int64_t)a.RT * a.SP + (int64_t)B * a.OS > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
+    int64_t items = (int64_t)a.RT * a.SP + (int64_t)B * a.OS;
+    if (a.run) items = a.NS + ((int64_t)B * a.gO + a.run - 1) / a.run;
+    if (items > 0x7FFFFFFF) return CSA_ERR_UNSUPPORTED;
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
@@ -1262,8 +1341,7 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
     a.max_rows = (int)max_rows;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
-    return from_cuda(launch_pair(a, q, kv, (int64_t)a.RT * a.SP + (int64_t)B * a.OS, workspace,
-                                 static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_pair(a, q, kv, items, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,

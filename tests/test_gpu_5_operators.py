@@ -135,6 +135,20 @@ def test_prefix_attention(m, H, shared, n_rows, rpp):
     assert torch.equal(out, again) and torch.equal(lse, lse2)  # the same bits
 
 
+RUNS = [  # H, shared, rows of each request, rows per page: many tiles, cut in runs of one length
+    (16, 20000, [20000 + (i * 97) % 2000 for i in range(32)], 64),
+    (128, 3000, [3000 + 13 * i for i in range(20)], 32),
+    (128, 6000, [6000] * 12, 64),                       # nothing of their own
+    (64, 0, [1200 + 31 * i for i in range(40)], 64),    # nothing shared
+    (33, 5000, [0, 700, 5000, 5001] + [5000 + 300 * i for i in range(30)], 40),
+]
+
+
+@pytest.mark.parametrize("H,shared,n_rows,rpp", RUNS)
+def test_prefix_attention_in_runs(m, H, shared, n_rows, rpp):
+    test_prefix_attention(m, H, shared, n_rows, rpp)
+
+
 def test_attention_over_nothing(m):
     """No rows at all: outputs of zero and lse -inf; no new tokens: nothing is written."""
     g = gen(7)
