@@ -16,7 +16,7 @@
 // a tile against 2,048 at the nominal rate.
 //
 // What bounds it.  Many query rows over a long prefix: the tensor cores under the power limit (4,096 rows over
-// 32K keys, 276 GFLOP: 172 us, 1.6 PFLOP/s; fewer cycles a tile only lowered the clock).  A prompt under a
+// 32K keys, 276 GFLOP: 158 us with the same inputs again, 181 us with others, 1.53 PFLOP/s).  A prompt under a
 // short window: the softmax warps' chain through an item (8,192 tokens of 128 heads, window 128: 459 us, 4.7 TB/s
 // of queries and outputs; 40 percent of an item is its output).  Single tokens: one chain of dependent loads,
 // products and stores, 9 to 11 us.
