@@ -81,9 +81,9 @@ constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row 
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
 constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of the threads
 constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
-constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] bit 0: plain (tile_plain); bit 8 + u: unit u's
-                                                          // rows lie one behind the other (gathers)
-constexpr uint32_t LP_SMEM = LP_SM_PLAIN + 32 + 1024;     // + alignment slack
+constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] plain (tile_plain)
+constexpr uint32_t LP_SM_NEXT = LP_SM_PLAIN + 32;         // [8 tiles] gathers: which quads' rows follow each other
+constexpr uint32_t LP_SMEM = LP_SM_NEXT + 128 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
 // Tiles of a split at most: O takes eight additions a tile in the tensor cores, each of which may lose 2^-23 of the
@@ -113,7 +113,7 @@ struct LatArgs {
     uint32_t negate;           // instruction-descriptor bit that negates Q
     DPaged kv;
     int64_t table_pages;       // entries of a request's page table
-    int rpp_shift;             // log2 of the rows per page, -1 where they are no power of two
+    FastDiv by_rpp;
     int B;
     // prefix: request b = row / H sees rows [0, n_rows[b]); rows below n_shared through table row 0
     const int64_t* n_rows;     // nullptr: window
@@ -413,24 +413,34 @@ __device__ __forceinline__ void store_sector(uint8_t* p, const uint32_t* w, bool
     }
 }
 
-// Page of logical row j of the item's request and j's row in it; -1 where there is no page (or none inside the pool).
-__device__ __forceinline__ int lat_page(const LatArgs& a, const int32_t* pt, int j, int& slot) {
-    const uint32_t lp = a.rpp_shift >= 0 ? (uint32_t)j >> a.rpp_shift : (uint32_t)j / (uint32_t)a.kv.rpp;
-    slot = j - (int)lp * a.kv.rpp;
-    int pp = -1;
-    if ((int64_t)lp < a.table_pages) pp = __ldg(pt + lp);
-    if (pp < 0 || pp >= a.kv.n_pages) {
-        raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
-        return -1;
-    }
-    return pp;
+// Page-table entry of logical row j of the item's request (-1 behind the table) and j's row in its page.
+__device__ __forceinline__ int lat_entry(const LatArgs& a, const int32_t* pt, int j, int& slot) {
+    const int lp = div_by(j, a.by_rpp);
+    slot = j - lp * a.kv.rpp;
+    return lp < a.table_pages ? __ldg(pt + lp) : -1;
 }
 
 // The cache's tensor maps: boxes of 64 dims and [0] 16, [1] 32, [2] 64 rows of a page, or, over all rows of the
-// pool, [0] one row (gathers) and [1] 16 rows.
+// pool, [0] one row (gathers) and [1] 8, [2] 16, [3] 32 rows.
 struct KeyMaps {
-    CUtensorMap m[3];
+    CUtensorMap m[4];
 };
+
+// Caches read by gathers, quad q (rows 4q .. 4q+3 of a tile): the map of its copy, -1 where another quad's copy takes
+// its rows along.  Boxes of 32, 16 and 8 rows where two units, a unit or half of one lie row behind row in memory, a
+// gather for any four rows.  Bits at the run's first quad (LP_SM_NEXT); q0: the copying warp's first quad; two: it
+// copies both units of the pair.  (Pages of 40 rows, a window of 512: 91.9 us
+// with 16-row boxes and gathers only, 90.0 so.)
+struct QuadRuns {
+    uint32_t half, unit, pair;
+};
+__device__ __forceinline__ int quad_map(QuadRuns n, int q, int q0, bool two) {
+    const int u = q & ~3, p = q0 + ((q - q0) & ~7);  // the quad's unit, and pair of units
+    if (two && (n.pair >> p) & 1u) return q == p ? 3 : -1;
+    if ((n.unit >> u) & 1u) return q == u ? 2 : -1;
+    if ((n.half >> (q & ~1)) & 1u) return q & 1 ? -1 : 1;
+    return 0;
+}
 
 template <bool BOX, bool WINDOW>
 __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps& km, const LatArgs& a) {
@@ -532,7 +542,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     if (c < nc) tc_ld16(ts + 16 * c, sr + 16 * c);
-                const bool plain = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4) & 1u;
+                const bool plain = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4) != 0;
                 tc_wait_ld();
                 float mt = -INFINITY;  // of the logits before scaling
                 bool bad = false;
@@ -869,11 +879,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 if (g >= 4) ok = lat_wait(sb + LP_USED + 8 * ((g - 4) & 7), ((g - 4) >> 3) & 1, dead);
                 uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + slot * 4;
                 int* look = reinterpret_cast<int*>(sm + LP_SM_LOOK) + slot * 128;
-                uint32_t whole = 0;  // bit u: unit u's rows lie one behind the other
                 if (BOX) {
                     int pg = -1, rw = 0;
                     const int j = u0 + lane < x.nU && lane < 8 ? unit_row<WINDOW>(x, u0 + lane) : x.hi;
-                    if (j < x.hi) pg = lat_page(a, pt, j, rw);  // (a unit behind the last row that is seen: none)
+                    if (j < x.hi) {  // (a unit behind the last row that is seen: none)
+                        pg = lat_entry(a, pt, j, rw);
+                        if (pg < 0 || pg >= a.kv.n_pages) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS), pg = -1;
+                    }
                     const uint32_t b = __ballot_sync(0xffffffffu, pg >= 0);
                     const uint32_t b2 = b >> (2 * lane);
                     if (lane < 4) vw[lane] = (b2 & 1 ? 0xFFFFu : 0u) | (b2 & 2 ? 0xFFFF0000u : 0u);
@@ -887,26 +899,35 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                     if (lane == 0) look[16] = (int)runs;
                 } else {
-                    int id[4];
-                    uint32_t v = 0;
+                    int id[4], pg[4], rw[4];
+                    uint32_t v = 0, seen = 0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // rows of a unit that no query sees are not looked up
                         const int k = lane * 4 + e, u = u0 + (k >> 4);
                         const int j = u < x.nU ? unit_row<WINDOW>(x, u) + (k & 15) : -1;
-                        int rw, pg = -1;
-                        if (j >= 0 && ((WINDOW && j < x.a1) || (j >= x.lo && j < x.hi))) pg = lat_page(a, pt, j, rw);
-                        id[e] = pg >= 0 ? pg * (int)(a.kv.page_stride / ROW_BYTES) + rw : 0;
-                        if (pg >= 0) v |= 1u << (4 * (lane & 7) + e);
+                        if (j >= 0 && ((WINDOW && j < x.a1) || (j >= x.lo && j < x.hi))) seen |= 1u << e;
+                        pg[e] = (seen >> e) & 1u ? lat_entry(a, pt, j, rw[e]) : -1;
                     }
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // (after all four loads)
+                        const bool there = pg[e] >= 0 && pg[e] < a.kv.n_pages;
+                        bad = bad || (!there && ((seen >> e) & 1u));
+                        id[e] = there ? pg[e] * (int)(a.kv.page_stride / ROW_BYTES) + rw[e] : 0;
+                        if (there) v |= 1u << (4 * (lane & 7) + e);
+                    }
+                    if (bad) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
                     *reinterpret_cast<int4*>(look + 4 * lane) = make_int4(id[0], id[1], id[2], id[3]);
+                    // bit q: quad q's rows follow each other; the next quad's follow them
                     const int behind = __shfl_down_sync(0xffffffffu, id[0], 1);
                     const bool all4 = ((v >> (4 * (lane & 7))) & 15u) == 15u;
-                    const uint32_t b = __ballot_sync(0xffffffffu, all4 && id[1] == id[0] + 1 && id[2] == id[0] + 2 &&
-                                                                      id[3] == id[0] + 3 &&
-                                                                      ((lane & 3) == 3 || behind == id[0] + 4));
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (((b >> (4 * u)) & 15u) == 15u) whole |= 256u << u;
+                    const uint32_t in = __ballot_sync(0xffffffffu, all4 && id[1] == id[0] + 1 && id[2] == id[0] + 2 &&
+                                                                       id[3] == id[0] + 3);
+                    const uint32_t to = __ballot_sync(0xffffffffu, lane < 31 && behind == id[0] + 4);
+                    const uint32_t half = in & (in >> 1) & to, unit = half & (to >> 1) & (half >> 2);
+                    if (lane == 0)
+                        *reinterpret_cast<uint4*>(sm + LP_SM_NEXT + slot * 16) =
+                            make_uint4(half, unit, unit & (to >> 3) & (unit >> 4), 0);
                     v |= __shfl_xor_sync(0xffffffffu, v, 1);
                     v |= __shfl_xor_sync(0xffffffffu, v, 2);
                     v |= __shfl_xor_sync(0xffffffffu, v, 4);
@@ -914,7 +935,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    plain[slot] = whole | (tile_plain<WINDOW>(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u);
+                    plain[slot] = tile_plain<WINDOW>(x, i, *reinterpret_cast<const uint4*>(vw)) ? 1u : 0u;
                     mbar_arrive(sb + LP_LOOK + 8 * slot);
                 }
                 if (i == 0 && n > 0) load_q(n);  // behind the first tile's lookups, as it may have to wait
@@ -964,12 +985,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         } else {
                             const int slab = lane >> 4, qd = lane & 15;
                             const uint4 id = ld_shared_v4(look + 16 * ((first * 4 + qd) & 31));
-                            const uint32_t whole = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) >> (8 + first);
+                            const uint4 nx = ld_shared_v4(sb + LP_SM_NEXT + (gt & 7) * 16);
+                            const int how = quad_map({nx.x, nx.y, nx.z}, first * 4 + qd, first * 4, (qd >> 2 | 1) < ku);
                             ok = ok && claim((uint32_t)nu * 4096u);
-                            const bool there = ok && qd < 4 * ku, box = (whole >> (qd >> 2)) & 1u;
-                            if (there && box && !(qd & 3))
-                                tma_load_2d_pair(dst + slab * 8192 + qd * 512, &km.m[1], (2 * kk + slab) * 64, (int)id.x, bar);
-                            if (there && !box)
+                            if (ok && qd < 4 * ku && how > 0)
+                                tma_load_2d_pair(dst + slab * 8192 + qd * 512, &km.m[how], (2 * kk + slab) * 64, (int)id.x,
+                                                 bar);
+                            if (ok && qd < 4 * ku && how == 0)
                                 tma_gather4_pair(dst + slab * 8192 + qd * 512, &km.m[0], (2 * kk + slab) * 64,
                                                  make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
                         }
@@ -1002,12 +1024,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         } else {
                             const int s = lane >> 3, qd = lane & 7;
                             const uint4 id = ld_shared_v4(look + 16 * ((v * 8 + qd) & 31));
-                            const uint32_t whole = ld_shared_u32(sb + LP_SM_PLAIN + (gt & 7) * 4) >> (8 + 2 * v);
+                            const uint4 nx = ld_shared_v4(sb + LP_SM_NEXT + (gt & 7) * 16);
+                            const int how = quad_map({nx.x, nx.y, nx.z}, v * 8 + qd, v * 8, vu == 2);
                             ok = ok && claim((uint32_t)vu * 16384u);
-                            const bool there = ok && qd < 4 * vu, box = (whole >> (qd >> 2)) & 1u;
-                            if (there && box && !(qd & 3))
-                                tma_load_2d_pair(dst + s * 4096 + qd * 512, &km.m[1], (int)rank * 256 + s * 64, (int)id.x, bar);
-                            if (there && !box)
+                            if (ok && qd < 4 * vu && how > 0)
+                                tma_load_2d_pair(dst + s * 4096 + qd * 512, &km.m[how], (int)rank * 256 + s * 64, (int)id.x,
+                                                 bar);
+                            if (ok && qd < 4 * vu && how == 0)
                                 tma_gather4_pair(dst + s * 4096 + qd * 512, &km.m[0], (int)rank * 256 + s * 64,
                                                  make_int4((int)id.x, (int)id.y, (int)id.z, (int)id.w), bar);
                         }
@@ -1254,6 +1277,7 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     }
     a.wide_out = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     a.by_H = fast_div(a.H);
+    a.by_rpp = fast_div((uint32_t)kv.rows_per_page);
     a.by_RT = fast_div(std::max(a.RT, 1));
     a.by_SP = fast_div(std::max(a.SP, 1));
     a.by_OS = fast_div(std::max(a.OS, 1));
@@ -1263,9 +1287,6 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
     a.by_gO = fast_div(std::max(a.gO, 1));
     const int sms = device_sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
-    a.rpp_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (kv.rows_per_page == 1 << i) a.rpp_shift = i;
     CUtensorMap qm;
     KeyMaps km = {};
     const uint64_t qd[2] = {(uint64_t)D, (uint64_t)a.rows}, qs[1] = {ROW_BYTES};
@@ -1283,8 +1304,8 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
         const uint64_t per_page = (uint64_t)(kv.page_stride_bytes / ROW_BYTES);
         const uint64_t d[2] = {(uint64_t)D, (uint64_t)(kv.n_pages - 1) * per_page + (uint64_t)kv.rows_per_page};
         const uint64_t st[1] = {ROW_BYTES};
-        for (int i = 0; i < 2 && (i == 0 || d[1] >= 16); ++i) {  // (fewer than 16 rows: no unit is copied as a box)
-            const uint32_t b[2] = {64, i == 0 ? 1u : 16u};
+        for (int i = 0; i < 4 && (i == 0 || d[1] >= 4u << i); ++i) {  // (a pool of fewer rows has no such run)
+            const uint32_t b[2] = {64, i == 0 ? 1u : 4u << i};
             if (!make_bf16_map(&km.m[i], kv.base, 2, d, st, b)) return cudaErrorInvalidValue;
         }
     }
