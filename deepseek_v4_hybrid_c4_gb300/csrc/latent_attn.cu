@@ -909,13 +909,22 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         pg[e] = (seen >> e) & 1u ? lat_entry(a, pt, j, rw[e]) : -1;
                     }
                     bool bad = false;
+                    int some = -1;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // (after all four loads)
                         const bool there = pg[e] >= 0 && pg[e] < a.kv.n_pages;
                         bad = bad || (!there && ((seen >> e) & 1u));
                         id[e] = there ? pg[e] * (int)(a.kv.page_stride / ROW_BYTES) + rw[e] : 0;
-                        if (there) v |= 1u << (4 * (lane & 7) + e);
+                        if (there) v |= 1u << (4 * (lane & 7) + e), some = id[e];
                     }
+                    // rows that are not looked up (masked ones of a unit): another row of the tile stands in -- the same
+                    // row for all items was read from a few L2 slices by every SM
+                    const uint32_t have = __ballot_sync(0xffffffffu, some >= 0);
+                    const int other = __shfl_sync(0xffffffffu, some, have ? __ffs(have) - 1 : 0);
+                    const int fill = some >= 0 ? some : max(other, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((v >> (4 * (lane & 7) + e)) & 1u)) id[e] = fill;
                     if (bad) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
                     *reinterpret_cast<int4*>(look + 4 * lane) = make_int4(id[0], id[1], id[2], id[3]);
                     // bit q: quad q's rows follow each other; the next quad's follow them
