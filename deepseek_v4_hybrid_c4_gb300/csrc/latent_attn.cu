@@ -429,8 +429,7 @@ struct KeyMaps {
 // Caches read by gathers, quad q (rows 4q .. 4q+3 of a tile): the map of its copy, -1 where another quad's copy takes
 // its rows along.  Boxes of 32, 16 and 8 rows where two units, a unit or half of one lie row behind row in memory, a
 // gather for any four rows.  Bits at the run's first quad (LP_SM_NEXT); q0: the copying warp's first quad; two: it
-// copies both units of the pair.  (Pages of 40 rows, a window of 512: 91.9 us
-// with 16-row boxes and gathers only, 90.0 so.)
+// copies both units of the pair.
 struct QuadRuns {
     uint32_t half, unit, pair;
 };
@@ -902,11 +901,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     int id[4], pg[4], rw[4];
                     uint32_t v = 0, seen = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {  // rows of a unit that no query sees are not looked up
+                    for (int e = 0; e < 4; ++e) {  // pages without a row that a query sees are not looked up
                         const int k = lane * 4 + e, u = u0 + (k >> 4);
-                        const int j = u < x.nU ? unit_row<WINDOW>(x, u) + (k & 15) : -1;
-                        if (j >= 0 && ((WINDOW && j < x.a1) || (j >= x.lo && j < x.hi))) seen |= 1u << e;
-                        pg[e] = (seen >> e) & 1u ? lat_entry(a, pt, j, rw[e]) : -1;
+                        const int j = u < x.nU ? unit_row<WINDOW>(x, u) + (k & 15) : x.hi;
+                        const int lp = div_by(j, a.by_rpp), p0 = lp * a.kv.rpp;
+                        rw[e] = j - p0;
+                        if (j < x.hi && ((WINDOW && p0 < x.a1) || p0 > x.lo - a.kv.rpp)) seen |= 1u << e;
+                        pg[e] = (seen >> e) & 1u && lp < a.table_pages ? __ldg(pt + lp) : -1;
                     }
                     bool bad = false;
                     int some = -1;
@@ -917,8 +918,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         id[e] = there ? pg[e] * (int)(a.kv.page_stride / ROW_BYTES) + rw[e] : 0;
                         if (there) v |= 1u << (4 * (lane & 7) + e), some = id[e];
                     }
-                    // rows that are not looked up (masked ones of a unit): another row of the tile stands in -- the same
-                    // row for all items was read from a few L2 slices by every SM
+                    // for rows that are not looked up another row of the tile stands in: with one and the same for all
+                    // items, read by every SM from a few L2 slices, ragged chunks took 90 us and not 78
                     const uint32_t have = __ballot_sync(0xffffffffu, some >= 0);
                     const int other = __shfl_sync(0xffffffffu, some, have ? __ffs(have) - 1 : 0);
                     const int fill = some >= 0 ? some : max(other, 0);
