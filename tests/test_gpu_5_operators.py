@@ -391,6 +391,36 @@ def test_window_attention_nan_reaches_only_its_readers(m, rpp):
         t += 1
 
 
+@pytest.mark.parametrize("H,rpp", [(128, 64), (128, 40), (24, 64), (24, 40)])
+def test_window_attention_nan_in_masked_rows_of_every_kind(m, H, rpp):
+    """Windows whose tiles are a full one and a short one: NaN behind the last position, infinity between the sinks
+    and the window and in the sinks' own unit, in every sequence; and a NaN that only the later tokens of one
+    sequence have left behind."""
+    g = gen(27)
+    n_tokens, q_len, W, S = [1000, 641, 333, 150, 2000], [1, 2, 1, 6, 3], 128, 4
+    c = Cache(g, [n + 16 for n in n_tokens], rpp)
+    for b, n in enumerate(n_tokens):
+        c.pool[c.at(b, range(n, n + 16))] = math.nan
+        c.pool[c.at(b, range(S, n - q_len[b] - W))] = math.inf
+    p = n_tokens[3] - q_len[3] - W + 2             # the first two tokens of sequence 3 still see it
+    clean = c.pool[c.row(3, p)].clone()
+    c.pool[c.row(3, p)] = math.nan
+    q = randn(g, sum(q_len), H, D)
+    out, lse = window(m, q, c, q_len, n_tokens, W, S)
+    t = 0
+    for b, (ql, n) in enumerate(zip(q_len, n_tokens)):
+        for i in range(ql):
+            pos = n - ql + i
+            keys = list(range(S)) + list(range(max(S, pos - W + 1), pos + 1))
+            if b == 3 and p in keys:
+                assert bool(torch.isnan(out[t]).all()) and bool(torch.isnan(lse[t]).all())
+            else:
+                check(out[t], lse[t], attend(q[t].double(), c.rows(b, keys)), f"sequence {b} token {i}")
+            t += 1
+    c.pool[c.row(3, p)] = clean
+    assert m.csa_read_device_status() == 0
+
+
 def test_window_attention_bad_pages(m):
     g = gen(16)
     c = Cache(g, [300, 300], 32)
