@@ -51,6 +51,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -130,7 +131,7 @@ struct LatArgs {
     int64_t total_q, max_q;
     int window, n_sink;
     int WS;                    // splits of a row tile's keys
-    int items;                 // at most, where the sequences do not overlap
+    int items;                 // runs, or items (window: at most, where the sequences do not overlap)
     int rows;                  // query rows in all (B * H, total_q * H)
     int parts;                 // partial results of a row (1: written to out directly)
     float* part_o;             // [parts][rows][512] normalised
@@ -179,27 +180,32 @@ __device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t 
 
 __device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y); }
 
-// Item number `it` (warp-collective), or false behind the last one.
+// The pair's next item (warp-collective), or false behind its last one.  `it`: the item's number, or, in runs, that of
+// the run that the pair is in; a pair takes every `pairs`-th, whatever number of pairs the device has room for.
 template <bool WINDOW>
-__device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int it, int lane, bool report, LatItem& x) {
+__device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int& it, int pairs, int lane, bool report,
+                                         LatItem& x) {
     int split, splits;
     FastDiv by;
     int first = 0, last = 0;  // tiles of a run's item
     if (!WINDOW) {
         int kb0, kb1, seg;
         if (a.run) {
-            if (cur.pos < 0) {
-                cur.run = it < a.NS ? it : it - a.NS;
-                cur.pos = cur.run * a.run;
-                cur.end = min(cur.pos + a.run, it < a.NS ? a.RT * a.gS : a.B * a.gO);
-                cur.total = it < a.NS;
+            int g, t;
+            for (;; it += pairs, cur.pos = -1) {
+                if (cur.pos < 0) {
+                    if (it >= a.items) return false;
+                    cur.run = it < a.NS ? it : it - a.NS;
+                    cur.pos = cur.run * a.run;
+                    cur.end = min(cur.pos + a.run, it < a.NS ? a.RT * a.gS : a.B * a.gO);
+                    cur.total = it < a.NS;
+                }
+                x.shared = cur.total;
+                g = x.shared ? a.gS : a.gO, t = x.shared ? a.tS : a.tO;
+                seg = div_by(cur.pos, x.shared ? a.by_gS : a.by_gO);
+                if (cur.pos - seg * g >= t) cur.pos = ++seg * g;
+                if (cur.pos < cur.end) break;  // (else the run ends, in places behind a segment's tiles)
             }
-            x.shared = cur.total;
-            const int g = x.shared ? a.gS : a.gO, t = x.shared ? a.tS : a.tO;
-            const FastDiv by_g = x.shared ? a.by_gS : a.by_gO;
-            seg = div_by(cur.pos, by_g);
-            if (cur.pos - seg * g >= t) cur.pos = ++seg * g;
-            if (cur.pos >= cur.end) return false;
             first = cur.pos - seg * g;
             last = min(first + cur.end - cur.pos, t);
             cur.pos += last - first;
@@ -207,7 +213,7 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int i
             splits = 0;
             by = a.by_run;
         } else {
-            if (it >= a.RT * a.SP + a.B * a.OS) return false;
+            if (it >= a.items) return false;
             x.shared = it < a.RT * a.SP;
             if (x.shared) {  // neighbouring items read the same keys
                 split = div_by(it, a.by_RT);
@@ -851,8 +857,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         const uint32_t qfull = mapa(sb + LP_QFULL, 0);
         uint32_t* plain = reinterpret_cast<uint32_t*>(sm + LP_SM_PLAIN);
         SeqCursor cur;
-        for (int it = pair; ok; it += pairs, ++q) {
-            const bool there = lat_item<WINDOW>(a, cur, it, lane, rank == 0, x);
+        for (int it = pair; ok; it += !WINDOW && a.run ? 0 : pairs, ++q) {
+            const bool there = lat_item<WINDOW>(a, cur, it, pairs, lane, rank == 0, x);
             if (!there) x.T = -1;
             if (q >= 4) ok = lat_wait(sb + LP_TAKEN + 8 * (q & 3), ((q >> 2) - 1) & 1, dead);
             if (lane == 0) {
@@ -1279,6 +1285,9 @@ static size_t parts_bytes(const LatArgs& a) {
            align_up((size_t)a.parts * a.rows * sizeof(float), 256);
 }
 
+// Pairs in a grid at most, as a device of fewer SMs has them (csa_selftest_pairs); 0: as many as the device has.
+static std::atomic<int> g_pairs_most{0};
+
 static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, int64_t items, void* ws, cudaStream_t s) {
     if (a.parts > 1) {
         uint8_t* base = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
@@ -1324,7 +1333,9 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
                  : (box ? lat_pair_kernel<true, true> : lat_pair_kernel<false, true>);
     cudaError_t e = set_func_attr_once((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LP_SMEM);
     if (e != cudaSuccess) return e;
-    const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, sms / 2));
+    const int cap = g_pairs_most.load(std::memory_order_relaxed);
+    const int64_t most = cap > 0 ? std::min(cap, sms / 2) : sms / 2;
+    const unsigned pairs = (unsigned)std::max<int64_t>(1, std::min(items, most));
     e = launch_after(kernel, dim3(2 * pairs), LP_T, LP_SMEM, s, qm, km, a);
     if (e != cudaSuccess || a.parts == 1) return e;
     return launch_after(a.parts <= 8 ? lat_merge_kernel<8> : lat_merge_kernel<16>, dim3((unsigned)a.rows), 128, 0, s,
@@ -1336,6 +1347,12 @@ static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, i
 using namespace csa;
 
 extern "C" {
+
+csa_status csa_selftest_pairs(int32_t pairs) {
+    if (pairs < 0) return CSA_ERR_INVALID_ARG;
+    g_pairs_most.store(pairs, std::memory_order_relaxed);
+    return CSA_OK;
+}
 
 size_t csa_prefix_attn_workspace_size(int32_t B, int32_t H, int64_t n_shared, int64_t max_rows) {
     if (check_prefix(B, H, n_shared, max_rows)) return 0;
@@ -1368,6 +1385,7 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
     a.table_pages = page_table_stride;
     a.B = B;
     a.n_rows = n_rows;
+    a.items = (int)items;
     a.n_shared = (int)n_shared;
     a.max_rows = (int)max_rows;
     a.out = static_cast<uint16_t*>(out);

@@ -531,6 +531,13 @@ int32_t csa_version(void);
 csa_status csa_selftest_bounded_wait(void* stream);
 
 /*
+ * Fewer-SMs self-test: later csa_prefix_attn and csa_window_attn calls of this process run on at most
+ * `pairs` pairs of SMs, as they would on a partition of a device; 0 lifts the cap.  Results are the same
+ * bits whatever it is.  Negative: CSA_ERR_INVALID_ARG.
+ */
+csa_status csa_selftest_pairs(int32_t pairs);
+
+/*
  * HiSparse coordinator ([V4-deploy] "HiSparse": a coordinator swaps pages every step and evicts
  * by LRU; [Day-0] "创新 3": a GPU miss is swapped in from the CPU mirror).  A host object holding
  * the working set's bookkeeping: which (request, logical page) each slot holds and the last step
