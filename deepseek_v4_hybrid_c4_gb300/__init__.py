@@ -225,19 +225,20 @@ def csa_topk_workspace_size(B: int, max_G: int, k: int) -> int:
     return int(lib().csa_topk_workspace_size(B, max_G, k))
 
 
-def _scratch(nbytes: int, like):
+def _scratch(nbytes: int, like, stream):
+    """A scratch tensor for a call on `stream` (None: the current one), allocated on that stream: a block that the
+    current stream's pool hands out may still be in use by work pending there, and one given back when the call
+    returns goes to work behind it on the same stream."""
     import torch
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=like.device if hasattr(like, "device") else "cuda")
-
-
-def _workspace(need: int, like, stream):
-    """A scratch tensor of `need` bytes that stays allocated until the work on `stream` that uses it is
-    done, and its size."""
-    ws = _scratch(need, like)
-    if stream is not None and ws.is_cuda:
-        import torch
-        ws.record_stream(torch.cuda.ExternalStream(stream, ws.device) if isinstance(stream, int) else stream)
-    return ws, need
+    device = like.device if hasattr(like, "device") else "cuda"
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int) or not isinstance(stream, torch.cuda.Stream):
+        d = None if device == "cuda" else device
+        stream = torch.cuda.ExternalStream(handle, d) if handle else torch.cuda.default_stream(d)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def csa_topk(scores, G: int, k: int, idx_out, keys_out=None, workspace=None, ws_bytes: int = 0,
@@ -245,7 +246,7 @@ def csa_topk(scores, G: int, k: int, idx_out, keys_out=None, workspace=None, ws_
     """workspace None: a scratch tensor of csa_topk_workspace_size(1, G, k) bytes is allocated."""
     if workspace is None:
         ws_bytes = csa_topk_workspace_size(1, G, k)
-        workspace = _scratch(ws_bytes, scores)
+        workspace = _scratch(ws_bytes, scores, stream)
     _check(lib().csa_topk(_ptr(scores), G, k, _ptr(idx_out), _ptr(keys_out), _ptr(workspace), ws_bytes,
                           _stream(stream)), "csa_topk")
 
@@ -254,7 +255,7 @@ def csa_topk_batched(scores, offsets, B: int, max_G: int, k: int, idx_out, keys_
                      ws_bytes: int = 0, stream=None) -> None:
     if workspace is None:
         ws_bytes = csa_topk_workspace_size(B, max_G, k)
-        workspace = _scratch(ws_bytes, scores)
+        workspace = _scratch(ws_bytes, scores, stream)
     _check(lib().csa_topk_batched(_ptr(scores), _ptr(offsets), B, max_G, k, _ptr(idx_out), _ptr(keys_out),
                                   _ptr(workspace), ws_bytes, _stream(stream)), "csa_topk_batched")
 
@@ -282,7 +283,7 @@ def csa_topk_merge(keys, idx, rank_lo, R: int, k: int, rank: int = -1, sel_local
                    workspace=None, ws_bytes: int = 0, stream=None) -> None:
     if workspace is None:
         ws_bytes = csa_topk_merge_workspace_size(R, k)
-        workspace = _scratch(ws_bytes, keys)
+        workspace = _scratch(ws_bytes, keys, stream)
     _check(lib().csa_topk_merge(_ptr(keys), _ptr(idx), _ptr(rank_lo), R, k, rank, _ptr(sel_local), _ptr(idx_out),
                                 _ptr(keys_out), _ptr(workspace), ws_bytes, _stream(stream)), "csa_topk_merge")
 
@@ -292,7 +293,7 @@ def csa_sparse_attn_partial(q, H: int, scale: float, kv_c: csa_paged, sel, n_sel
                             stream=None) -> None:
     if workspace is None:
         ws_bytes = csa_sparse_attn_workspace_size(H, n_sel, swa)
-        workspace = _scratch(ws_bytes, q)
+        workspace = _scratch(ws_bytes, q, stream)
     _check(lib().csa_sparse_attn_partial(_ptr(q), H, scale, kv_c, _ptr(sel), n_sel, kv_raw, n_tokens, swa,
                                          _ptr(o_part), _ptr(lse_part), _ptr(workspace), ws_bytes, _stream(stream)),
            "csa_sparse_attn_partial")
@@ -312,7 +313,8 @@ def csa_prefix_attn(q, B: int, H: int, scale: float, kv: csa_paged, page_table_s
     """One token per request over a batch whose requests share their first n_shared rows (kv: the pool
     with the [B, page_table_stride] table).  workspace None: a scratch tensor is allocated."""
     if workspace is None:
-        workspace, ws_bytes = _workspace(csa_prefix_attn_workspace_size(B, H, n_shared, max_rows), q, stream)
+        ws_bytes = csa_prefix_attn_workspace_size(B, H, n_shared, max_rows)
+        workspace = _scratch(ws_bytes, q, stream)
     _check(lib().csa_prefix_attn(_ptr(q), B, H, scale, kv, page_table_stride, n_shared, _ptr(n_rows), max_rows,
                                  _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)), "csa_prefix_attn")
 
@@ -327,8 +329,8 @@ def csa_window_attn(q, H: int, scale: float, kv_raw: csa_paged, page_table_strid
     """Causal attention of each sequence's new tokens over a sliding window and the first n_sink tokens.
     workspace None: a scratch tensor is allocated."""
     if workspace is None:
-        need = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink)
-        workspace, ws_bytes = _workspace(need, q, stream)
+        ws_bytes = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink)
+        workspace = _scratch(ws_bytes, q, stream)
     _check(lib().csa_window_attn(_ptr(q), H, scale, kv_raw, page_table_stride, B, _ptr(q_offsets), _ptr(n_tokens),
                                  total_q, max_q, window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
                                  _stream(stream)), "csa_window_attn")
@@ -358,7 +360,8 @@ def csa_pages_workspace_size(n_pages: int) -> int:
 def csa_pages_alloc(refs, n_pages: int, page_table, table_stride: int, B: int, first, count, workspace=None,
                     ws_bytes: int = 0, stream=None) -> None:
     if workspace is None:
-        workspace, ws_bytes = _workspace(csa_pages_workspace_size(n_pages), refs, stream)
+        ws_bytes = csa_pages_workspace_size(n_pages)
+        workspace = _scratch(ws_bytes, refs, stream)
     _check(lib().csa_pages_alloc(_ptr(refs), n_pages, _ptr(page_table), table_stride, B, _ptr(first), _ptr(count),
                                  _ptr(workspace), ws_bytes, _stream(stream)), "csa_pages_alloc")
 
@@ -371,7 +374,8 @@ def csa_pages_free(refs, n_pages: int, page_table, table_stride: int, B: int, ro
 def csa_pages_fork(pools: csa_page_pools, refs, page_table, table_stride: int, B: int, src, dst, F: int, n_tokens,
                    rows_per_page: int, workspace=None, ws_bytes: int = 0, stream=None) -> None:
     if workspace is None:
-        workspace, ws_bytes = _workspace(csa_pages_workspace_size(pools.n_pages), refs, stream)
+        ws_bytes = csa_pages_workspace_size(pools.n_pages)
+        workspace = _scratch(ws_bytes, refs, stream)
     _check(lib().csa_pages_fork(ctypes.byref(pools), _ptr(refs), _ptr(page_table), table_stride, B, _ptr(src),
                                 _ptr(dst), F, _ptr(n_tokens), rows_per_page, _ptr(workspace), ws_bytes, _stream(stream)),
            "csa_pages_fork")
@@ -380,7 +384,8 @@ def csa_pages_fork(pools: csa_page_pools, refs, page_table, table_stride: int, B
 def csa_pages_compact(pools: csa_page_pools, refs, refs_out, page_table, page_table_out, table_stride: int, B: int,
                       n_used=None, workspace=None, ws_bytes: int = 0, stream=None) -> None:
     if workspace is None:
-        workspace, ws_bytes = _workspace(csa_pages_workspace_size(pools.n_pages), refs, stream)
+        ws_bytes = csa_pages_workspace_size(pools.n_pages)
+        workspace = _scratch(ws_bytes, refs, stream)
     _check(lib().csa_pages_compact(ctypes.byref(pools), _ptr(refs), _ptr(refs_out), _ptr(page_table),
                                    _ptr(page_table_out), table_stride, B, _ptr(n_used), _ptr(workspace), ws_bytes,
                                    _stream(stream)), "csa_pages_compact")

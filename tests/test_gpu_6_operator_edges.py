@@ -52,3 +52,60 @@ def test_window_attention_on_fewer_pairs(m, capped, H, q_len, n_tokens, W, S, pa
     out, lse2 = window(m, q, c, q_len, n_tokens, W, S, workspace=dirty(need), ws_bytes=need)
     assert torch.equal(out, want) and torch.equal(lse, lse2)
     assert m.csa_read_device_status() == 0
+
+
+# ------------------------------------------------------------------ a stream given with the call
+@pytest.mark.parametrize("as_handle", [False, True])
+@pytest.mark.parametrize("call", ["prefix", "window", "pages"])
+def test_scratch_of_a_call_on_another_stream(m, call, as_handle):  # noqa: F811
+    """Memory that was given back with a copy from it still pending on the current stream is no scratch for a call on
+    another one."""
+    g = gen(49)
+    n_rows = [2000, 2100]
+    c = Cache(g, n_rows, 64, 1900)
+    q = randn(g, 2, 16, D)
+    n, off = (torch.tensor(x, dtype=torch.int64, device="cuda") for x in (n_rows, [0, 1, 2]))
+    out, lse = torch.zeros_like(q), torch.zeros(2, 16, dtype=torch.float32, device="cuda")
+    pages = 1 << 20
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    table, first, count = torch.full((1, 9), -1, dtype=torch.int32, device="cuda"), refs.new_zeros(1), refs.new_ones(1)
+    need = {"prefix": m.csa_prefix_attn_workspace_size(2, 16, 1900, 2100),
+            "window": m.csa_window_attn_workspace_size(2, 16, 2, 1, 900, 4),
+            "pages": m.csa_pages_workspace_size(pages)}[call]
+    assert need > 1 << 16
+    side = torch.cuda.Stream()
+    held = torch.full((need,), 1, dtype=torch.uint8, device="cuda")
+    copy = torch.zeros_like(held)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    copy.copy_(held)
+    del held
+    s = side.cuda_stream if as_handle else side
+    if call == "prefix":
+        m.csa_prefix_attn(q, 2, 16, SCALE, c.paged(m), c.width, 1900, n, 2100, out, lse, stream=s)
+    elif call == "window":
+        m.csa_window_attn(q, 16, SCALE, c.paged(m), c.width, 2, off, n, 2, 1, 900, 4, out, lse, stream=s)
+    else:
+        m.csa_pages_alloc(refs, pages, table, 9, 1, first, count, stream=s)
+    torch.cuda.synchronize()
+    assert bool((copy == 1).all())
+    if call == "pages":
+        assert table.tolist() == [[0] + [-1] * 8] and int(refs.sum()) == 1
+    for b in range(2) if call != "pages" else ():
+        keys = range(n_rows[b]) if call == "prefix" else list(range(4)) + list(range(n_rows[b] - 900, n_rows[b]))
+        check(out[b], lse[b], attend(q[b].double(), c.rows(b, keys)), f"request {b}")
+    assert m.csa_read_device_status() == 0
+
+
+def test_scratch_of_a_call_on_the_default_stream(m):  # noqa: F811
+    """The handle 0 is the default stream, whatever stream is the current one."""
+    g = gen(50)
+    c = Cache(g, [700], 64)
+    q = randn(g, 1, 16, D)
+    n, out = torch.tensor([700], dtype=torch.int64, device="cuda"), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        m.csa_prefix_attn(q, 1, 16, SCALE, c.paged(m), c.width, 600, n, 700, out, stream=0)
+    torch.cuda.synchronize()
+    w = attend(q[0].double(), c.rows(0, range(700)))
+    check(out[0], w[1].float(), w, "prefix")
