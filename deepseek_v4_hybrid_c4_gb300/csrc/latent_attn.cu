@@ -239,8 +239,10 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int& 
             // the shortest and the longest of the rows' requests
             const int b0 = div_by(x.row0, a.by_H), b1 = div_by(x.row0 + x.nrows - 1, a.by_H);
             int mn = 0x7FFFFFFF, mx = 0;
+            const bool look = report && first == 0 && a.OS == 0;  // (with rows of their own: reported there)
             for (int b = b0 + lane; b <= b1; b += 32) {
                 const int64_t n = __ldg(a.n_rows + b);
+                if (look && (n < 0 || n > a.max_rows)) raise_status(a.status, CSA_ERR_DEVICE_BOUNDS);
                 const int c = n < 0 ? 0 : (n > a.n_shared ? a.n_shared : (int)n);
                 mn = min(mn, c);
                 mx = max(mx, c);

@@ -249,9 +249,9 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * read through row 0 of the table; rows n_shared .. n_rows[b]-1 are request b's own, read through
  * row b (csa_pages_fork makes such tables).  For request b and head h, over j < n_rows[b]:
  *   l_j = scale * q_bh . K_j,  o_bh = softmax(l) . V   (K = V = the row)
- * q bf16 [B, H, 512]; n_rows device int64 [B], 0 <= n_rows[b] <= max_rows (above it: the excess is
- * not read and the device status gets CSA_ERR_DEVICE_BOUNDS); n_rows[b] may be below n_shared, and
- * 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32 [B, H] (natural
+ * q bf16 [B, H, 512]; n_rows device int64 [B], 0 <= n_rows[b] <= max_rows (a length outside is
+ * taken for the nearest one inside, and the device status gets CSA_ERR_DEVICE_BOUNDS); n_rows[b] may be
+ * below n_shared, and 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32 [B, H] (natural
  * log, nullable).  Entries of the page table behind a request's rows are not read.  A page id
  * outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
  * infinity reaches only the requests that attend it.

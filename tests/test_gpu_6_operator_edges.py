@@ -109,3 +109,22 @@ def test_scratch_of_a_call_on_the_default_stream(m):  # noqa: F811
     torch.cuda.synchronize()
     w = attend(q[0].double(), c.rows(0, range(700)))
     check(out[0], w[1].float(), w, "prefix")
+
+
+# ------------------------------------------------------------------ lengths out of range, no rows of their own
+@pytest.mark.parametrize("B,H,shared", [(3, 16, 100), (12, 128, 6000), (5, 7, 1)])
+@pytest.mark.parametrize("n", [1, 1 << 31, (1 << 63) - 1, -1, -(1 << 63)])
+def test_prefix_attention_reports_lengths_where_every_row_is_shared(m, B, H, shared, n):  # noqa: F811
+    """max_rows = n_shared: a length above it (by 1 and more) or below 0 is reported, and taken for the nearest one."""
+    g = gen(48)
+    c = Cache(g, [shared] * B, 64, shared)
+    n_rows = [shared] * B
+    q = randn(g, B, H, D)
+    want, lse = prefix(m, q, c, shared, n_rows)
+    assert m.csa_read_device_status() == 0
+    n_rows[B - 1] = n if n < 0 or n > 1 else shared + n
+    out, lse2 = prefix(m, q, c, shared, n_rows, max_rows=shared)
+    assert m.csa_read_device_status() == BOUNDS
+    last = B - 1 if n < 0 else B
+    assert torch.equal(out[:last], want[:last]) and torch.equal(lse[:last], lse2[:last])
+    assert n > 0 or (bool((out[last] == 0).all()) and bool((lse2[last] == -math.inf).all()))
