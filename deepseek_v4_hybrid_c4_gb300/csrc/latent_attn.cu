@@ -47,7 +47,10 @@
 // a tile with masked rows a NaN or an infinity in any row makes that row's logits of all 128 query rows
 // non-finite; where a thread finds one, its CTA replaces the non-finite values of the tile's V rows by 0 before the
 // product, once the products' thread has told it that they are there (waiting for them in every tile with masked rows
-// cost a prompt 6 percent).  Query rows that do attend such a key have a NaN weight from its logit and stay NaN.
+// cost a prompt 6 percent).  Query rows that do attend such a key get what the formula gives: a logit of NaN or +inf makes
+// them NaN; one of -inf is a weight of 0, and 0 times what V holds is NaN in the dims that are not finite.  In tiles without
+// masked rows the product says so itself; for the others, and where every logit of a tile is -inf, the query's row is
+// noted (LP_SM_LOST), and its output mended behind the item (lat_not_finite).
 #include <cuda.h>
 
 #include <algorithm>
@@ -84,7 +87,9 @@ constexpr uint32_t LP_SM_SUM = LP_SM_MAX + 2048;          // [256] row sums of t
 constexpr uint32_t LP_SM_ITEM = LP_SM_SUM + 1024;         // [4] items
 constexpr uint32_t LP_SM_PLAIN = LP_SM_ITEM + 4 * 128;    // [8 tiles] plain (tile_plain)
 constexpr uint32_t LP_SM_NEXT = LP_SM_PLAIN + 32;         // [8 tiles] gathers: which quads' rows follow each other
-constexpr uint32_t LP_SMEM = LP_SM_NEXT + 128 + 1024;     // + alignment slack
+constexpr uint32_t LP_SM_LOST = LP_SM_NEXT + 128;         // [64] the last item in which the row's query saw a logit of
+                                                          // -inf that calls for a look at its output; [64]: any row
+constexpr uint32_t LP_SMEM = LP_SM_LOST + 272 + 1024;     // + alignment slack
 static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
 // Tiles of a split at most: O takes eight additions a tile in the tensor cores, each of which may lose 2^-23 of the
@@ -93,6 +98,8 @@ constexpr int LP_MAX_TILES = 4096;
 constexpr float LP_LOG2E = 1.4426950408889634f;
 constexpr float LP_LN2 = 0.6931471805599453f;
 constexpr float LP_RESCALE = 8.0f;                        // log2 units
+constexpr float LP_LSE_LOST = -3.4028235e38f;             // lse of a partial result whose rows all have logits of -inf: a
+                                                          // weight of 0 in the merge, times NaN where they are not finite
 
 // n / d for 0 <= n < 2^31 by a multiplication: with s = ceil(log2 d) and m = ceil(2^(31+s) / d) < 2^32,
 // m n / 2^(31+s) exceeds n / d by less than n / 2^31 / d < 1 / d.
@@ -176,6 +183,17 @@ struct SeqCursor {
 
 __device__ __forceinline__ bool seq_valid(const LatArgs& a, int64_t q0, int64_t q1, int64_t nt) {
     return q0 >= 0 && q1 >= q0 && q1 <= a.total_q && q1 - q0 <= a.max_q && nt <= LP_MAX_ROWS;
+}
+
+// The last sequence that starts at or before token tok.
+__device__ __forceinline__ int seq_of(const LatArgs& a, int64_t tok) {
+    int l = 0, r = a.B;
+    while (r - l > 1) {
+        const int m = (l + r) / 2;
+        if (__ldg(a.q_offsets + m) <= tok) l = m;
+        else r = m;
+    }
+    return l;
 }
 
 __device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y); }
@@ -449,6 +467,58 @@ __device__ __forceinline__ int quad_map(QuadRuns n, int q, int q0, bool two) {
     return 0;
 }
 
+// 0 times a value that is not finite: dims [at, at + 128) of an output row (of out, or of partial result `part`) whose
+// query saw a logit of -inf become NaN where one of the rows that it sees holds no finite value; all of them where it saw
+// no other logit (l_run 0).  Rare and slow: it reads every row that the query sees.
+__device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part, int at, float l_run) {
+    if (l_run != l_run) return;  // all NaN already
+    const bool direct = a.parts == 1;
+    const int64_t to = (direct ? (int64_t)row : (int64_t)part * a.rows + row) * D + at;
+    auto put = [&](int d) {
+        if (direct) a.out[to + d] = 0x7FFFu;
+        else a.part_o[to + d] = __int_as_float(0x7FFFFFFF);
+    };
+    if (l_run == 0.f) {
+        if (direct) {
+            for (int d = 0; d < 128; ++d) put(d);
+            return;
+        }
+        if (at == 0) a.part_lse[(int64_t)part * a.rows + row] = LP_LSE_LOST;
+    }
+    int lo, hi, sinks = 0, b = div_by(row, a.by_H);
+    if (a.n_rows) {
+        const int64_t n = __ldg(a.n_rows + b);
+        lo = part < a.SP ? 0 : a.n_shared;
+        hi = (int)max(min(n, (int64_t)(part < a.SP ? a.n_shared : a.max_rows)), (int64_t)0);
+        if (part < a.SP) b = 0;
+    } else {
+        const int64_t tok = b;
+        b = seq_of(a, tok);
+        const int64_t q1 = __ldg(a.q_offsets + b + 1), nt = __ldg(a.n_tokens + b);
+        if (!seq_valid(a, __ldg(a.q_offsets + b), q1, nt)) return;
+        hi = (int)max(nt - (q1 - tok) + 1, (int64_t)0);
+        lo = max(0, hi - a.window);
+        sinks = min(a.n_sink, lo);
+    }
+    const int32_t* pt = a.kv.pt + (int64_t)b * a.kv.pt_stride;
+#pragma unroll 1
+    for (int j = sinks > 0 ? 0 : lo; j < hi; j = j + 1 == sinks ? lo : j + 1) {
+        int slot;
+        const int pg = lat_entry(a, pt, j, slot);
+        if (pg < 0 || pg >= a.kv.n_pages) continue;
+        const uint4* p = reinterpret_cast<const uint4*>(a.kv.base + (int64_t)pg * a.kv.page_stride +
+                                                        (int64_t)slot * ROW_BYTES + at * 2);
+#pragma unroll 4
+        for (int d = 0; d < 128; d += 8) {
+            const uint4 v = __ldg(p + (d >> 3));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (((w[e >> 1] >> (16 * (e & 1))) & 0x7F80u) == 0x7F80u) put(d + e);
+        }
+    }
+}
+
 template <bool BOX, bool WINDOW>
 __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps& km, const LatArgs& a) {
     extern __shared__ uint8_t lp_raw[];
@@ -467,6 +537,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&km.m[0]);
     }
+    if (tid >= 96 && tid < 96 + 65) reinterpret_cast<volatile int*>(sm + LP_SM_LOST)[tid - 96] = 0;
     if (tid == 32) {
         for (int i = 0; i < LP_SLOTS; ++i) {
             mbar_init(sb + LP_FULL + 8 * i, 1);  // even CTA: both CTAs' rows
@@ -516,6 +587,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         const int r = tid & 63, half = (warp >> 1) & 1, ch = warp >> 2;
         float* mx = reinterpret_cast<float*>(sm + LP_SM_MAX);
         float* ls = reinterpret_cast<float*>(sm + LP_SM_SUM);
+        volatile int* lost = reinterpret_cast<volatile int*>(sm + LP_SM_LOST);  // (items are counted from 1)
         while (next_item()) {
             const int row = x.row0 + (int)rank * 64 + r;  // this thread's query row
             const bool mine = (int)rank * 64 + r < x.nrows;
@@ -602,6 +674,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         alpha = lat_ex2(m_run - mt);
                         m_run = mt;
                     }
+                } else if (plain) {  // every logit is -inf or NaN
+                    lost[r] = lost[64] = q;
                 }
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 const uint64_t sl2 = f32x2(a.sl2, a.sl2), mneg = f32x2(-mref, -mref);
@@ -652,6 +726,14 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 if (any_bad) {  // non-finite values of this CTA's V rows -> 0
+#pragma unroll 1
+                    for (int j = 0; j < 16 * nc; ++j) {
+                        const uint32_t w = tc_ld1(ts + j);  // (S stays until this warp reports P)
+                        const int u = ub + (j >> 4), k = unit_row<WINDOW>(x, u0 + u) + (j & 15);
+                        if (w == 0xFF800000u && u < nu && (k < vs || (k >= vlo && k < vhi)) &&
+                            ((ld_shared_u32(sb + LP_SM_VALID + (g & 7) * 16 + (u >> 1) * 4) >> ((u & 1) * 16 + (j & 15))) & 1u))
+                            lost[r] = lost[64] = q;
+                    }
                     // (the products' thread, waiting for P, answers; a warp that gave up lets its own wait run out)
                     if (lane == 0) st_dsmem_u32(mapa(sb + LP_SM_WANT, 0), (uint32_t)g + 1);
                     ok = lat_word(sb + LP_SM_LAND, (uint32_t)g + 1, dead) && ok;
@@ -758,6 +840,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 tc_fence_before();
+                if (lost[64] == q) {
+                    __syncwarp();  // (behind the other lanes' stores to this lane's row)
+                    if (mine && lost[r] == q) lat_not_finite(a, row, x.part, half * 256 + ch * 128, l_run);
+                }
             }
         }
     } else if (warp == LP_SOFT && rank == 0) {
@@ -1095,12 +1181,7 @@ __global__ void __launch_bounds__(128, IN > 8 ? 4 : 8) lat_merge_kernel(LatArgs 
     const int row = blockIdx.x, t = threadIdx.x;
     if (!a.n_rows) {
         const int64_t q = row / a.H;
-        int l = 0, r = a.B;  // the last sequence that starts at or before token q
-        while (r - l > 1) {
-            const int m = (l + r) / 2;
-            if (__ldg(a.q_offsets + m) <= q) l = m;
-            else r = m;
-        }
+        const int l = seq_of(a, q);
         const int64_t q0 = __ldg(a.q_offsets + l), q1 = __ldg(a.q_offsets + l + 1);
         if (q < q0 || q >= q1 || !seq_valid(a, q0, q1, __ldg(a.n_tokens + l))) return;
     }
@@ -1149,12 +1230,13 @@ __global__ void __launch_bounds__(128, IN > 8 ? 4 : 8) lat_merge_kernel(LatArgs 
             o3 = fmaf(w, f[s].w, o3);
         }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const bool lost = M == LP_LSE_LOST;  // rows, and every logit -inf
+    const float inv = lost ? __int_as_float(0x7FFFFFFF) : L == 0.f ? 0.f : 1.f / L;
     uint2 w;
     w.x = pack_bf16x2(o0 * inv, o1 * inv);
     w.y = pack_bf16x2(o2 * inv, o3 * inv);
     *reinterpret_cast<uint2*>(a.out + (int64_t)row * D + t * 4) = w;
-    if (t == 0 && a.lse) a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f ? -INFINITY : M + log2f(L) * LP_LN2);
+    if (t == 0 && a.lse) a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f || lost ? -INFINITY : M + log2f(L) * LP_LN2);
 }
 
 // What both calls ask of the cache: a page table, pages of whole 1,024-byte rows, row ids below 2^31.

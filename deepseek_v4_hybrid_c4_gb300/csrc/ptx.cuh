@@ -250,6 +250,15 @@ CSA_DEV void tc_ld16(uint32_t taddr, uint32_t* r) {
         : CSA_R8(0), CSA_R8(8)
         : "r"(taddr));
 }
+// One column, waited for.
+CSA_DEV uint32_t tc_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(taddr)
+                 : "memory");
+    return r;
+}
 CSA_DEV void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

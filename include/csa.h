@@ -254,7 +254,8 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * below n_shared, and 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32 [B, H] (natural
  * log, nullable).  Entries of the page table behind a request's rows are not read.  A page id
  * outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
- * infinity reaches only the requests that attend it.
+ * infinity reaches only the requests that attend it, and those as the formula has it: a logit of NaN or +inf
+ * leaves a head no finite output, one of -inf is a weight of 0, and 0 times what is not finite is NaN.
  * B * H rows are padded to 128-row tensor-core tiles; key ranges are split and merged by
  * log-sum-exp, in a fixed order: the same inputs give the same bits.  A range holds up to 524,288
  * rows, so that the workspace grows with max_rows beyond that.
@@ -284,7 +285,8 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
  * sees nothing: out 0, lse -inf.  Pages that hold only positions no new token sees are not read and
  * their table entries may be anything (a cache that gives the pages behind the window back).  A page
  * id outside the pool, or a position behind page_table_stride pages, leaves its rows out
- * (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an infinity reaches only the tokens that see it.
+ * (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an infinity reaches only the tokens that see it,
+ * as in csa_prefix_attn.
  * The same inputs give the same bits.
  * 1 <= H <= 128, 1 <= B <= 65535, 1 <= window <= 2^30, 0 <= n_sink <= 2^30, 0 <= total_q,
  * total_q * H < 2^31 (else CSA_ERR_UNSUPPORTED), 1 <= max_q; the limits of csa_prefix_attn on kv.

@@ -128,3 +128,99 @@ def test_prefix_attention_reports_lengths_where_every_row_is_shared(m, B, H, sha
     last = B - 1 if n < 0 else B
     assert torch.equal(out[:last], want[:last]) and torch.equal(lse[:last], lse2[:last])
     assert n > 0 or (bool((out[last] == 0).all()) and bool((lse2[last] == -math.inf).all()))
+
+
+# ------------------------------------------------------------------ infinities in rows that are attended
+def check_readers(out, lse, q, kv, where):
+    """Against the formula, element for element: a logit of +inf or NaN leaves nothing but NaN; one of -inf has the
+    weight 0, and 0 times what its row holds is NaN where that is not finite.  What stays finite is what the other
+    rows give."""
+    x = SCALE * (q @ kv.t())
+    w = torch.exp(x - torch.logsumexp(x, -1, keepdim=True))
+    nan = torch.isnan(w @ kv)
+    assert torch.equal(torch.isnan(out), nan), f"{where}: {int((torch.isnan(out) != nan).sum())} of {nan.sum()}"
+    o, l, to, tl = attend(q, kv[torch.isfinite(kv).all(1)])
+    off = torch.where(nan, torch.zeros_like(o), (out.double() - o).abs() - to)
+    assert float(off.max()) <= 0, where
+    fin = torch.isfinite(torch.logsumexp(x, -1))
+    assert bool((~torch.isfinite(lse[~fin])).all()), where
+    if bool(fin.any()):
+        assert float(((lse.double() - l).abs() - tl)[fin].max()) <= 0, where
+
+
+@pytest.mark.parametrize("rpp", [64, 40])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("j", [100, 650, 690, 699, 1279, 1280, 1299])
+def test_prefix_attention_readers_of_an_infinity(m, rpp, value, j):  # noqa: F811
+    """Rows of tiles that every request sees whole, of tiles that one sees in part, and of a request's own."""
+    g = gen(43)
+    shared, n_rows = 1280, [1300, 1280, 700, 1281]
+    c = Cache(g, [1300] * 4, rpp, shared)
+    for b in range(4):
+        c.pool[c.row(0 if j < shared else b, j), 17] = value
+    q = randn(g, 4, 30, D)
+    out, lse = prefix(m, q, c, shared, n_rows)
+    for b, n in enumerate(n_rows):
+        kv = torch.cat([c.rows(0, range(min(n, shared))), c.rows(b, range(shared, n))])
+        check_readers(out[b], lse[b], q[b].double(), kv, f"request {b}")
+    assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [[0], [30], [30, 31, 69], list(range(70))])
+def test_prefix_attention_readers_of_infinities_in_one_item(m, bad):  # noqa: F811
+    """A whole context of one tile, of which any row may be the only one that a request attends."""
+    g = gen(44)
+    n_rows = [70, 1, 33, 64]
+    c = Cache(g, n_rows, 16)
+    for b in range(4):
+        for j in bad:
+            if j < n_rows[b]:
+                c.pool[c.row(b, j), 500] = math.inf
+    q = randn(g, 4, 33, D)
+    out, lse = prefix(m, q, c, 0, n_rows)
+    for b, n in enumerate(n_rows):
+        check_readers(out[b], lse[b], q[b].double(), c.rows(b, range(n)), f"request {b}")
+
+
+@pytest.mark.parametrize("H,shared,n", [(128, 256, 300), (16, 2000, 2100), (40, 0, 128)])
+def test_prefix_attention_readers_of_a_channel_of_infinities(m, H, shared, n):  # noqa: F811
+    """Every row holds an infinity at one place: a head's logits are all +inf or all -inf, and no output is finite."""
+    g = gen(45)
+    c = Cache(g, [n, n], 64, shared)
+    c.pool[:, 9] = math.inf
+    q = randn(g, 2, H, D)
+    out, lse = prefix(m, q, c, shared, [n, n])
+    assert bool(torch.isnan(out).all()) and not bool(torch.isfinite(lse).any())
+
+
+@pytest.mark.parametrize("rpp", [64, 24])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("p", [1, 330, 380, 399])
+@pytest.mark.parametrize("H", [16, 128])
+def test_window_attention_readers_of_an_infinity(m, rpp, value, p, H):  # noqa: F811
+    """A sink, rows that only earlier or only later tokens of the chunk see, the last row."""
+    g = gen(46)
+    c = Cache(g, [400], rpp)
+    c.pool[c.row(0, p), 300] = value
+    q = randn(g, 60, H, D)
+    out, lse = window(m, q, c, [60], [400], 50, 3)
+    for t in range(0, 60, 1 if H == 16 else 3):
+        pos = 340 + t
+        kv = c.rows(0, list(range(3)) + list(range(pos - 49, pos + 1)))
+        check_readers(out[t], lse[t], q[t].double(), kv, f"position {pos}")
+    assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("H,ql,W", [(128, 3, 500), (16, 1, 2000), (8, 1, 2000)])
+@pytest.mark.parametrize("back", [0, 3, 140, 300, 499])
+def test_window_attention_readers_of_an_infinity_in_wide_windows(m, H, ql, W, back):  # noqa: F811
+    """Tiles that every token of an item sees whole, and keys that are split."""
+    g = gen(47)
+    n = 2500
+    c = Cache(g, [n], 64)
+    c.pool[c.row(0, n - 1 - back), 0] = math.inf
+    q = randn(g, ql, H, D)
+    out, lse = window(m, q, c, [ql], [n], W, 0)
+    for t in range(ql):
+        pos = n - ql + t
+        check_readers(out[t], lse[t], q[t].double(), c.rows(0, range(pos - W + 1, pos + 1)), f"position {pos}")
