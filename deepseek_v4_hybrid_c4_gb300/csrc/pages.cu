@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(256) pages_alloc_kernel(int32_t* refs, int32_t
     }
     const int64_t n_free = w.hdr[0];
     int32_t* row = table + (int64_t)b * stride + first[b];
-    for (int j = threadIdx.x; j < count[b]; j += blockDim.x) {
+    const int64_t n = count[b];  // (up to 2^31 - 1: a 32-bit index would pass it by wrapping)
+    for (int64_t j = threadIdx.x; j < n; j += blockDim.x) {
         int32_t p = -1;
         if (s + j < n_free) {
             p = w.list[s + j];

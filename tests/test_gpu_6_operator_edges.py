@@ -224,3 +224,17 @@ def test_window_attention_readers_of_an_infinity_in_wide_windows(m, H, ql, W, ba
     for t in range(ql):
         pos = n - ql + t
         check_readers(out[t], lse[t], q[t].double(), c.rows(0, range(pos - W + 1, pos + 1)), f"position {pos}")
+
+
+# ------------------------------------------------------------------ pages
+@pytest.mark.parametrize("first", [0, 1, 255])
+def test_pages_alloc_of_the_longest_row(m, first):  # noqa: F811
+    """A table row of 2^31 - 1 entries, all of them (or all but the first ones) asked for, in a pool of seven pages."""
+    width = (1 << 31) - 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    refs, table = torch.zeros(7, **i32), torch.full((1, width), -9, **i32)
+    m.csa_pages_alloc(refs, 7, table, width, 1, torch.tensor([first], **i32), torch.tensor([width - first], **i32))
+    assert m.csa_read_device_status() == 1 << 6
+    assert refs.tolist() == [1] * 7
+    assert table[0, :first].tolist() == [-9] * first and table[0, first:first + 7].tolist() == list(range(7))
+    assert all(bool((t == -1).all()) for t in table[0, first + 7:].split(1 << 28))
