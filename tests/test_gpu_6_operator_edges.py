@@ -238,3 +238,59 @@ def test_pages_alloc_of_the_longest_row(m, first):  # noqa: F811
     assert refs.tolist() == [1] * 7
     assert table[0, :first].tolist() == [-9] * first and table[0, first:first + 7].tolist() == list(range(7))
     assert all(bool((t == -1).all()) for t in table[0, first + 7:].split(1 << 28))
+
+
+def real_pools(n_pages, seed=5):
+    """Pages of a cache's sizes (raw rows, compressed rows, index keys) and of one that ends inside a piece of its
+    copy, in a pool whose pages lie apart; random bytes."""
+    g = gen(seed)
+    words = (16384, 4096, 1024, 6164 + 12)
+    p = [torch.randint(-2**31, 2**31 - 1, (n_pages, w), generator=g, device="cuda", dtype=torch.int32) for w in words]
+    return p[:3] + [p[3][:, 4:6168]], p[3]
+
+
+def test_pages_of_real_sizes(m):  # noqa: F811
+    """Copies, forks and moves of whole pages, byte for byte, every other page and byte left as it was."""
+    n_pages, rpp, width = 200, 64, 40
+    pools, wide = real_pools(n_pages)
+    assert pools[3].stride(0) == 6176 and pools[3].shape[1] * 4 % 8192 not in (0, 16)
+    d = m.page_pools(pools, n_pages)
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def moved(before, src, dst):
+        for p, old in zip(pools, before):
+            old[dst] = old[src]
+            assert torch.equal(p, old)
+
+    gaps = wide[:, :4].clone(), wide[:, 6168:].clone()
+    before = [p.clone() for p in pools]
+    m.csa_pages_copy(d, i32([3, 199, 3]), i32([198, 0, 77]), 3)
+    moved(before, [3, 199, 3], [198, 0, 77])
+
+    refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    refs[::3] = 1
+    table = torch.full((6, width), -1, dtype=torch.int32, device="cuda")
+    tokens = [30 * rpp + 17, 5 * rpp + 63]
+    m.csa_pages_alloc(refs, n_pages, table, width, 6, i32([0] * 6), i32([31, 6, 0, 0, 0, 0]))
+    nt = torch.tensor(tokens + [0] * 4, dtype=torch.int64, device="cuda")
+    free = [p for p, r in enumerate(refs.tolist()) if r == 0]
+    before = [p.clone() for p in pools]
+    last = [int(table[0, 30]), int(table[1, 5])]
+    m.csa_pages_fork(d, refs, table, width, 6, i32([0, 1, 1, 0]), i32([2, 3, 4, 5]), 4, nt, rpp)
+    moved(before, [last[0], last[1], last[1], last[0]], free[:4])
+    assert [int(table[2, 30]), int(table[3, 5]), int(table[4, 5]), int(table[5, 30])] == free[:4]
+
+    m.csa_pages_free(refs, n_pages, table, width, 6, i32([0, 4]), 2)
+    before = [p.clone() for p in pools]
+    n = torch.zeros(1, dtype=torch.int64, device="cuda")
+    refs[::3] += 1  # (pages that no table names move too)
+    used = [p for p, r in enumerate(refs.tolist()) if r > 0]
+    holes = [p for p in range(len(used)) if p not in used]
+    m.csa_pages_compact(d, refs, refs, table, table, width, 6, n)
+    far = [p for p in used if p >= len(used)]
+    assert n.item() == len(used) and 0 < len(far) == len(holes)
+    moved(before, far, holes)
+    assert torch.equal(wide[:, :4], gaps[0]) and torch.equal(wide[:, 6168:], gaps[1])
+    assert m.csa_read_device_status() == 0
