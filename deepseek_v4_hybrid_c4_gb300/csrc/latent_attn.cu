@@ -55,6 +55,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <limits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -1277,7 +1278,8 @@ static csa_status check_window(int32_t B, int32_t H, int64_t total_q, int64_t ma
 
 static void set_scale(LatArgs& a, float scale) {
     a.sl2 = (scale < 0.f ? -scale : scale) * LP_LOG2E;
-    if (a.sl2 == 0.f) a.sl2 = 1e-30f;  // every weight 1, and a masked logit still -inf
+    // every weight 1 (whatever the logits: at most 3.4e38 times the least number above 0), and a masked logit still -inf
+    if (a.sl2 == 0.f) a.sl2 = std::numeric_limits<float>::denorm_min();
     a.negate = scale < 0.f ? 1u << 13 : 0u;
 }
 

@@ -294,3 +294,27 @@ def test_pages_of_real_sizes(m):  # noqa: F811
     moved(before, far, holes)
     assert torch.equal(wide[:, :4], gaps[0]) and torch.equal(wide[:, 6168:], gaps[1])
     assert m.csa_read_device_status() == 0
+
+
+# ------------------------------------------------------------------ scales
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-45, -1e-45])
+@pytest.mark.parametrize("call", ["prefix", "window"])
+def test_attention_of_no_scale_over_large_rows(m, call, scale):  # noqa: F811
+    """Logits before scaling of 1e33 to 1e35: every weight is the same (off by 1e35 * 1.4e-45, far below 2^-20)."""
+    g = gen(51)
+    n_rows, H = [300, 190], 20
+    c = Cache(g, n_rows, 32, 160)
+    c.pool.mul_(1e16)
+    q = randn(g, 2, H, D) * 1e16
+    n, off = (torch.tensor(x, dtype=torch.int64, device="cuda") for x in (n_rows, [0, 1, 2]))
+    out, lse = torch.zeros_like(q), torch.zeros(2, H, dtype=torch.float32, device="cuda")
+    if call == "prefix":
+        m.csa_prefix_attn(q, 2, H, scale, c.paged(m), c.width, 160, n, 300, out, lse)
+    else:
+        m.csa_window_attn(q, H, scale, c.paged(m), c.width, 2, off, n, 2, 1, 70, 3, out, lse)
+    for b, x in enumerate(n_rows):
+        kv = c.rows(b, range(x) if call == "prefix" else list(range(3)) + list(range(x - 70, x)))
+        o, a = kv.mean(0).expand(H, D), kv.abs().mean(0)
+        want = torch.full((H,), math.log(len(kv)), dtype=torch.float64, device="cuda")
+        check(out[b], lse[b], (o, want, 2.0**-8 * (a + o.abs()) + 2.0**-20 * a, 2.0**-20 * (1 + want)), f"request {b}")
+    assert m.csa_read_device_status() == 0
