@@ -81,6 +81,7 @@ static_assert(LP_TAKEN + 32 <= LP_SM_BAR + 512, "barriers");
 constexpr uint32_t LP_SM_TMEM = LP_SM_BAR + 512, LP_SM_DEAD = LP_SM_TMEM + 8;
 constexpr uint32_t LP_SM_WANT = LP_SM_TMEM + 16, LP_SM_LAND = LP_SM_TMEM + 20;  // the last tile whose V rows a softmax
                                                           // warp asked for (even CTA), and that are there (both)
+constexpr uint32_t LP_SM_CLOSED = LP_SM_TMEM + 24;        // the first item that warp 9 will not bring
 constexpr uint32_t LP_SM_VALID = LP_SM_TMEM + 64;         // [8 tiles][128 keys] bits of the rows that are there
 constexpr uint32_t LP_SM_LOOK = LP_SM_VALID + 128;        // [8 tiles][128] row ids, or [8] units {page, row}, runs
 constexpr uint32_t LP_SM_MAX = LP_SM_LOOK + 8 * 512;      // [2][256] row maxima of the threads
@@ -373,8 +374,9 @@ __device__ __forceinline__ bool tile_plain(const LatItem& x, int i, uint4 vw) {
 }
 
 // Bounded wait; false once any wait of this CTA has run out.  The loads, the products and the passing on
-// stop there; the softmax warps run on to the end of their loops (their barriers count on one another), each
-// further wait returning at once.
+// stop there; the softmax warps run on to the end of their item (their barriers count on one another), each
+// further wait returning at once, and to the next one if there is one: that is for warp 9 alone to say (lat_wait_item),
+// as a warp that found its item just there would wait for ever for one that had looked before and given up.
 // Lane i waits on the barrier at its own address: a warp can wait on several at once.  A wait that is not over at
 // the first look goes on out of line (the code of all roles goes through one instruction cache).
 __device__ __noinline__ bool lat_wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* dead) {
@@ -391,7 +393,22 @@ __device__ __forceinline__ bool lat_wait(uint32_t bar, uint32_t parity, volatile
     return mbar_try_wait(bar, parity) || lat_wait_on(bar, parity, dead);
 }
 
-// The same for a word of shared memory.
+// Item number `it`, or false where warp 9 has ended before it (the first item that never comes: closed).  Warp 9's own
+// waits are bounded, and none of them is for a warp that waits here, so that the limit is only the last resort.
+__device__ __noinline__ bool lat_wait_item_on(uint32_t bar, uint32_t parity, int it, volatile int* closed) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < 4 * CSA_SPIN_LIMIT; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*closed <= it) return false;
+        if (i >= 32) __nanosleep(64);
+    }
+    return false;
+}
+__device__ __forceinline__ bool lat_wait_item(uint32_t bar, uint32_t parity, int it, volatile int* closed) {
+    return mbar_try_wait(bar, parity) || lat_wait_item_on(bar, parity, it, closed);
+}
+
+// The same as lat_wait for a word of shared memory.
 __device__ __forceinline__ bool lat_word(uint32_t at, uint32_t want, volatile uint32_t* dead) {
 #pragma unroll 1
     for (uint32_t i = 0; i < CSA_SPIN_LIMIT; ++i) {
@@ -529,6 +546,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     volatile uint32_t* dead = reinterpret_cast<volatile uint32_t*>(sm + LP_SM_DEAD);
+    volatile int* closed = reinterpret_cast<volatile int*>(sm + LP_SM_CLOSED);
 
     if (warp == 0) {
         tmem_alloc_pair(sb + LP_SM_TMEM, 512);
@@ -559,6 +577,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             mbar_init(sb + LP_TAKEN + 8 * i, LP_SOFT + LP_PROD + (rank == 0 ? 1 : 0));
         }
         *dead = 0;
+        *closed = 0x7FFFFFFF;
         *reinterpret_cast<uint32_t*>(sm + LP_SM_WANT) = *reinterpret_cast<uint32_t*>(sm + LP_SM_LAND) = 0;
         fence_mbar_init();
     }
@@ -573,7 +592,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
     bool ok = true;
     // The next item as warp 9 left it; false behind the last one, and when a wait has run out.
     auto next_item = [&]() -> bool {
-        const bool in = lat_wait(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, dead);
+        const bool in = lat_wait_item(sb + LP_ITEM + 8 * (q & 3), (q >> 2) & 1, q, closed);
         x = load_item(sb + LP_SM_ITEM + (q & 3) * 128);
         __syncwarp();
         if (lane == 0) mbar_arrive(sb + LP_TAKEN + 8 * (q & 3));
@@ -729,11 +748,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 if (any_bad) {  // non-finite values of this CTA's V rows -> 0
 #pragma unroll 1
                     for (int j = 0; j < 16 * nc; ++j) {
+                        __syncwarp();
                         const uint32_t w = tc_ld1(ts + j);  // (S stays until this warp reports P)
                         const int u = ub + (j >> 4), k = unit_row<WINDOW>(x, u0 + u) + (j & 15);
-                        if (w == 0xFF800000u && u < nu && (k < vs || (k >= vlo && k < vhi)) &&
-                            ((ld_shared_u32(sb + LP_SM_VALID + (g & 7) * 16 + (u >> 1) * 4) >> ((u & 1) * 16 + (j & 15))) & 1u))
-                            lost[r] = lost[64] = q;
+                        if (w != 0xFF800000u || u >= nu || !(k < vs || (k >= vlo && k < vhi))) continue;
+                        const uint32_t vv = ld_shared_u32(sb + LP_SM_VALID + (g & 7) * 16 + (u >> 1) * 4);
+                        if ((vv >> ((u & 1) * 16 + (j & 15))) & 1u) lost[r] = lost[64] = q;
                     }
                     // (the products' thread, waiting for P, answers; a warp that gave up lets its own wait run out)
                     if (lane == 0) st_dsmem_u32(mapa(sb + LP_SM_WANT, 0), (uint32_t)g + 1);
@@ -949,7 +969,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         for (int it = pair; ok; it += !WINDOW && a.run ? 0 : pairs, ++q) {
             const bool there = lat_item<WINDOW>(a, cur, it, pairs, lane, rank == 0, x);
             if (!there) x.T = -1;
-            if (q >= 4) ok = lat_wait(sb + LP_TAKEN + 8 * (q & 3), ((q >> 2) - 1) & 1, dead);
+            if (q >= 4) ok = __all_sync(0xffffffffu, lat_wait(sb + LP_TAKEN + 8 * (q & 3), ((q >> 2) - 1) & 1, dead));
+            if (!ok) break;  // (the item that is there may be in use)
             if (lane == 0) {
                 *reinterpret_cast<LatItem*>(sm + LP_SM_ITEM + (q & 3) * 128) = x;
                 mbar_arrive(sb + LP_ITEM + 8 * (q & 3));
@@ -958,7 +979,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             if (!there) break;
             const int32_t* pt = a.kv.pt + (int64_t)x.trow * a.kv.pt_stride;
             auto load_q = [&](int k) {
-                if (k > 0) ok = lat_wait(sb + LP_QEMPTY, (k - 1) & 1, dead) && ok;
+                if (k > 0) ok = __all_sync(0xffffffffu, lat_wait(sb + LP_QEMPTY, (k - 1) & 1, dead)) && ok;
                 if (ok && rank == 0 && lane == 0) mbar_arrive_expect_tx(sb + LP_QFULL, 2 * 8 * LP_QSLAB);
                 __syncwarp();
                 if (ok && lane < 8)
@@ -970,7 +991,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const int u0 = (x.t0 + i) * 8, slot = g & 7;
                 // the tile's place in the ring: read by the loading warps eight tiles ago, and no further than
                 // four tiles ahead of them
-                if (g >= 4) ok = lat_wait(sb + LP_USED + 8 * ((g - 4) & 7), ((g - 4) >> 3) & 1, dead);
+                if (g >= 4)
+                    ok = ok && __all_sync(0xffffffffu, lat_wait(sb + LP_USED + 8 * ((g - 4) & 7), ((g - 4) >> 3) & 1, dead));
                 uint32_t* vw = reinterpret_cast<uint32_t*>(sm + LP_SM_VALID) + slot * 4;
                 int* look = reinterpret_cast<int*>(sm + LP_SM_LOOK) + slot * 128;
                 if (BOX) {
@@ -1047,13 +1069,16 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 if (i == 0) ++n;
             }
         }
+        if (!ok && lane == 0) *closed = q;
     } else if (warp >= LP_SOFT + 2) {
         // ---------------------------------------------------------------- key rows
         const uint32_t full0 = mapa(sb + LP_FULL, 0);  // the even CTA's barriers
         int turn = warp - (LP_SOFT + 2);               // slots until this warp's next one
         auto claim = [&](uint32_t pair_bytes) -> bool {  // slot sidx: free, and both CTAs' bytes announced
             const int sl = sidx & (LP_SLOTS - 1);
-            if (sidx >= LP_SLOTS && !lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)) return false;
+            if (sidx >= LP_SLOTS &&
+                !__all_sync(0xffffffffu, lat_wait(sb + LP_EMPTY + 8 * sl, ((sidx / LP_SLOTS) - 1) & 1, dead)))
+                return false;
             if (rank == 0 && lane == 0) {
                 if (pair_bytes) mbar_arrive_expect_tx(sb + LP_FULL + 8 * sl, pair_bytes);
                 else mbar_arrive(sb + LP_FULL + 8 * sl);
@@ -1070,7 +1095,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     if (turn < 4) {  // (six warps: one slot of the four at most)
                         const int kk = turn, gt = g + i, nu = min(8, units - 8 * i);
                         const int mu = (nu + 1) >> 1, ku = min(max(nu - (int)rank * mu, 0), mu), first = (int)rank * mu;
-                        ok = lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead);
+                        ok = __all_sync(0xffffffffu, lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead));
                         const uint32_t look = sb + LP_SM_LOOK + (gt & 7) * 512;
                         sidx += kk;
                         const int sl = sidx & (LP_SLOTS - 1);
@@ -1112,7 +1137,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     const int gt = g + i - 1;
                     if (turn < 4) {
                         const int v = turn, nu = min(8, units - 8 * (i - 1));
-                        ok = ok && lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead);
+                        ok = ok && __all_sync(0xffffffffu, lat_wait(sb + LP_LOOK + 8 * (gt & 7), (gt >> 3) & 1, dead));
                         const uint32_t look = sb + LP_SM_LOOK + (gt & 7) * 512;
                         sidx += v;
                         const int vu = min(max(nu - 2 * v, 0), 2), sl = sidx & (LP_SLOTS - 1);
@@ -1152,7 +1177,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             g += x.T;
         }
     }
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);  // (the products' thread is any lane)
     pdl_launch_dependents();
     if (!ok) {  // a wait ran out: leave the copies and products in flight some time to end
         if (lane == 0) raise_status(a.status, CSA_ERR_TIMEOUT);
