@@ -1297,7 +1297,7 @@ static csa_status check_prefix(int32_t B, int32_t H, int64_t n_shared, int64_t m
 static csa_status check_window(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window, int32_t n_sink) {
     if (H < 1 || H > 128 || B < 1 || B > 65535 || window > (1 << 30) || n_sink > (1 << 30)) return CSA_ERR_UNSUPPORTED;
     if (window < 1 || n_sink < 0 || total_q < 0 || max_q < 1) return CSA_ERR_INVALID_ARG;
-    if (total_q > 0x7FFFFFFFLL / H || max_q > 0x7FFFFFFFLL) return CSA_ERR_UNSUPPORTED;
+    if (total_q > 0x7FFFFFFFLL / H) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }
 
@@ -1377,7 +1377,7 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
 static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, LatArgs* a,
                         int64_t* items) {
     a->rows = (int)(total_q * H);
-    const int64_t per_seq = (max_q * H + 127) / 128;
+    const int64_t per_seq = (std::min<int64_t>(max_q, 0x7FFFFFFF) * H + 127) / 128;
     const int64_t tiles_q = std::min((int64_t)B * per_seq, (total_q * H + 127) / 128 + B);
     // key tiles of a row tile: its tokens' windows and the sinks
     const int64_t keys = (int64_t)window + n_sink + 127 / H + 32;

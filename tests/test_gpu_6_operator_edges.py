@@ -4,8 +4,8 @@ import math
 
 import pytest
 
-from test_gpu_5_operators import (BOUNDS, D, RUNS, SCALE, Cache, attend, check, gen, m, prefix, randn,  # noqa: F401
-                                  window)
+from test_gpu_5_operators import (BOUNDS, D, RUNS, SCALE, Cache, attend, check, check_window, gen, m, prefix,  # noqa: F401
+                                  randn, window)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -317,4 +317,67 @@ def test_attention_of_no_scale_over_large_rows(m, call, scale):  # noqa: F811
         o, a = kv.mean(0).expand(H, D), kv.abs().mean(0)
         want = torch.full((H,), math.log(len(kv)), dtype=torch.float64, device="cuda")
         check(out[b], lse[b], (o, want, 2.0**-8 * (a + o.abs()) + 2.0**-20 * a, 2.0**-20 * (1 + want)), f"request {b}")
+    assert m.csa_read_device_status() == 0
+
+
+# ------------------------------------------------------------------ bounds and batches
+@pytest.mark.parametrize("max_q", [1 << 31, (1 << 63) - 1])
+def test_window_attention_with_any_bound_on_new_tokens(m, max_q):  # noqa: F811
+    g = gen(52)
+    q_len, n_tokens = [40, 1, 3], [300, 2000, 3]
+    c = Cache(g, n_tokens, 64)
+    q = randn(g, 44, 20, D)
+    want, lse = window(m, q, c, q_len, n_tokens, 700, 3, max_q=(1 << 31) - 1)
+    out, lse2 = window(m, q, c, q_len, n_tokens, 700, 3, max_q=max_q)
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+    check_window(q, c, q_len, n_tokens, 700, 3, out, lse2, every=7)
+    assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("H,B", [(1, 300), (2, 131), (3, 90)])
+def test_prefix_attention_of_many_requests_with_few_heads(m, H, B):  # noqa: F811
+    """Query-row tiles of up to 128 requests, whose lengths lie on both sides of the prefix's end."""
+    g = gen(53)
+    shared = 333
+    n_rows = [(b * 29) % 420 for b in range(B)]
+    c = Cache(g, [max(n, shared) for n in n_rows], 16, shared)
+    q = randn(g, B, H, D)
+    out, lse = prefix(m, q, c, shared, n_rows)
+    for b, n in enumerate(n_rows):
+        kv = torch.cat([c.rows(0, range(min(n, shared))), c.rows(b, range(shared, n))])
+        check(out[b], lse[b], attend(q[b].double(), kv), f"request {b}")
+    assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("H,seqs,W,S,rpp", [
+    (1, [(500, 500), (1, 2), (130, 900)], 60, 3, 64),
+    (2, [(1, 1 + 37 * i) for i in range(140)], 128, 4, 40),   # more sequences than are looked at together
+    (127, [(5, 5), (0, 9), (4, 300)], 33, 0, 16),
+])
+def test_window_attention_of_few_heads_and_many_sequences(m, H, seqs, W, S, rpp):  # noqa: F811
+    g = gen(54)
+    q_len, n_tokens = [s[0] for s in seqs], [s[1] for s in seqs]
+    c = Cache(g, n_tokens, rpp)
+    q = randn(g, sum(q_len), H, D)
+    out, lse = window(m, q, c, q_len, n_tokens, W, S)
+    check_window(q, c, q_len, n_tokens, W, S, out, lse, every=3)
+    assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("at", [10, 600, 1900])
+@pytest.mark.parametrize("call", ["prefix", "window"])
+def test_attention_of_one_dominant_key(m, call, at):  # noqa: F811
+    """A key of the first tile far above all others, and one behind it that weighs up to 2^7.9 times as much: no more than
+    the running maximum lets pass, so that its weight is far above 1 and rounded."""
+    g = gen(55)
+    n, H = 2000, 16
+    c = Cache(g, [n], 64)
+    c.pool.mul_(2.0**-6)
+    u = randn(g, D)
+    up = torch.linspace(0.05, 0.97, H, device="cuda").view(H, 1)
+    q = (u.float() * up).to(torch.bfloat16).view(1, H, D)
+    c.pool[c.row(0, 3)] = u * 2
+    c.pool[c.row(0, at)] = (u.float() * (2 + 7.9 * math.log(2) / (SCALE * float(u.double() @ u.double())))).to(torch.bfloat16)
+    out, lse = prefix(m, q, c, n, [n]) if call == "prefix" else window(m, q, c, [1], [n], n, 0)
+    check(out[0], lse[0], attend(q[0].double(), c.rows(0, range(n))), call)
     assert m.csa_read_device_status() == 0

@@ -165,3 +165,17 @@ def test_page_pools_helper_refuses(csa):
     with pytest.raises(ValueError):
         csa.page_pools([torch.zeros(4, 8, 8).transpose(1, 2)], 4)
     assert csa.status_string(csa.CSA_ERR_NO_PAGES) == "no free page left in the pool"
+
+
+def test_window_attn_takes_any_bound_on_new_tokens(csa):
+    """max_q is a bound, up to the largest integer: beyond the rows of the buffers it bounds nothing."""
+    f = csa.lib().csa_window_attn
+    for args in ((1, 16, 1, 4096, 4), (7, 128, 9000, 128, 4), (3, 5, 40, 1 << 30, 0)):
+        B, H, total, window, sink = args
+        want = csa.csa_window_attn_workspace_size(B, H, total, (1 << 31) - 1, window, sink)
+        for max_q in (1 << 31, 1 << 40, (1 << 63) - 1):
+            assert csa.csa_window_attn_workspace_size(B, H, total, max_q, window, sink) == want
+            if want:
+                assert f(A16, H, 0.04, kv(csa), 10, B, A16, A16, total, max_q, window, sink, A16, A4, A16, want - 1,
+                         None) == csa.CSA_ERR_WORKSPACE
+    assert csa.csa_window_attn_workspace_size(1, 16, 1, (1 << 31) - 1, 4096, 4) > 0
