@@ -342,6 +342,8 @@ def page_pools(pools, n_pages: int) -> csa_page_pools:
     d = csa_page_pools()
     if not 1 <= len(pools) <= CSA_POOLS_MAX:
         raise ValueError(f"1 to {CSA_POOLS_MAX} pools")
+    if n_pages < 1:
+        raise ValueError("a pool has at least one page")
     d.n_pools, d.n_pages = len(pools), n_pages
     for i, t in enumerate(pools):
         if t.shape[0] < n_pages or not t[0].is_contiguous():

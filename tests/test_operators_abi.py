@@ -179,3 +179,10 @@ def test_window_attn_takes_any_bound_on_new_tokens(csa):
                 assert f(A16, H, 0.04, kv(csa), 10, B, A16, A16, total, max_q, window, sink, A16, A4, A16, want - 1,
                          None) == csa.CSA_ERR_WORKSPACE
     assert csa.csa_window_attn_workspace_size(1, 16, 1, (1 << 31) - 1, 4096, 4) > 0
+
+
+def test_page_pools_helper_refuses_empty_pools(csa):
+    torch = pytest.importorskip("torch")
+    for n in (0, -1):
+        with pytest.raises(ValueError):
+            csa.page_pools([torch.zeros(0, 8)], n)
