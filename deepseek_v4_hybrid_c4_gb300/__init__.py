@@ -329,7 +329,9 @@ def csa_window_attn(q, H: int, scale: float, kv_raw: csa_paged, page_table_strid
     """Causal attention of each sequence's new tokens over a sliding window and the first n_sink tokens.
     workspace None: a scratch tensor is allocated."""
     if workspace is None:
-        ws_bytes = csa_window_attn_workspace_size(B, H, total_q, max_q, window, n_sink)
+        reach = min(window + n_sink, max(page_table_stride * kv_raw.rows_per_page, 1 << 18))  # (all that it needs)
+        near = min(window, reach)
+        ws_bytes = csa_window_attn_workspace_size(B, H, total_q, max_q, near, min(n_sink, reach - near))
         workspace = _scratch(ws_bytes, q, stream)
     _check(lib().csa_window_attn(_ptr(q), H, scale, kv_raw, page_table_stride, B, _ptr(q_offsets), _ptr(n_tokens),
                                  total_q, max_q, window, n_sink, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,

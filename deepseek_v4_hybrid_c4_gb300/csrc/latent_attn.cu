@@ -1374,13 +1374,19 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
     a->parts = a->SP + a->OS;
 }
 
-static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, LatArgs* a,
-                        int64_t* items) {
+// positions: those that a row of the page table has pages for.  A window beyond them counts as one of them, down to
+// 2^18 (half of what a split takes at most): wide ones are split because of LP_MAX_TILES, with a partial result of
+// every row for each split, and one that is only meant to reach over everything needs none.
+constexpr int64_t kLeastReach = 1 << 18;
+static_assert(kLeastReach + 256 <= (int64_t)LP_MAX_TILES * 128, "a window of kLeastReach is one split");
+static void plan_window(int B, int H, int64_t total_q, int64_t max_q, int window, int n_sink, int64_t positions,
+                        LatArgs* a, int64_t* items) {
     a->rows = (int)(total_q * H);
     const int64_t per_seq = (std::min<int64_t>(max_q, 0x7FFFFFFF) * H + 127) / 128;
     const int64_t tiles_q = std::min((int64_t)B * per_seq, (total_q * H + 127) / 128 + B);
     // key tiles of a row tile: its tokens' windows and the sinks
-    const int64_t keys = (int64_t)window + n_sink + 127 / H + 32;
+    const int64_t reach = std::min((int64_t)window + n_sink, std::max(positions, kLeastReach));
+    const int64_t keys = reach + 127 / H + 32;
     const int64_t tiles = (keys + 127) / 128;
     int64_t s = 1;
     if (tiles >= 4 && tiles_q <= LP_PAIRS / 2) s = std::min(tiles / 2, LP_PAIRS / std::max<int64_t>(tiles_q, 1));
@@ -1508,7 +1514,7 @@ size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int
                                       int32_t n_sink) {
     if (check_window(B, H, total_q, max_q, window, n_sink)) return 0;
     LatArgs a = {};
-    plan_window(B, H, total_q, max_q, window, n_sink, &a, nullptr);
+    plan_window(B, H, total_q, max_q, window, n_sink, INT64_MAX, &a, nullptr);
     return parts_bytes(a);
 }
 
@@ -1524,7 +1530,8 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
     if ((rc = check_cache(kv_raw, page_table_stride))) return rc;
     LatArgs a = {};
     int64_t items;
-    plan_window(B, H, total_q, max_q, window, n_sink, &a, &items);
+    const int64_t positions = std::min(page_table_stride, LP_MAX_ROWS) * kv_raw.rows_per_page;
+    plan_window(B, H, total_q, max_q, window, n_sink, positions, &a, &items);
     const size_t need = parts_bytes(a);
     if (need && (!workspace || !al16(workspace) || ws_bytes < need)) return CSA_ERR_WORKSPACE;
     if (total_q == 0) return CSA_OK;

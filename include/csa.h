@@ -291,7 +291,9 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
  * 1 <= H <= 128, 1 <= B <= 65535, 1 <= window <= 2^30, 0 <= n_sink <= 2^30, 0 <= total_q,
  * total_q * H < 2^31 (else CSA_ERR_UNSUPPORTED), 1 <= max_q; the limits of csa_prefix_attn on kv.
  * workspace: 16-byte aligned, csa_window_attn_workspace_size(...) bytes, contents overwritten
- * (0 bytes where no key range is split).  With total_q = 0 q and out may be null.  Graph capture: yes.
+ * (0 bytes where no key range is split; beyond 524,288 positions of window and sinks there is a
+ * partial result of every row for each 524,288.  A window that is to reach over everything needs no
+ * more than the size for window + n_sink = the larger of 262,144 and page_table_stride * rows_per_page).  With total_q = 0 q and out may be null.  Graph capture: yes.
  */
 size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
                                       int32_t n_sink);

@@ -381,3 +381,25 @@ def test_attention_of_one_dominant_key(m, call, at):  # noqa: F811
     out, lse = prefix(m, q, c, n, [n]) if call == "prefix" else window(m, q, c, [1], [n], n, 0)
     check(out[0], lse[0], attend(q[0].double(), c.rows(0, range(n))), call)
     assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("W,S", [(1 << 30, 0), (1 << 20, 3), (1, 1 << 30), (1 << 30, 1 << 30)])
+def test_window_attention_over_everything(m, W, S):  # noqa: F811
+    """Windows (or sinks) far wider than the cache, without a workspace given: as many bytes as the cache needs, and
+    for a prompt the same bits as under a window of its own length."""
+    g = gen(56)
+    c = Cache(g, [300, 5000], 64)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    base = torch.cuda.memory_allocated()
+    q = randn(g, 300, 128, D)
+    out, lse = window(m, q, c, [299, 1], [300, 5000], W, S)
+    want, lse2 = window(m, q, c, [299, 1], [300, 5000], 5000, 0)
+    assert torch.cuda.max_memory_allocated() - base < 1 << 30
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+    check_window(q, c, [299, 1], [300, 5000], 5000, 0, out, lse, every=40)
+    q1 = q[:1].contiguous()
+    c.table = c.table[1:].contiguous()
+    out, lse = window(m, q1, c, [1], [5000], W, S)
+    check_window(q1, c, [1], [5000], 5000, 0, out, lse)
+    assert m.csa_read_device_status() == 0

@@ -170,7 +170,7 @@ def test_page_pools_helper_refuses(csa):
 def test_window_attn_takes_any_bound_on_new_tokens(csa):
     """max_q is a bound, up to the largest integer: beyond the rows of the buffers it bounds nothing."""
     f = csa.lib().csa_window_attn
-    for args in ((1, 16, 1, 4096, 4), (7, 128, 9000, 128, 4), (3, 5, 40, 1 << 30, 0)):
+    for args in ((1, 16, 1, 4096, 4), (7, 128, 9000, 128, 4), (3, 5, 40, 1 << 17, 0)):
         B, H, total, window, sink = args
         want = csa.csa_window_attn_workspace_size(B, H, total, (1 << 31) - 1, window, sink)
         for max_q in (1 << 31, 1 << 40, (1 << 63) - 1):
@@ -186,3 +186,24 @@ def test_page_pools_helper_refuses_empty_pools(csa):
     for n in (0, -1):
         with pytest.raises(ValueError):
             csa.page_pools([torch.zeros(0, 8)], n)
+
+
+def test_window_attn_workspace_of_a_window_over_everything(csa):
+    """A window wider than the page table's positions needs the workspace of one that reaches over them, whatever
+    csa_window_attn_workspace_size says for its width."""
+    f = csa.lib().csa_window_attn
+    size = csa.csa_window_attn_workspace_size
+
+    def go(window, sink, nbytes, stride=128, rpp=64):
+        return f(A16, 128, 0.04, kv(csa, rpp=rpp, stride=rpp * 1024), stride, 1, A16, A16, 8192, 8192, window, sink, A16, A4,
+                 A16 if nbytes else None, nbytes, None)
+
+    for window in (1 << 17, 1 << 19, (1 << 19) + 1, 1 << 20, 1 << 30):
+        for sink in (0, 4, 1 << 30):
+            assert go(window, sink, 0) != csa.CSA_ERR_WORKSPACE, (window, sink)
+    # a table row of 2^21 positions: as much as for a window of them
+    need = size(1, 128, 8192, 8192, 1 << 21, 0)
+    assert need > 0
+    for window in (1 << 21, 1 << 22, 1 << 30):
+        assert go(window, 0, need - 1, stride=1 << 15) == csa.CSA_ERR_WORKSPACE
+        assert go(window, 0, need, stride=1 << 15) != csa.CSA_ERR_WORKSPACE
