@@ -485,56 +485,95 @@ __device__ __forceinline__ int quad_map(QuadRuns n, int q, int q0, bool two) {
     return 0;
 }
 
-// 0 times a value that is not finite: dims [at, at + 128) of an output row (of out, or of partial result `part`) whose
-// query saw a logit of -inf become NaN where one of the rows that it sees holds no finite value; all of them where it saw
-// no other logit (l_run 0).  Rare and slow: it reads every row that the query sees.
-__device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part, int at, float l_run) {
-    if (l_run != l_run) return;  // all NaN already
+// 0 times a value that is not finite (a warp; lanes with `go` have a row each): dims [at, at + 128) of an output row (of
+// out, or of partial result `part`) whose query saw a logit of -inf become NaN where one of the rows that it sees holds no
+// finite value; all of them where it saw no other logit (l_run 0).  Rare: the warp reads all rows that its queries see,
+// two at a time, eight in flight, and each lane gathers the dims of those that its own query sees.
+__device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part, int at, float l_run, bool go) {
     const bool direct = a.parts == 1;
     const int64_t to = (direct ? (int64_t)row : (int64_t)part * a.rows + row) * D + at;
     auto put = [&](int d) {
         if (direct) a.out[to + d] = 0x7FFFu;
         else a.part_o[to + d] = __int_as_float(0x7FFFFFFF);
     };
-    if (l_run == 0.f) {
+    if (l_run != l_run) go = false;  // all NaN already
+    if (go && l_run == 0.f) {
         if (direct) {
             for (int d = 0; d < 128; ++d) put(d);
-            return;
+            go = false;
+        } else if (at == 0) {
+            a.part_lse[(int64_t)part * a.rows + row] = LP_LSE_LOST;
         }
-        if (at == 0) a.part_lse[(int64_t)part * a.rows + row] = LP_LSE_LOST;
     }
-    int lo, hi, sinks = 0, b = div_by(row, a.by_H);
-    if (a.n_rows) {
-        const int64_t n = __ldg(a.n_rows + b);
-        lo = part < a.SP ? 0 : a.n_shared;
-        hi = (int)max(min(n, (int64_t)(part < a.SP ? a.n_shared : a.max_rows)), (int64_t)0);
-        if (part < a.SP) b = 0;
-    } else {
-        const int64_t tok = b;
-        b = seq_of(a, tok);
-        const int64_t q1 = __ldg(a.q_offsets + b + 1), nt = __ldg(a.n_tokens + b);
-        if (!seq_valid(a, __ldg(a.q_offsets + b), q1, nt)) return;
-        hi = (int)max(nt - (q1 - tok) + 1, (int64_t)0);
-        lo = max(0, hi - a.window);
-        sinks = min(a.n_sink, lo);
+    int lo = 0, hi = 0, sinks = 0, b = 0;
+    if (go) {
+        b = div_by(row, a.by_H);
+        if (a.n_rows) {
+            const int64_t n = __ldg(a.n_rows + b);
+            lo = part < a.SP ? 0 : a.n_shared;
+            hi = (int)max(min(n, (int64_t)(part < a.SP ? a.n_shared : a.max_rows)), (int64_t)0);
+            if (part < a.SP) b = 0;
+        } else {
+            const int64_t tok = b;
+            b = seq_of(a, tok);
+            const int64_t q0 = __ldg(a.q_offsets + b), q1 = __ldg(a.q_offsets + b + 1), nt = __ldg(a.n_tokens + b);
+            hi = seq_valid(a, q0, q1, nt) ? (int)max(nt - (q1 - tok) + 1, (int64_t)0) : 0;
+            lo = max(0, hi - a.window);
+            sinks = min(a.n_sink, lo);
+        }
     }
-    const int32_t* pt = a.kv.pt + (int64_t)b * a.kv.pt_stride;
+    const unsigned all = 0xffffffffu, who = __ballot_sync(all, go);
+    if (!who) return;
+    // the rows of an item come through one row of the table: sinks, then what any of the queries sees
+    const int32_t* pt = a.kv.pt + (int64_t)__shfl_sync(all, b, __ffs(who) - 1) * a.kv.pt_stride;
+    const int s1 = __reduce_max_sync(all, sinks);
+    const int l1 = max(__reduce_min_sync(all, go ? lo : 0x7FFFFFFF), s1), h1 = __reduce_max_sync(all, hi);
+    const uint32_t total = (uint32_t)s1 + (uint32_t)max(h1 - l1, 0);
+    auto key = [&](uint32_t k) { return k < (uint32_t)s1 ? (int)k : (int)(k - (uint32_t)s1) + l1; };
+    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+    uint32_t acc[4] = {0, 0, 0, 0};  // [x / 2], 16 bits for each x: bit c is dim 8 c + x
 #pragma unroll 1
-    for (int j = sinks > 0 ? 0 : lo; j < hi; j = j + 1 == sinks ? lo : j + 1) {
-        int slot;
-        const int pg = lat_entry(a, pt, j, slot);
-        if (pg < 0 || pg >= a.kv.n_pages) continue;
-        const uint4* p = reinterpret_cast<const uint4*>(a.kv.base + (int64_t)pg * a.kv.page_stride +
-                                                        (int64_t)slot * ROW_BYTES + at * 2);
-#pragma unroll 4
-        for (int d = 0; d < 128; d += 8) {
-            const uint4 v = __ldg(p + (d >> 3));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (uint32_t k0 = 0; k0 < total; k0 += 8) {
+        uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (((w[e >> 1] >> (16 * (e & 1))) & 0x7F80u) == 0x7F80u) put(d + e);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t k = k0 + 2 * e + half;
+            v[e] = make_uint4(0, 0, 0, 0);
+            if (k >= total) continue;
+            int slot;
+            const int pg = lat_entry(a, pt, key(k), slot);
+            if (pg < 0 || pg >= a.kv.n_pages) continue;
+            v[e] = __ldg(reinterpret_cast<const uint4*>(a.kv.base + (int64_t)pg * a.kv.page_stride +
+                                                        (int64_t)slot * ROW_BYTES + at * 2) + c);
+        }
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+            const uint4 u = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            uint32_t bad = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (((w[x >> 1] >> (16 * (x & 1))) & 0x7F80u) == 0x7F80u) bad |= 1u << x;
+            if (!__any_sync(all, bad != 0)) continue;
+            uint32_t sees = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = k0 + 2 * e + h;
+                const int j = key(k);
+                if (go && k < total && (j < sinks || (j >= lo && j < hi))) sees |= 0xFFFFu << (16 * h);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t m = __ballot_sync(all, (bad >> x) & 1u) & sees;
+                acc[x >> 1] |= ((m | (m >> 16)) & 0xFFFFu) << (16 * (x & 1));
+            }
         }
     }
+#pragma unroll 1
+    for (int d = 0; d < 16; ++d)
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if ((acc[x >> 1] >> (16 * (x & 1) + d)) & 1u) put(8 * d + x);
 }
 
 template <bool BOX, bool WINDOW>
@@ -863,7 +902,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 tc_fence_before();
                 if (lost[64] == q) {
                     __syncwarp();  // (behind the other lanes' stores to this lane's row)
-                    if (mine && lost[r] == q) lat_not_finite(a, row, x.part, half * 256 + ch * 128, l_run);
+                    lat_not_finite(a, row, x.part, half * 256 + ch * 128, l_run, mine && lost[r] == q);
                 }
             }
         }
