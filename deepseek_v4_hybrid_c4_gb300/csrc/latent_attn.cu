@@ -16,8 +16,8 @@
 // a tile against 2,048 at the nominal rate.
 //
 // What bounds it.  Many query rows over a long prefix: the tensor cores under the power limit (4,096 rows over
-// 32K keys, 276 GFLOP: 158 us with the same inputs again, 181 us with others, 1.53 PFLOP/s).  A prompt under a
-// short window: the softmax warps' chain through an item (8,192 tokens of 128 heads, window 128: 459 us, 4.7 TB/s
+// 32K keys, 276 GFLOP: 161 us with the same inputs again, 183 us with others, 1.51 PFLOP/s).  A prompt under a
+// short window: the softmax warps' chain through an item (8,192 tokens of 128 heads, window 128: 461 us, 4.7 TB/s
 // of queries and outputs; 40 percent of an item is its output).  Single tokens: one chain of dependent loads,
 // products and stores, 9 to 11 us.
 //
@@ -27,7 +27,8 @@
 // barriers.  The code is kept small and, for the products, free of branches: with the items worked out in
 // every role and a wait before each slot's products, the kernel was 175 KB of code, every step of a role
 // cost some 200 cycles (the waits themselves were over at once), and a tile took 4,400 cycles.  Windows and
-// prefixes are separate kernels (a shared one: prefixes 2 to 5 percent slower), 63 to 67 KB each.
+// prefixes are separate kernels (a shared one: prefixes 2 to 5 percent slower), 64 to 68 KB each, and 14 KB
+// (lat_not_finite) that only infinities call.
 // Key rows come through a ring of 8 slots of 16 KB in the order in which the products take them: S of a tile
 // in four slots (128 dims each of the CTA's own keys), P V in four (32 keys each, the CTA's half of the
 // dims; empty ones in a short tile).  The order is S(0), then S(i+1), PV(i): the softmax of tile i runs beside S(i+1).
@@ -41,7 +42,10 @@
 // maxima.  The running maximum moves only when a tile exceeds it by 2^8 (O is then rescaled in TMEM);
 // P is rounded to bf16 for the product, its sum is taken in fp32 before the rounding.  P and O wait for the
 // product before; the last tile of a window item, when it is short, has a place of its own for P and waits only to
-// rescale O (a prompt of 8K tokens: 524 -> 503 us).
+// rescale O (a prompt of 8K tokens: 524 -> 503 us).  So a weight is off by up to half a bf16 step, also a dominant one whose
+// tile did not move the maximum, and an output by as much of its weighted absolute values; a second sum, of the rounded
+// weights, would cancel the dominant one's share and cost 2 percent (a prompt of 8K tokens: 462 -> 470 us; mean errors against
+// 64 bits stay 1.7 to 2.1e-3, where the output's own rounding alone is 1.65e-3).
 //
 // A masked weight is exactly 0, but 0 * NaN is NaN, and the products see every row of a unit.  In
 // a tile with masked rows a NaN or an infinity in any row makes that row's logits of all 128 query rows
@@ -499,6 +503,7 @@ __device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part,
     if (l_run != l_run) go = false;  // all NaN already
     if (go && l_run == 0.f) {
         if (direct) {
+#pragma unroll 1
             for (int d = 0; d < 128; ++d) put(d);
             go = false;
         } else if (at == 0) {
@@ -1363,7 +1368,8 @@ static int64_t deal_cost(int64_t n1, int64_t t1, int64_t n2, int64_t t2) {
 
 // How the tiles are dealt to the pairs: the splits of the shared rows (SP) and of a request's own (OS) that end
 // soonest, or runs (then SP and OS are the most partial results that a row has of each); a partial result of every row,
-// written and read again, costs about 1.4 tiles for each 4,096 rows.
+// written and read again, is taken to cost 1.4 tiles for each 4,096 rows (16 MB through L2 beside the products) and 0.02
+// for its place in the merge: estimates, which the shapes below bear out.
 static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArgs* a) {
     a->rows = B * H;
     a->RT = (a->rows + 127) / 128;
@@ -1389,8 +1395,10 @@ static void plan_prefix(int B, int H, int64_t n_shared, int64_t max_rows, LatArg
     // end in a run's midst and of row tiles that read the same keys at different times.  Behind each row tile's or
     // request's tiles are places that stand for an item's cost beside its tiles (three and two: 158 and 60.6 us for
     // the two cases below; three and three 158 and 62.4, two and two 159 and 61.3, one and one 171 and 62.3).
-    // 32 requests of 128 heads over 32K rows + 300: 171.6 us in splits, 158.0 in runs; of 16 heads over 64K + 2K: 65.3
-    // and 60.6; where the splits come out even (8 x 128 over 8K + 512, one item a pair) they are the faster by the same rule.
+    // 32 requests of 128 heads over 32K rows + 300: 174.7 us in splits, 160.7 in runs; of 16 heads over 64K + 2K: 65.4
+    // and 61.3; where the splits come out even (8 x 128 over 8K + 512, one item a pair) they are the faster, 23.3 to 24.4.
+    // Over 18 shapes (1 to 100 requests, 3 to 128 heads, 1 to 131K shared rows) runs alone were up to 7 percent slower
+    // and splits alone up to 12; this choice was never more than 2 percent behind the better of the two.
     const int64_t gS = tiles ? tiles + 3 : 0, gO = own ? own + 2 : 0, inS = a->RT * gS, inO = B * gO;
     if (inS + inO >= 4 * LP_PAIRS && std::max(inS, inO) < 1 << 30) {
         int64_t C = (inS + inO + LP_PAIRS - 1) / LP_PAIRS;

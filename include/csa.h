@@ -250,12 +250,16 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * row b (csa_pages_fork makes such tables).  For request b and head h, over j < n_rows[b]:
  *   l_j = scale * q_bh . K_j,  o_bh = softmax(l) . V   (K = V = the row)
  * q bf16 [B, H, 512]; n_rows device int64 [B], 0 <= n_rows[b] <= max_rows (a length outside is
- * taken for the nearest one inside, and the device status gets CSA_ERR_DEVICE_BOUNDS); n_rows[b] may be
- * below n_shared, and 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32 [B, H] (natural
- * log, nullable).  Entries of the page table behind a request's rows are not read.  A page id
- * outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
- * infinity reaches only the requests that attend it, and those as the formula has it: a logit of NaN or +inf
- * leaves a head no finite output, one of -inf is a weight of 0, and 0 times what is not finite is NaN.
+ * taken for the nearest one inside, and the device status gets CSA_ERR_DEVICE_BOUNDS); n_rows[b] may
+ * be below n_shared, and 0 leaves the request empty: out 0, lse -inf.  out bf16 [B, H, 512]; lse fp32
+ * [B, H] (natural log, nullable).  Entries of the page table behind a request's rows are not read.  A
+ * page id outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
+ * infinity reaches only the requests that attend it, and those as the formula has it: a logit of NaN
+ * or +inf leaves a head no finite output (nor do logits that are all -inf), one of -inf is a weight of
+ * 0, and 0 times what is not finite is NaN.
+ * Weights are rounded to bf16 for the product with V, their sums and lse are fp32 and taken before
+ * that: an output is off by up to 2^-8 of its weighted sum of |V| (over hundreds of thousands of rows
+ * in one range by up to twice that, from fp32 sums) and by its own rounding to bf16.
  * B * H rows are padded to 128-row tensor-core tiles; key ranges are split and merged by
  * log-sum-exp, in a fixed order: the same inputs give the same bits.  A range holds up to 524,288
  * rows, so that the workspace grows with max_rows beyond that.
@@ -281,19 +285,20 @@ csa_status csa_prefix_attn(const void* q, int32_t B, int32_t H, float scale, csa
  * q bf16 [total_q, H, 512]; out bf16 [total_q, H, 512]; lse fp32 [total_q, H] (nullable).  Rows of
  * out and lse that no sequence covers are left as they were.  total_q and max_q are host bounds: the
  * rows of the buffers, and the most new tokens of a sequence; a sequence whose offsets leave them, or
- * whose n_tokens is above 2^31 - 128, is skipped (CSA_ERR_DEVICE_BOUNDS).  A token before position 0 (more new tokens than n_tokens)
- * sees nothing: out 0, lse -inf.  Pages that hold only positions no new token sees are not read and
- * their table entries may be anything (a cache that gives the pages behind the window back).  A page
- * id outside the pool, or a position behind page_table_stride pages, leaves its rows out
- * (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an infinity reaches only the tokens that see it,
- * as in csa_prefix_attn.
+ * whose n_tokens is above 2^31 - 128, is skipped (CSA_ERR_DEVICE_BOUNDS).  A token before position 0
+ * (more new tokens than n_tokens) sees nothing: out 0, lse -inf.  Pages that hold only positions no
+ * new token sees are not read and their table entries may be anything (a cache that gives the pages
+ * behind the window back).  A page id outside the pool, or a position behind page_table_stride pages,
+ * leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an infinity reaches only the
+ * tokens that see it, as in csa_prefix_attn, and the accuracy is the same.
  * The same inputs give the same bits.
  * 1 <= H <= 128, 1 <= B <= 65535, 1 <= window <= 2^30, 0 <= n_sink <= 2^30, 0 <= total_q,
  * total_q * H < 2^31 (else CSA_ERR_UNSUPPORTED), 1 <= max_q; the limits of csa_prefix_attn on kv.
  * workspace: 16-byte aligned, csa_window_attn_workspace_size(...) bytes, contents overwritten
  * (0 bytes where no key range is split; beyond 524,288 positions of window and sinks there is a
  * partial result of every row for each 524,288.  A window that is to reach over everything needs no
- * more than the size for window + n_sink = the larger of 262,144 and page_table_stride * rows_per_page).  With total_q = 0 q and out may be null.  Graph capture: yes.
+ * more than the size for window + n_sink = the larger of 262,144 and page_table_stride *
+ * rows_per_page).  With total_q = 0 q and out may be null.  Graph capture: yes.
  */
 size_t csa_window_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
                                       int32_t n_sink);
