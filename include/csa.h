@@ -256,7 +256,7 @@ csa_status csa_attn_merge(const float* o_parts, const float* lse_parts, int32_t 
  * page id outside the pool leaves its rows out (CSA_ERR_DEVICE_BOUNDS).  A row that holds a NaN or an
  * infinity reaches only the requests that attend it, and those as the formula has it: a logit of NaN
  * or +inf leaves a head no finite output (nor do logits that are all -inf), one of -inf is a weight of
- * 0, and 0 times what is not finite is NaN.
+ * 0, and 0 times what is not finite is NaN.  A scale of 0 counts as the least number above 0.
  * Weights are rounded to bf16 for the product with V, their sums and lse are fp32 and taken before
  * that: an output is off by up to 2^-8 of its weighted sum of |V| (over hundreds of thousands of rows
  * in one range by up to twice that, from fp32 sums) and by its own rounding to bf16.
