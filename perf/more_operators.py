@@ -280,9 +280,7 @@ def _own_write(s):
     c = s["case"]
     m.csa_quant_write(s["rows"], _cache(m, s), s["table"].shape[1], c["B"], s["offsets"], s["n_tokens"], s["total"],
                       c["q"])
-    if "values" not in s:                                 # (views, which a program makes once)
-        s["values"] = _values(s["pool"], c["rpp"])
-    return s["values"]
+    return _values(s["pool"], c["rpp"])
 
 
 def _own_read(s):
