@@ -1154,9 +1154,28 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const float ref = even ? yref - tpow - LQ_ROOM : mref;
                 const uint64_t sl2 = f32x2(tsl2, tsl2), mneg = f32x2(-ref, -ref);
                 uint64_t sum = 0;
+                // (rows with scales of their own: a weight times its scale by an exponential of its own, as a weight and a
+                // scale may each be next to nothing, or a scale and what the product is kept over)
+                const bool two = QUANT && LAT_RARE(!even && some);
+                if (two) {
+                    const float shift = LQ_ROOM - yref;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (c < nc) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                const uint2 f = ld_shared_v2(fa + 64 * c + 4 * j);
+                                const uint64_t y = f32x2(xs[16 * c + j], xs[16 * c + j + 1]);
+                                const float2 e = f32x2_split(f32x2_fma(y, sl2, mneg));
+                                const float2 t = f32x2_split(f32x2_fma(y, sl2, f32x2(q_log(f.x) + shift, q_log(f.y) + shift)));
+                                sum = f32x2_add(sum, f32x2(lat_ex2(e.x), lat_ex2(e.y)));
+                                xs[16 * c + j] = lat_ex2(t.x), xs[16 * c + j + 1] = lat_ex2(t.y);
+                            }
+                        }
+                }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (c < nc && some) {
+                    if (c < nc && some && !two) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float2 e = f32x2_split(f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), sl2, mneg));
@@ -1170,22 +1189,6 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const float2 ss = f32x2_split(sum);
                 l_run = l_run * alpha_l + (even ? lat_ex2(ref - mref) * (ss.x + ss.y) : ss.x + ss.y);
                 if (QUANT && some) {
-                    if (LAT_RARE(!even)) {  // weights times scales
-                        const float gain = lat_ex2(mref - yref + LQ_ROOM);
-                        const uint64_t g2 = f32x2(gain, gain);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            if (c < nc) {
-#pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const uint4 f = ld_shared_v4(fa + 64 * c + 4 * j);
-                                    float* y = xs + 16 * c + j;
-                                    const float2 p = f32x2_split(f32x2_mul(f32x2_mul(f32x2(y[0], y[1]), f32x2_bits(f.x, f.y)), g2));
-                                    const float2 o = f32x2_split(f32x2_mul(f32x2_mul(f32x2(y[2], y[3]), f32x2_bits(f.z, f.w)), g2));
-                                    y[0] = p.x, y[1] = p.y, y[2] = o.x, y[3] = o.y;
-                                }
-                            }
-                    }
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         if (c < nc) {
@@ -1274,7 +1277,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 if (QUANT) named_bar_sync(1, 32 * LP_SOFT);  // (the next tile's maxima go there)
             }
             float inv = l_run == 0.f ? 0.f : 1.f / l_run, old = 0.f;  // what was there counts `old`
-            if (QUANT && l_run != 0.f) inv *= lat_ex2(y_run - m_run - LQ_ROOM);
+            // quantised: O's unit too; one next to nothing would leave inv no bits, so that its root comes in twice
+            float root = 1.f;
+            if (QUANT && l_run != 0.f) {
+                const float unit = y_run - m_run - LQ_ROOM;
+                if (LAT_RARE(unit < -64.f)) root = lat_ex2(0.5f * unit);
+                else inv *= lat_ex2(unit);
+            }
             const bool direct = QUANT ? (x.shared & QUANT_DIRECT) != 0 : a.parts == 1;
             const bool more = QUANT && (x.shared & QUANT_MORE) != 0;
             // this row of the partial results
@@ -1316,7 +1325,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     ok = lat_wait<QUANT>(sb + LP_PVDONE + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, dead) && ok;
                     tc_fence_after();
                 }
-                if (LAT_RARE(more)) {
+                if (LAT_RARE(more || (QUANT && __any_sync(0xffffffffu, root != 1.f)))) {
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
                         uint32_t o[32];
@@ -1324,7 +1333,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         tc_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), inv, had ? old * __ldcg(was + c + e) : 0.f));
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]) * inv * root, root, had ? old * __ldcg(was + c + e) : 0.f));
                         tc_st32(tmem + lane_off + 128 * ch + c, o);
                     }
                     tc_wait_st();

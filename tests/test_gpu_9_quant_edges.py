@@ -1,0 +1,65 @@
+"""The quantised latent cache at the ends of its ranges: scales far apart, rows of nothing, queries and rows of any size,
+codes that are no numbers, many short items, and the merge over a list of any contents."""
+import math
+
+import pytest
+
+from test_gpu_5_operators import D, SCALE, attend, gen, m, randn  # noqa: F401
+from test_gpu_6_operator_edges import capped  # noqa: F401
+from test_gpu_7_operator_draws import check_formula
+from test_gpu_8_quant import ALL, Cache, attention, check_tokens, keys, power, values
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def places(c, b, n):
+    js = torch.arange(n, device="cuda")
+    return c.table[b].long()[js // c.rpp], js % c.rpp
+
+
+def set_scales(c, b, codes):
+    """Scale codes of a sequence's rows: [n] (all four blocks) or [n, 4]."""
+    page, slot = places(c, b, len(codes))
+    c.scales()[page, slot] = (codes if codes.dim() == 2 else codes.view(-1, 1).expand(-1, 4)).to(torch.uint8)
+
+
+def set_codes(c, b, codes):
+    page, slot = places(c, b, len(codes))
+    c.codes()[page, slot] = codes.to(torch.uint8)
+
+
+FORMS = [(16, 1, 256), (128, 3, 3000), (128, 310, 1000)]  # heads, new tokens, rows: one item, cut row tiles, whole row tiles
+
+
+def check_tiny(c, q, out, lse, n, tokens):
+    """As check_tokens, with what results below 2^-126 lose as bf16: half of their step of 2^-133 at most."""
+    for i in tokens:
+        kv = c.rows(0, range(n - q.shape[0] + i + 1))
+        o, l, to, tl = attend(q[i].double(), kv)
+        assert float(((out[i].double() - o).abs() - to - 2.0**-133).max()) <= 0, i
+        assert float(((lse[i].double() - l).abs() - tl).max()) <= 0, i
+
+
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+@pytest.mark.parametrize("scale", [0, 1, 5, 6, 9, 10, 11, 20])
+def test_rows_of_next_to_nothing(m, H, q_len, n, scale):  # noqa: F811
+    """The least scales there are, with codes of 0 (a pool of zero bytes has scales of 0) and with others."""
+    g = gen(scale)
+    c = Cache(g, [n], 64)
+    q = randn(g, q_len, H, D)
+    c.scales()[:] = scale
+    kept = c.codes().clone()
+    c.codes()[:] = 0
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    assert bool((out == 0).all())
+    want = torch.log(torch.arange(n - q_len + 1, n + 1, device="cuda").double()).view(-1, 1)
+    assert float(((lse.double() - want).abs() - 2.0**-20 * (1 + want)).max()) <= 0
+    c.codes()[:] = kept
+    out, lse = attention(m, c, q, [q_len], [n])
+    check_tiny(c, q, out, lse, n, sorted({0, q_len // 2, q_len - 1}))
+    # some rows of ordinary size among them
+    set_scales(c, 0, torch.where(torch.arange(n, device="cuda") % 97 == 5, 118, scale))
+    out, lse = attention(m, c, q, [q_len], [n])
+    check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in {0, q_len // 2, q_len - 1}])
