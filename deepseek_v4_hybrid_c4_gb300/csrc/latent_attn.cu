@@ -124,6 +124,7 @@ constexpr uint32_t LP_SM_QTOP = LP_SM_NEXT;
 static_assert(LP_SM_RATIO + 4 * 1024 <= LP_SM_BAR && LP_QTOP + 16 <= LP_SM_BAR + 512, "places of quantised rows");
 constexpr uint32_t LQ_PLAIN = 1, LQ_EVEN = 2, LQ_HUGE = 4; // of a tile: plain; one factor for all rows; values of 2^128
 constexpr float LQ_ROOM = 7.f;                             // weights are at most 2^(LP_RESCALE + LQ_ROOM) in fp16
+constexpr float LQ_APART = 64.f;                          // log2: how far sums may lie below their weights
 constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
 // Tiles of a split at most: O takes eight additions a tile in the tensor cores, each of which may lose 2^-23 of the
 // sum so far, in all no more than the 2^-8 that a rounded weight may be off.
@@ -1150,14 +1151,16 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 const float yref = QUANT && y_run != -INFINITY ? y_run : 0.f;
-                // (quantised and one scale: the weight in fp16 times that scale at once, and the sum without it)
-                const float ref = even ? yref - tpow - LQ_ROOM : mref;
+                // Quantised and one scale: the weight in fp16 times that scale at once, and the sum without it.  Rows with scales
+                // of their own, and a scale so far below the others that the sum's terms would be lost under 2^-126: a
+                // weight times its scale has an exponential of its own (a weight, a scale and the largest product may each
+                // be next to nothing).
+                const float apart = yref - tpow - LQ_ROOM - mref;
+                const bool two = QUANT && some && (LAT_RARE(!even) || __any_sync(0xffffffffu, apart > LQ_APART));
+                const float ref = even && !two ? yref - tpow - LQ_ROOM : mref;
                 const uint64_t sl2 = f32x2(tsl2, tsl2), mneg = f32x2(-ref, -ref);
                 uint64_t sum = 0;
-                // (rows with scales of their own: a weight times its scale by an exponential of its own, as a weight and a
-                // scale may each be next to nothing, or a scale and what the product is kept over)
-                const bool two = QUANT && LAT_RARE(!even && some);
-                if (two) {
+                if (LAT_RARE(two)) {
                     const float shift = LQ_ROOM - yref;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)

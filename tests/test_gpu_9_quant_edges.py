@@ -32,6 +32,23 @@ def set_codes(c, b, codes):
 FORMS = [(16, 1, 256), (128, 3, 3000), (128, 310, 1000)]  # heads, new tokens, rows: one item, cut row tiles, whole row tiles
 
 
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+@pytest.mark.parametrize("first,second", [(147, 12), (12, 147), (146, 12), (200, 60), (60, 200), (127, 11), (246, 11),
+                                          (11, 246), (140, 70)])
+def test_tiles_whose_scales_lie_far_apart(m, H, q_len, n, first, second):  # noqa: F811
+    """Tiles of 128 rows with one scale each, by turns of two: every row counts in the sum of the weights."""
+    g = gen(first)
+    c = Cache(g, [n], 64)
+    js = torch.arange(n, device="cuda")
+    set_scales(c, 0, torch.where(js // 128 % 2 == 0, first, second))
+    # logits of a few units: a row's values are some 2^7 times its scale
+    q = (randn(g, q_len, H, D).double() * power(torch.tensor(127 - 7 - max(first, second), device="cuda"))).to(torch.bfloat16)
+    q[:, ::3] = 0
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in {0, q_len // 2, q_len - 1}])
+
+
 def check_tiny(c, q, out, lse, n, tokens):
     """As check_tokens, with what results below 2^-126 lose as bf16: half of their step of 2^-133 at most."""
     for i in tokens:
