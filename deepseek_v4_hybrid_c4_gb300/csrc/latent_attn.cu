@@ -73,6 +73,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <limits>
 
 #include "common.cuh"
@@ -122,9 +123,11 @@ constexpr uint32_t LP_QTOP = LP_QREADY + 8;                // and its rows' expo
                                                           // queries may be one item ahead of the softmax, not two)
 constexpr uint32_t LP_SM_QTOP = LP_SM_NEXT;
 static_assert(LP_SM_RATIO + 4 * 1024 <= LP_SM_BAR && LP_QTOP + 16 <= LP_SM_BAR + 512, "places of quantised rows");
-constexpr uint32_t LQ_PLAIN = 1, LQ_EVEN = 2, LQ_HUGE = 4; // of a tile: plain; one factor for all rows; values of 2^128
+// Of a tile: plain; one factor for all rows; values of 2^128; from bit 8 on the largest scale code of its rows.
+constexpr uint32_t LQ_PLAIN = 1, LQ_EVEN = 2, LQ_HUGE = 4;
+constexpr int LQ_TOP = 8;
 constexpr float LQ_ROOM = 7.f;                             // weights are at most 2^(LP_RESCALE + LQ_ROOM) in fp16
-constexpr float LQ_APART = 64.f;                          // log2: how far sums may lie below their weights
+constexpr int LQ_APART = 60;                              // log2: how far sums may lie below their weights
 constexpr int64_t LP_MAX_ROWS = 0x7FFFFFFF - 127;         // of a request: a row id behind its last tile is an int too
 // Tiles of a split at most: O takes eight additions a tile in the tensor cores, each of which may lose 2^-23 of the
 // sum so far, in all no more than the 2^-8 that a rounded weight may be off.
@@ -154,6 +157,7 @@ struct LatArgs {
     int H;
     FastDiv by_H;
     float sl2;                 // |scale| * log2(e); the sign is in the products
+    int sl2_power;             // quantised rows: its power of two, and sl2 is in [1, 2)
     uint32_t negate;           // instruction-descriptor bit that negates Q
     DPaged kv;
     int64_t table_pages;       // entries of a request's page table
@@ -777,15 +781,22 @@ __device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part,
             if ((acc[x >> 1] >> (16 * (x & 1) + d)) & 1u) put(8 * d + x);
 }
 
-// Log2 units of a logit of a row whose largest value has the exponent E.
-__device__ __forceinline__ float lat_q_unit(float sl2, uint32_t E) {
-    return fmaxf(sl2 * __uint_as_float((E - 14u) << 23), __int_as_float(1));
+// Quantised rows: log2 units of a logit, sl2 2^e with sl2 in [1, 2): the scale's, the query's and the row's powers of two are
+// added up in e, before any of them could pass fp32's range.  At least the least number above 0 (a masked logit stays
+// -inf), and finite (one of 0 stays 0).
+__device__ __forceinline__ float lat_unit(float sl2, int e) {
+    e = min(max(e, -252), 254);
+    const int h = e >> 1;
+    const float u = sl2 * __uint_as_float((uint32_t)(h + 127) << 23) * __uint_as_float((uint32_t)(e - h + 127) << 23);
+    return fminf(fmaxf(u, __int_as_float(1)), 3.4028235e38f);
 }
+// The part of e of a query whose largest value has the exponent E and is now in [2^14, 2^15).
+__device__ __forceinline__ int lat_q_power(uint32_t E) { return (int)E - 141; }
 
 // The CTA's 64 rows of Q in place from bf16 to fp16, each with its largest value in [2^14, 2^15) (the softmax
-// warps).  Returns the row's log2 units of a logit.  A value 2^29 below its row's largest still has all
+// warps).  Returns the row's lat_q_power().  A value 2^29 below its row's largest still has all
 // its bits, and what is lost of smaller ones is 2^-39 of the largest.
-__device__ __noinline__ float lat_q_to_f16(uint32_t sb, float* shared, float sl2, int tid, bool wanted) {
+__device__ __noinline__ int lat_q_to_f16(uint32_t sb, float* shared, int tid, bool wanted) {
     const int r = tid & 63;
     const uint32_t row = sb + (uint32_t)(tid >> 6) * 2 * LP_QSLAB + (uint32_t)r * 128;
     uint4 v[16];
@@ -824,7 +835,7 @@ __device__ __noinline__ float lat_q_to_f16(uint32_t sb, float* shared, float sl2
     fence_proxy_async_smem();
     __syncwarp();
     if ((tid & 31) == 0) mbar_arrive_rank(sb + LP_QREADY, 0);
-    return lat_q_unit(sl2, E);
+    return lat_q_power(E);
 }
 
 // The same by the two warps that do nothing else, of all items but the first, a lane a row: beside the softmax and the output
@@ -916,7 +927,8 @@ __device__ __noinline__ uint32_t quant_uneven(uint32_t ratios, uint32_t factors,
     st_shared_v4(factors, make_uint4(f[0], f[1], f[2], f[3]));
     st_shared_v4(ratios, make_uint4(r[0], r[1], r[2], r[3]));
     st_shared_v4(ratios + 16, make_uint4(r[4], r[5], r[6], r[7]));
-    return __reduce_max_sync(0xffffffffu, most) >= 247u ? LQ_HUGE : 0u;
+    most = __reduce_max_sync(0xffffffffu, most);
+    return most << LQ_TOP | (most >= 247u ? LQ_HUGE : 0u);
 }
 
 template <LatKeys KEYS, bool WINDOW>
@@ -1015,14 +1027,16 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     vhi = x.hi;
                 }
             }
-            float sl2r = a.sl2;  // log2 units of a logit
+            int qe = 0;  // quantised: the query's and the scale's power of two in its logits
             if (QUANT && x.T > 0) {  // (the first item's queries have nobody else to wait for)
                 ok = lat_wait<QUANT>(sb + (n ? LP_QTOP + 8 * (n & 1) : LP_QFULL), (n ? (n - 1) >> 1 : 0) & 1, dead) && ok;
-                sl2r = n ? lat_q_unit(a.sl2, ld_shared_u8(sb + LP_SM_QTOP + (n & 1) * 64 + r))
-                         : lat_q_to_f16(sb, mx + (g & 1) * 256, a.sl2, tid, some);
+                qe = n ? lat_q_power(ld_shared_u8(sb + LP_SM_QTOP + (n & 1) * 64 + r))
+                       : lat_q_to_f16(sb, mx + (g & 1) * 256, tid, some);
+                qe += a.sl2_power;
                 ++n;
             }
             float m_run = -INFINITY, y_run = -INFINITY, l_run = 0.f;
+            int most = 0;
             for (int i = 0; i < x.T; ++i, ++g) {
                 const int nu = item_units(x, i), mu = (nu + 1) >> 1;  // units in all, and per half
                 const int c0 = ch ? (mu + 1) >> 1 : 0, nc = ch ? mu - c0 : (mu + 1) >> 1;  // this thread's
@@ -1038,30 +1052,38 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     if (c < nc && some) tc_ld16(ts + 16 * c, sr + 16 * c);
                 const uint32_t kind = ld_shared_u32(sb + LP_SM_PLAIN + (g & 7) * 4);
                 const bool plain = QUANT ? (kind & LQ_PLAIN) != 0 : kind != 0;
-                const bool even = QUANT && (kind & LQ_EVEN);  // quantised: one scale for all rows
+                // quantised: one scale for all rows; the largest one, of the item's tiles too
+                const bool even = QUANT && (kind & LQ_EVEN);
+                const int top = (int)(kind >> LQ_TOP);
+                most = max(most, top);
                 tc_wait_ld();
                 float mt = -INFINITY;  // of the logits before scaling
                 bool bad = false;
                 float* xs = reinterpret_cast<float*>(sr);
-                // quantised: the largest weight times its row's scale, in log2 units; the tile's scale, and its log2
-                float yt = -INFINITY, tsl2 = sl2r, tpow = 0.f;
+                // the unit of a logit; quantised: the largest weight times its row's scale, in log2 units; log2 of the tile's scale
+                float yt = -INFINITY, tsl2 = QUANT ? 1.f : a.sl2, tpow = 0.f;
                 const uint32_t fa = sb + LP_SM_FACTOR + (uint32_t)(g & 7) * 512 + (uint32_t)ub * 64;
                 if (QUANT) {
                     if (even) {
-                        const uint32_t f = ld_shared_u32(fa);
-                        tsl2 = fmaxf(sl2r * __uint_as_float(f), __int_as_float(1));
-                        tpow = q_log(f);
+                        const int e = qe + top;  // (biased by 127)
+                        tpow = (float)(top - 127);
+                        tsl2 = a.sl2 * __uint_as_float((uint32_t)e << 23);
+                        if (LAT_RARE((uint32_t)(e - 1) >= 254u)) tsl2 = lat_unit(a.sl2, e - 127);
                     } else if (LAT_RARE(some)) {
+                        // the logits themselves, in log2 units: times what makes them small before the rows' scales, times
+                        // what makes them large behind them
+                        const float u = lat_unit(a.sl2, qe);
+                        const uint64_t u0 = qe < 0 ? f32x2(u, u) : f32x2(1.f, 1.f), u1 = qe < 0 ? f32x2(1.f, 1.f) : f32x2(u, u);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             if (c < nc) {
 #pragma unroll
-                                for (int j = 0; j < 16; j += 4) {
-                                    const uint4 f = ld_shared_v4(fa + 64 * c + 4 * j);
+                                for (int j = 0; j < 16; j += 2) {
+                                    const uint2 f = ld_shared_v2(fa + 64 * c + 4 * j);
                                     float* y = xs + 16 * c + j;
-                                    const float2 p = f32x2_split(f32x2_mul(f32x2(y[0], y[1]), f32x2_bits(f.x, f.y)));
-                                    const float2 o = f32x2_split(f32x2_mul(f32x2(y[2], y[3]), f32x2_bits(f.z, f.w)));
-                                    y[0] = p.x, y[1] = p.y, y[2] = o.x, y[3] = o.y;
+                                    const uint64_t v = f32x2_mul(f32x2_mul(f32x2(y[0], y[1]), u0), f32x2_bits(f.x, f.y));
+                                    const float2 p = f32x2_split(f32x2_mul(v, u1));
+                                    y[0] = p.x, y[1] = p.y;
                                 }
                             }
                     }
@@ -1103,17 +1125,13 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 mt *= tsl2;
                 if (QUANT && LAT_RARE(!even && some)) {
-                    const uint64_t sl = f32x2(sl2r, sl2r);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         if (c < nc) {
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const uint4 f = ld_shared_v4(fa + 64 * c + 4 * j);
-                                const float* y = xs + 16 * c + j;
-                                const float2 p = f32x2_split(f32x2_fma(f32x2(y[0], y[1]), sl, f32x2(q_log(f.x), q_log(f.y))));
-                                const float2 o = f32x2_split(f32x2_fma(f32x2(y[2], y[3]), sl, f32x2(q_log(f.z), q_log(f.w))));
-                                yt = fmaxf(fmaxf(yt, fmaxf(p.x, p.y)), fmaxf(o.x, o.y));
+                            for (int j = 0; j < 16; j += 2) {
+                                const uint2 f = ld_shared_v2(fa + 64 * c + 4 * j);
+                                yt = fmaxf(yt, fmaxf(xs[16 * c + j] + q_log(f.x), xs[16 * c + j + 1] + q_log(f.y)));
                             }
                         }
                 }
@@ -1152,11 +1170,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 const float yref = QUANT && y_run != -INFINITY ? y_run : 0.f;
                 // Quantised and one scale: the weight in fp16 times that scale at once, and the sum without it.  Rows with scales
-                // of their own, and a scale so far below the others that the sum's terms would be lost under 2^-126: a
-                // weight times its scale has an exponential of its own (a weight, a scale and the largest product may each
-                // be next to nothing).
-                const float apart = yref - tpow - LQ_ROOM - mref;
-                const bool two = QUANT && some && (LAT_RARE(!even) || __any_sync(0xffffffffu, apart > LQ_APART));
+                // of their own, and a scale so far below another's that the sum's terms could be lost under 2^-126 (the two
+                // references are at most LP_RESCALE - LQ_ROOM further apart than the scales): a weight times its scale has an
+                // exponential of its own (a weight, a scale and the largest product may each be next to nothing).
+                const bool two = QUANT && some && LAT_RARE(!even || most - top > LQ_APART);
                 const float ref = even && !two ? yref - tpow - LQ_ROOM : mref;
                 const uint64_t sl2 = f32x2(tsl2, tsl2), mneg = f32x2(-ref, -ref);
                 uint64_t sum = 0;
@@ -1175,17 +1192,18 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                                 xs[16 * c + j] = lat_ex2(t.x), xs[16 * c + j + 1] = lat_ex2(t.y);
                             }
                         }
-                }
+                } else {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c < nc && some && !two) {
+                    for (int c = 0; c < 2; ++c) {
+                        if (c < nc && some) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 e = f32x2_split(f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), sl2, mneg));
-                            const float p0 = lat_ex2(e.x), p1 = lat_ex2(e.y);
-                            sum = f32x2_add(sum, f32x2(p0, p1));
-                            if (!QUANT) sr[8 * c + (j >> 1)] = pack_bf16x2(p0, p1);
-                            else xs[16 * c + j] = p0, xs[16 * c + j + 1] = p1;
+                            for (int j = 0; j < 16; j += 2) {
+                                const float2 e = f32x2_split(f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), sl2, mneg));
+                                const float p0 = lat_ex2(e.x), p1 = lat_ex2(e.y);
+                                sum = f32x2_add(sum, f32x2(p0, p1));
+                                if (!QUANT) sr[8 * c + (j >> 1)] = pack_bf16x2(p0, p1);
+                                else xs[16 * c + j] = p0, xs[16 * c + j + 1] = p1;
+                            }
                         }
                     }
                 }
@@ -1612,7 +1630,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     const uint32_t ratios = sb + LP_SM_RATIO + (uint32_t)(g & 3) * 1024 + 32 * lane;
                     const uint32_t factors = sb + LP_SM_FACTOR + (uint32_t)(g & 7) * 512 + 16 * lane;
                     if (most - 11u < 236u && most - least <= 15u) {  // (and no NaN)
-                        kind = LQ_EVEN;
+                        kind = LQ_EVEN | most << LQ_TOP;
                         const uint32_t f = most << 23;
                         st_shared_v4(factors, make_uint4(f, f, f, f));
                         uint32_t r[8];
@@ -2186,10 +2204,14 @@ static csa_status check_window(int32_t B, int32_t H, int64_t total_q, int64_t ma
     return CSA_OK;
 }
 
-static void set_scale(LatArgs& a, float scale) {
+static void set_scale(LatArgs& a, float scale, bool quant = false) {
     a.sl2 = (scale < 0.f ? -scale : scale) * LP_LOG2E;
     // every weight 1 (whatever the logits: at most 3.4e38 times the least number above 0), and a masked logit still -inf
     if (a.sl2 == 0.f) a.sl2 = std::numeric_limits<float>::denorm_min();
+    if (quant && std::isfinite(a.sl2)) {
+        a.sl2 = 2.f * std::frexp(a.sl2, &a.sl2_power);
+        --a.sl2_power;
+    }
     a.negate = scale < 0.f ? 1u << 13 : 0u;
 }
 
@@ -2404,7 +2426,7 @@ static csa_status window_attn(bool quant, const void* q, int32_t H, float scale,
     a.status = device_status_ptr();
     if (!a.status) return CSA_ERR_CUDA;
     a.H = H;
-    set_scale(a, scale);
+    set_scale(a, scale, quant);
     a.kv = cache_of(kv_raw, page_table_stride);
     a.table_pages = page_table_stride;
     a.B = B;

@@ -80,3 +80,51 @@ def test_rows_of_next_to_nothing(m, H, q_len, n, scale):  # noqa: F811
     set_scales(c, 0, torch.where(torch.arange(n, device="cuda") % 97 == 5, 118, scale))
     out, lse = attention(m, c, q, [q_len], [n])
     check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in {0, q_len // 2, q_len - 1}])
+
+
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+@pytest.mark.parametrize("size,scale", [(100, 190), (126, 240), (30, 246), (60, 220), (126, 127)])
+def test_large_queries_that_large_rows_do_not_meet(m, H, q_len, n, size, scale):  # noqa: F811
+    """Queries in the first 128 dims, rows in the others: every logit is 0, whatever the sizes."""
+    g = gen(size)
+    c = Cache(g, [n], 64)
+    q = (randn(g, q_len, H, D).double().clamp(-1.5, 1.5) * power(torch.tensor(size, device="cuda"))).to(torch.bfloat16)
+    q[..., 128:] = 0
+    c.codes()[..., :128] = 0
+    c.scales()[:] = scale
+    set_scales(c, 0, torch.where(torch.arange(n, device="cuda") // 128 % 2 == 0, scale, scale - 20))
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in {0, q_len // 2, q_len - 1}])
+
+
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+@pytest.mark.parametrize("size,scale", [(-118, 248), (-110, 244), (-124, 252), (80, 30), (94, 12)])
+def test_small_queries_of_large_rows_and_the_other_way_round(m, H, q_len, n, size, scale):  # noqa: F811
+    """Logits of ordinary size from factors that are near the ends of the range.  A weight times its row's scale is kept in
+    fp16 over the largest such product so far, which counts between 2^7 and 2^15: it is off by up to half of fp16's least
+    step, 2^-25, beside what attend() counts, so by 2^-32 of the largest product at most, times the row's value over
+    its scale.  (Rows of one scale in a tile, or 2^20 apart: each is kept over its own.)"""
+    g = gen(scale)
+    c = Cache(g, [n], 64)
+    c.codes()[:] = torch.randint(0, 0x38, c.codes().shape, generator=g, device="cuda").to(torch.uint8)  # values below 1
+    c.codes()[:] += (128 * torch.randint(0, 2, c.codes().shape, generator=g, device="cuda")).to(torch.uint8)
+    c.scales()[:] = scale
+    # rows of next to nothing in every other tile: tiles in which each row keeps a scale of its own
+    js = torch.arange(n, device="cuda")
+    set_scales(c, 0, torch.where((js // 128 % 2 == 0) & (js % 3 == 0), scale - 20 if scale > 40 else scale + 20, scale))
+    q = (randn(g, q_len, H, D).double() * power(torch.tensor(size, device="cuda"))).to(torch.bfloat16)
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    for i in {0, q_len // 2, q_len - 1}:
+        kv = c.rows(0, range(n - q_len + i + 1))
+        x = SCALE * (q[i].double() @ kv.t())
+        d = float(2.0**-14 * SCALE * (q[i].double().abs() @ kv.abs().t()).amax())
+        assert 2.0**-6 < float(x.abs().max()) and d < 2.0**8  # (2^22 of scale * sum |q_i k_i| at most)
+        o, l, to, tl = attend(q[i].double(), kv)
+        page, slot = places(c, 0, kv.shape[0])
+        s = power(c.scales()[page, slot, 0].long() - 127)
+        y = (torch.exp(x - l[:, None]) * s).amax(-1)
+        to = to + 2.0**-32 * y[:, None] * (kv.abs() / s[:, None]).sum(0)
+        assert float(((out[i].double() - o).abs() - to).max()) <= 0, i
+        assert float(((lse[i].double() - l).abs() - tl).max()) <= 0, i
