@@ -1313,8 +1313,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             bool had = false;
             float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
             if (more) {
-                const float before = mine ? __ldcg(a.part_lse + prow) : -INFINITY, top = fmaxf(e, before);
+                const float before = mine ? __ldcg(a.part_lse + prow) : -INFINITY;
                 had = before != -INFINITY;
+                if (before != before) e = before;  // (fmaxf would leave a NaN out)
+                const float top = fmaxf(e, before);
                 if (top > -INFINITY) {
                     const float w0 = had ? lat_ex2((before - top) * LP_LOG2E) : 0.f;
                     const float w1 = e == -INFINITY ? 0.f : lat_ex2((e - top) * LP_LOG2E);

@@ -128,3 +128,25 @@ def test_small_queries_of_large_rows_and_the_other_way_round(m, H, q_len, n, siz
         to = to + 2.0**-32 * y[:, None] * (kv.abs() / s[:, None]).sum(0)
         assert float(((out[i].double() - o).abs() - to).max()) <= 0, i
         assert float(((lse[i].double() - l).abs() - tl).max()) <= 0, i
+
+
+def test_nan_before_logits_of_minus_infinity(m):  # noqa: F811
+    """A NaN in the first of the pieces that many rows are worked off in, and logits of -infinity in all of the last one."""
+    g = gen(32)
+    n, q_len, H, piece = 530000, 305, 128, 4096 * 128
+    c = Cache(g, [n], 64, fill=False)
+    c.codes()[:] = torch.randint(0, 0x38, c.codes().shape, generator=g, device="cuda", dtype=torch.uint8)
+    c.scales()[:] = 127
+    js = torch.arange(piece, n, device="cuda")
+    page = c.table[0].long()[js // 64]
+    c.codes()[page, js % 64, 0] = 0x7E                   # 448 * 2^127 is an infinity
+    c.scales()[page, js % 64, 0] = 254
+    c.codes()[page, js % 64, 1:128] = 0
+    q = randn(g, q_len, H, D)
+    q[..., 0] = -1
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    assert bool(torch.isfinite(lse).all()) and bool(torch.isnan(out[..., 0]).all()) and bool(torch.isfinite(out[..., 1:]).all())
+    c.scales()[c.table[0, 9], 3, 1] = 255
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert bool(torch.isnan(lse).all()) and bool(torch.isnan(out).all())
