@@ -104,6 +104,7 @@ def lib() -> ctypes.CDLL:
         L.csa_version.restype = i32
         L.csa_selftest_bounded_wait.argtypes = [vp]
         L.csa_selftest_pairs.argtypes = [i32]
+        L.csa_selftest_quant_merge.argtypes = [vp, sz, i32, vp, vp, vp]
         L.csa_copy_batch.argtypes = [i32, ctypes.POINTER(csa_copy), vp]
         L.csa_prefix_attn.argtypes = [vp, i32, i32, f32, csa_paged, i64, i64, vp, i64, vp, vp, vp, sz, vp]
         L.csa_prefix_attn_workspace_size.argtypes = [i32, i32, i64, i64]
@@ -139,7 +140,8 @@ def lib() -> ctypes.CDLL:
                      "csa_topk_cluster", "csa_topk_merge", "csa_sparse_attn_partial", "csa_attn_merge", "csa_sparse_attn",
                      "csa_decode", "csa_decode_timed", "csa_decode_noalloc", "csa_read_device_status",
                      "csa_hisparse_create", "csa_hisparse_plan", "csa_hisparse_update", "csa_hisparse_collect",
-                     "csa_hisparse_apply", "csa_selftest_bounded_wait", "csa_selftest_pairs", "csa_copy_batch", "csa_prefix_attn",
+                     "csa_hisparse_apply", "csa_selftest_bounded_wait", "csa_selftest_pairs",
+                     "csa_selftest_quant_merge", "csa_copy_batch", "csa_prefix_attn",
                      "csa_window_attn", "csa_pages_alloc", "csa_pages_free", "csa_pages_fork", "csa_pages_compact",
                      "csa_pages_copy", "csa_quant_write", "csa_quant_read", "csa_quant_attn"):
             getattr(L, name).restype = i32
@@ -471,6 +473,12 @@ def csa_selftest_bounded_wait(stream=None) -> None:
 def csa_selftest_pairs(pairs: int) -> None:
     """Cap the pairs of SMs that csa_prefix_attn, csa_window_attn and csa_quant_attn run on (0: none)."""
     _check(lib().csa_selftest_pairs(pairs), "csa_selftest_pairs")
+
+
+def csa_selftest_quant_merge(workspace, ws_bytes: int, rows: int, out, lse=None, stream=None) -> None:
+    """The last kernel of csa_quant_attn alone, over a workspace of any contents."""
+    _check(lib().csa_selftest_quant_merge(_ptr(workspace), ws_bytes, rows, _ptr(out), _ptr(lse), _stream(stream)),
+           "csa_selftest_quant_merge")
 
 
 def csa_hisparse_create(B: int, table_stride: int, n_slots: int) -> int:

@@ -194,7 +194,9 @@ struct LatArgs {
 };
 
 // Of a run of a call over quantised rows: the row tile that begins in it and ends in run `last` (none: last is the run
-// itself).  Behind the last of them, row0 is the number of runs.
+// itself).  Behind the last of them, row0 is the number of runs.  A pair writes all of its runs before its first wait, so
+// that after a wait that ran out none of them is what the workspace held; and the merge takes nothing from the list
+// that would lead it out of the rows or of the partial results.
 struct QuantRun {
     int row0, nrows, last;
 };
@@ -478,6 +480,8 @@ __device__ __forceinline__ bool quant_item(const LatArgs& a, QuantCursor& c, int
             c.c0 = -32;
             c.base = c.sum = 0;
             if (report && pair == 0 && lane == 0) a.runs[QR].row0 = (int)((c.total + c.cut - 1) / c.cut);
+            for (int r = pair + lane * pairs; report && r < QR; r += 32 * pairs) a.runs[r] = {0, 0, r};
+            __syncwarp();
         }
         c.pos = c.end = 0;
         c.run = pair - pairs;
@@ -489,7 +493,6 @@ __device__ __forceinline__ bool quant_item(const LatArgs& a, QuantCursor& c, int
                 c.pos = c.run * c.cut;
                 c.end = min(c.pos + c.cut, c.total);
                 if (c.pos >= c.total) return false;
-                if (report && lane == 0) a.runs[c.run] = {0, 0, c.run};
             } else {
                 c.pos = c.run;
                 c.end = c.pos + 1;
@@ -2086,7 +2089,7 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 3 * (QR + 1)) listed[threadIdx.x] = __ldcg(reinterpret_cast<const int*>(a.runs) + threadIdx.x);
     __syncthreads();
-    const int runs = listed[3 * QR];
+    const int runs = (uint32_t)listed[3 * QR] <= QR ? listed[3 * QR] : 0;
     // runs 3 lane .. 3 lane + 2: the rows of the row tile that begins in each, added up
     static_assert(QR <= 96, "a warp holds all runs");
     QuantRun run[3];
@@ -2096,7 +2099,9 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
         const int r = 3 * lane + k;
         run[k] = {0, 0, 0};
         if (r < runs) run[k] = {listed[3 * r], listed[3 * r + 1], listed[3 * r + 2]};
-        rows[k] = run[k].last > r ? run[k].nrows : 0;
+        const bool fine = run[k].last > r && run[k].last < runs && run[k].nrows > 0 && run[k].nrows <= a.slot_rows &&
+                          run[k].row0 >= 0 && run[k].row0 <= a.rows - run[k].nrows;
+        rows[k] = fine ? run[k].nrows : 0;
         before += rows[k];
     }
     for (int o = 1; o < 32; o <<= 1) {
@@ -2337,17 +2342,22 @@ static size_t quant_bytes(const LatArgs& a) {
            align_up(rows * sizeof(float), 256);
 }
 
+// The places of the workspace: the list of runs, then the partial results.
+static void quant_places(LatArgs& a, void* ws) {
+    uint8_t* base = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
+    a.runs = reinterpret_cast<QuantRun*>(base);
+    base += align_up((QR + 1) * sizeof(QuantRun), 256);
+    a.part_o = reinterpret_cast<float*>(base);
+    a.part_lse = reinterpret_cast<float*>(base + align_up((size_t)a.parts * a.slot_rows * D * sizeof(float), 256));
+}
+
 // Pairs in a grid at most, as a device of fewer SMs has them (csa_selftest_pairs); 0: as many as the device has.
 static std::atomic<int> g_pairs_most{0};
 
 static cudaError_t launch_pair(LatArgs& a, const void* q, const csa_paged& kv, int64_t items, void* ws, cudaStream_t s,
                                bool quant = false) {
-    if (quant && a.parts > 0) {
-        uint8_t* base = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
-        a.runs = reinterpret_cast<QuantRun*>(base);
-        base += align_up((QR + 1) * sizeof(QuantRun), 256);
-        a.part_o = reinterpret_cast<float*>(base);
-        a.part_lse = reinterpret_cast<float*>(base + align_up((size_t)a.parts * a.slot_rows * D * sizeof(float), 256));
+    if (quant) {
+        if (a.parts > 0) quant_places(a, ws);
     } else if (a.parts > 1) {
         uint8_t* base = reinterpret_cast<uint8_t*>(align_up(reinterpret_cast<uintptr_t>(ws), 256));
         a.part_o = reinterpret_cast<float*>(base);
@@ -2455,6 +2465,20 @@ csa_status csa_selftest_pairs(int32_t pairs) {
     if (pairs < 0) return CSA_ERR_INVALID_ARG;
     g_pairs_most.store(pairs, std::memory_order_relaxed);
     return CSA_OK;
+}
+
+csa_status csa_selftest_quant_merge(const void* workspace, size_t ws_bytes, int32_t rows, void* out, float* lse,
+                                    void* stream) {
+    LatArgs a = {};
+    if (rows < 1 || !workspace || !al16(workspace) || !out || !al16(out) || (lse && !al4(lse))) return CSA_ERR_INVALID_ARG;
+    a.rows = rows;
+    a.slot_rows = std::min(128, rows);
+    a.parts = 3 * QR;
+    if (ws_bytes < quant_bytes(a)) return CSA_ERR_WORKSPACE;
+    quant_places(a, const_cast<void*>(workspace));
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    return from_cuda(launch_after(quant_merge_kernel, dim3(QM_CTAS), 256, 0, static_cast<cudaStream_t>(stream), a));
 }
 
 size_t csa_prefix_attn_workspace_size(int32_t B, int32_t H, int64_t n_shared, int64_t max_rows) {

@@ -596,6 +596,15 @@ csa_status csa_selftest_bounded_wait(void* stream);
 csa_status csa_selftest_pairs(int32_t pairs);
 
 /*
+ * Merge self-test: the last kernel of a csa_quant_attn call alone, over a workspace of any contents, as a call whose waits
+ * ran out may leave it.  out bf16 [rows, 512] (16-byte aligned), lse fp32 [rows] (nullable): nothing outside them is written
+ * and nothing outside the workspace (16-byte aligned, csa_quant_attn_workspace_size(1, 1, rows, rows, 1, 0) bytes, or that of
+ * 128 rows where there are more) is read, whatever it holds.  rows < 1 or bad pointers: CSA_ERR_INVALID_ARG.
+ */
+csa_status csa_selftest_quant_merge(const void* workspace, size_t ws_bytes, int32_t rows, void* out, float* lse,
+                                    void* stream);
+
+/*
  * HiSparse coordinator ([V4-deploy] "HiSparse": a coordinator swaps pages every step and evicts
  * by LRU; [Day-0] "创新 3": a GPU miss is swapped in from the CPU mirror).  A host object holding
  * the working set's bookkeeping: which (request, logical page) each slot holds and the last step

@@ -1,6 +1,7 @@
 """The quantised latent cache at the ends of its ranges: scales far apart, rows of nothing, queries and rows of any size,
 codes that are no numbers, many short items, and the merge over a list of any contents."""
 import math
+import random
 
 import pytest
 
@@ -150,3 +151,61 @@ def test_nan_before_logits_of_minus_infinity(m):  # noqa: F811
     c.scales()[c.table[0, 9], 3, 1] = 255
     out, lse = attention(m, c, q, [q_len], [n])
     assert bool(torch.isnan(lse).all()) and bool(torch.isnan(out).all())
+
+
+@pytest.mark.parametrize("rows", [1, 40, 5000])
+def test_merge_over_any_list(m, rows):  # noqa: F811
+    """The merge's list of runs as a call whose waits ran out may leave it: what an earlier call or nobody wrote.  It merges
+    what names rows and partial results that there are, and writes nowhere else."""
+    slots, QR = min(128, rows), 76
+    need = m.csa_quant_attn_workspace_size(1, 1, slots, slots, 1, 0)
+    r = random.Random(rows)
+    big = [-1, 0, 1, QR, QR + 1, 127, 128, 129, rows - 1, rows, rows + 1, 1 << 20, (1 << 31) - 1, -(1 << 31), 0x7F7F7F7F]
+    for turn in range(40):
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+        at = (-ws.data_ptr()) % 256
+        lst = []
+        for k in range(QR + 1):
+            if r.random() < 0.5:  # one that may be right
+                n = r.randint(0, slots)
+                lst.append([r.randint(0, rows - n), n, min(QR - 1, k + r.randint(0, 3))])
+            else:
+                lst.append([r.choice(big), r.choice(big), r.choice(big)])
+        lst[QR][0] = r.choice([QR, QR, QR, 5, *big])
+        ws[at: at + 12 * (QR + 1)] = torch.tensor(lst, dtype=torch.int32).view(torch.uint8).view(-1).cuda()
+        if turn == 0:  # all bits set
+            ws.fill_(255)
+            lst = [[-1, -1, -1]] * (QR + 1)
+        guard = 300
+        buf = torch.full((rows + 2 * guard, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((rows + 2 * guard,), 7.0, device="cuda")
+        m.csa_selftest_quant_merge(ws[at:], need, rows, buf[guard: guard + rows], lse[guard: guard + rows])
+        assert m.csa_read_device_status() == 0
+        runs = lst[QR][0] if 0 <= lst[QR][0] <= QR else 0
+        named = torch.zeros(rows + 2 * guard, dtype=torch.bool, device="cuda")
+        for k, (row0, n, last) in enumerate(lst[:runs]):
+            if k < last < runs and 0 < n <= slots and 0 <= row0 <= rows - n:
+                named[guard + row0: guard + row0 + n] = True
+        assert turn == 0 or runs < 20 or bool(named.any())
+        assert bool((buf[~named] == 7).all()) and bool((lse[~named] == 7).all())
+        assert not bool((lse[named] == 7).any())
+
+
+def test_unwritten_runs_are_empty(m, capped):  # noqa: F811
+    """The list of runs in the workspace of a call with few row tiles: whatever it held, every run is named in it, those without
+    a row tile that is cut as empty."""
+    g = gen(33)
+    n, QR = [3000, 40], 76
+    c = Cache(g, n, 64)
+    q = randn(g, 2, 16, D)
+    need = m.csa_quant_attn_workspace_size(2, 16, 2, 1, ALL, 0)
+    for pairs in (0, 1, 13):
+        capped(pairs)
+        ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+        at = (-ws.data_ptr()) % 256
+        attention(m, c, q, [1, 1], n, workspace=ws[at:], ws_bytes=need)
+        lst = ws[at: at + 12 * (QR + 1)].clone().view(torch.int32).view(-1, 3).tolist()
+        # 24 + 3 places and 1 + 3, two to a run
+        assert lst[QR][0] == 16
+        assert lst[0] == [0, 16, 11] and all(lst[k] == [0, 0, k] for k in range(1, QR))
+    assert m.csa_read_device_status() == 0

@@ -69,3 +69,15 @@ def test_attn_refusals(csa):
     for kw in ({"ws": None}, {"ws": A8}, {"ws_bytes": 16}):
         assert go(B=1, total=1, max_q=1, window=1 << 30, sink=0, stride=5000, **kw) == csa.CSA_ERR_WORKSPACE, kw
     assert csa.csa_quant_attn_workspace_size(0, 16, 1, 1, 128, 0) == 0
+
+
+def test_merge_selftest_refusals(csa):
+    f = csa.lib().csa_selftest_quant_merge
+    need = csa.csa_quant_attn_workspace_size(1, 1, 40, 40, 1, 0)
+
+    def go(ws=A16, ws_bytes=need, rows=40, out=A16, lse=A4):
+        return f(ws, ws_bytes, rows, out, lse, None)
+
+    for kw in ({"ws": None}, {"ws": A8}, {"rows": 0}, {"rows": -1}, {"out": None}, {"out": A8}, {"lse": A2}):
+        assert go(**kw) == csa.CSA_ERR_INVALID_ARG, kw
+    assert go(ws_bytes=need - 1) == csa.CSA_ERR_WORKSPACE and go(rows=41) == csa.CSA_ERR_WORKSPACE
