@@ -1871,8 +1871,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         const int r = tid - 32 * (LP_SOFT + 2 + lat_loaders(KEYS));
         while (next_item()) {
             if (x.T == 0) continue;
-            ok = lat_wait<QUANT>(sb + LP_QFULL, n & 1, dead) && ok;  // (of the first item too: a wait is for one phase)
+            // The first item's queries are the softmax warps'.  A wait tells a phase from the one before it only: the first
+            // wait is over once the item before's queries came and were used (which no later item's can be before these
+            // are turned into fp16 here), the second once this one's are there.
             if (n > 0) {
+                ok = lat_wait<QUANT>(sb + LP_QEMPTY, (n - 1) & 1, dead) && ok;
+                ok = lat_wait<QUANT>(sb + LP_QFULL, n & 1, dead) && ok;
                 if ((int)rank * 64 + r < x.nrows) lat_q_row(sb, sb + LP_SM_QTOP + (n & 1) * 64 + r, r);
                 fence_proxy_async_smem();
                 __syncwarp();

@@ -209,3 +209,23 @@ def test_unwritten_runs_are_empty(m, capped):  # noqa: F811
         assert lst[QR][0] == 16
         assert lst[0] == [0, 16, 11] and all(lst[k] == [0, 0, k] for k in range(1, QR))
     assert m.csa_read_device_status() == 0
+
+
+@pytest.mark.parametrize("B,pairs", [(200, 1), (200, 3), (280, 1), (280, 0)])
+def test_many_short_items(m, capped, B, pairs):  # noqa: F811
+    """Row tiles of a key tile or two, or of none, one behind the other: the next items' queries come while an item is worked
+    on.  The same bits every time."""
+    g = gen(34)
+    H = 128
+    lens = [(1, 1, 2, 0, 1)[i % 5] for i in range(B)]
+    n = [(1, 130, 17, 9, 0, 128, 3)[i % 7] for i in range(B)]
+    c = Cache(g, n, 64)
+    q = randn(g, sum(lens), H, D)
+    capped(pairs)
+    out, lse = attention(m, c, q, lens, n)
+    assert m.csa_read_device_status() == 0
+    check_tokens(c, q, out, lse, lens, n, ALL, 0, [(b, i) for b in (*range(0, 14), *range(B - 7, B)) for i in range(lens[b])])
+    for _ in range(100):
+        got = attention(m, c, q, lens, n)
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    assert m.csa_read_device_status() == 0
