@@ -749,6 +749,8 @@ __device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part,
                 uint4 none;
                 q_values(make_uint4(w.x, w.y, 0, 0), q_factor(s), v[e], none);
                 q_times(v[e], q_factor_rest(s));
+                const uint2 x = e4m3x4_nan(w.x), y = e4m3x4_nan(w.y);
+                v[e].x |= x.x, v[e].y |= x.y, v[e].z |= y.x, v[e].w |= y.y;
             } else {
                 v[e] = __ldg(reinterpret_cast<const uint4*>(a.kv.base + (int64_t)pg * a.kv.page_stride +
                                                             (int64_t)slot * ROW_BYTES + at * 2) + c);

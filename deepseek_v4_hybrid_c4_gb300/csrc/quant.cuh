@@ -32,11 +32,19 @@ CSA_DEV uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 // Four e4m3 codes with their bits at their places in a bf16: sign, four bits of exponent, three of fraction.  As a
 // bf16 that is the code's value times 2^-120, subnormals among them (both formats count those from their least
-// exponent), so that one multiplication by a power of two is exact.  The codes 0x7F and 0xFF, which a quantised row does not have,
-// become +-480 and no NaN: looking for them would be a third of the work on top.
+// exponent), so that one multiplication by a power of two is exact.  The codes 0x7F and 0xFF, which csa_quant_write does not
+// make, become +-480 and no NaN here, where rows are read back: looking for them would be a third of the work on top.
+// (cvt.rn.f16x2.e4m3x2, by which attention converts, has NaN for them.)
 CSA_DEV uint2 e4m3x4_bits(uint32_t w) {
     const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
     return make_uint2((lo & 0x80008000u) | ((lo >> 4) & 0x07F007F0u), (hi & 0x80008000u) | ((hi >> 4) & 0x07F007F0u));
+}
+
+// 0x7F80 at the places of those bf16 whose codes are 0x7F or 0xFF.
+CSA_DEV uint2 e4m3x4_nan(uint32_t w) {
+    const uint32_t n = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    const uint32_t lo = __byte_perm(n, 0, 0x1404), hi = __byte_perm(n, 0, 0x3424);
+    return make_uint2(lo - (lo >> 8), hi - (hi >> 8));
 }
 
 // 16 codes as 16 bf16 (two uint4).

@@ -315,8 +315,9 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
  * csa_paged a row counts 516 bytes: page_stride_bytes >= rows_per_page * 516 and a multiple of 16; slot s of a page has its
  * codes at s * 512 and its scales at rows_per_page * 512 + s * 4.  Such a pool is one of a csa_page_pools like any other.
  * page_table [B, page_table_stride] is required; n_pages < 2^31 and n_pages * page_stride_bytes <= 64 GiB (else
- * CSA_ERR_UNSUPPORTED).  The e4m3 codes 0x7F and 0xFF
- * (NaN) do not occur in a row that csa_quant_write made; in any other they count as 480 and -480.
+ * CSA_ERR_UNSUPPORTED).  The e4m3 codes 0x7F and 0xFF, which are no numbers, do not occur in a row that csa_quant_write
+ * made.  In any other csa_quant_attn takes them as NaN, and csa_quant_read, which does not tell them from the codes below them,
+ * gives 480 and -480 times the scale.
  *
  * The three calls take a ragged batch the same way: B sequences, sequence b with offsets[b+1] - offsets[b] rows of the
  * batch's buffers (device int64 [B+1], non-decreasing), which are the last of its n_tokens[b] tokens (device int64 [B]).

@@ -131,6 +131,32 @@ def test_small_queries_of_large_rows_and_the_other_way_round(m, H, q_len, n, siz
         assert float(((lse[i].double() - l).abs() - tl).max()) <= 0, i
 
 
+def test_codes_that_are_no_numbers(m):  # noqa: F811
+    """The codes 0x7F and 0xFF are NaN in attention: those who see one get NaN, nobody else does."""
+    g = gen(31)
+    lens, n, W = [390, 2], [400, 300], 100
+    c = Cache(g, n, 64)
+    for b, j, d, code in ((0, 40, 5, 0x7F), (0, 250, 500, 0xFF), (1, 100, 300, 0x7F)):
+        c.codes()[c.table[b, j // 64], j % 64, d] = code
+    bad = {0: {40, 250}, 1: {100}}
+    q = randn(g, sum(lens), 16, D)
+    out, lse = attention(m, c, q, lens, n, W, 3)
+    assert m.csa_read_device_status() == 0
+    nan = 0
+    for b, i in [(0, i) for i in range(0, 390, 13)] + [(0, 30), (0, 29), (0, 129), (0, 130), (1, 0), (1, 1)]:
+        p, t = n[b] - lens[b] + i, (0, 390)[b] + i
+        js = keys(p, W, 3)
+        kv = c.rows(b, js)
+        for k, j in enumerate(js):
+            if j in bad[b]:
+                kv[k, 0] = math.nan
+        nan += not bool(torch.isfinite(kv).all())
+        check_formula(out[t], lse[t], q[t].double(), kv, (b, i))
+    assert nan >= 8
+    out, lse = attention(m, c, q, [0, 2], n)             # without a window
+    assert bool(torch.isnan(out[:2]).all()) and bool(torch.isnan(lse[:2]).all())
+
+
 def test_nan_before_logits_of_minus_infinity(m):  # noqa: F811
     """A NaN in the first of the pieces that many rows are worked off in, and logits of -infinity in all of the last one."""
     g = gen(32)
@@ -229,3 +255,30 @@ def test_many_short_items(m, capped, B, pairs):  # noqa: F811
         got = attention(m, c, q, lens, n)
         assert torch.equal(got[0], out) and torch.equal(got[1], lse)
     assert m.csa_read_device_status() == 0
+
+
+def test_codes_that_are_no_numbers_beside_infinite_rows(m):  # noqa: F811
+    """A query with a logit of -infinity has NaN where the rows that it sees are not finite, whole where one of its own logits is
+    NaN: the same for a code of NaN in a run of its own."""
+    g = gen(35)
+    n, H = 3000, 16
+    c = Cache(g, [n], 64)
+    c.codes()[:] = c.codes() % 128 % 0x38 + c.codes() // 128 * 128  # values below 1
+    c.scales()[:] = 127
+    page, slot = places(c, 0, n)
+    c.codes()[page[5], slot[5], :128] = 0
+    c.codes()[page[5], slot[5], 3] = 0x7E
+    c.scales()[page[5], slot[5], 0] = 254                # an infinity in dim 3 of row 5
+    c.codes()[page[2900], slot[2900], 400] = 0xFF
+    q = randn(g, 120, H, D)
+    q[..., 3] = -1
+    out, lse = attention(m, c, q, [120], [n])
+    assert m.csa_read_device_status() == 0
+    for i in (0, 19, 20, 21, 119):                       # row 2900 is the 21st token's own
+        kv = c.rows(0, range(n - 120 + i + 1))
+        if i >= 20:
+            kv[2900, 400] = math.nan
+        nan = torch.isnan(torch.softmax(SCALE * (q[i].double() @ kv.t()), -1) @ kv)
+        assert torch.equal(torch.isnan(out[i]), nan), i
+        assert bool(torch.isnan(lse[i]).all()) == (i >= 20)
+    assert bool(torch.isfinite(out[:20, :, 4:]).all()) and bool(torch.isnan(out[:, :, 3]).all())
