@@ -1169,7 +1169,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         m_run = mt;
                     }
                     if (!QUANT) alpha = alpha_l;
-                } else if (plain) {  // every logit is -inf or NaN
+                } else if (plain && some) {  // every logit is -inf or NaN
                     lost[r] = lost[64] = q;
                 }
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
