@@ -1073,7 +1073,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         const int e = qe + top;  // (biased by 127)
                         tpow = (float)(top - 127);
                         tsl2 = a.sl2 * __uint_as_float((uint32_t)e << 23);
-                        if (LAT_RARE((uint32_t)(e - 1) >= 254u)) tsl2 = lat_unit(a.sl2, e - 127);
+                        if (LAT_RARE(__any_sync(0xffffffffu, (uint32_t)(e - 1) >= 254u))) tsl2 = lat_unit(a.sl2, e - 127);
                     } else if (LAT_RARE(some)) {
                         // the logits themselves, in log2 units: times what makes them small before the rows' scales, times
                         // what makes them large behind them
