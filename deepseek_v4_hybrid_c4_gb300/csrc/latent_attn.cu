@@ -690,6 +690,7 @@ __device__ __forceinline__ int quad_map(QuadRuns n, int q, int q0, bool two) {
 template <bool QUANT>
 __device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part, int64_t prow, bool direct, int at,
                                             float l_run, bool go) {
+    if (!QUANT) direct = a.parts == 1, prow = (int64_t)part * a.rows + row;
     const int64_t to = (direct ? (int64_t)row : prow) * D + at;
     auto put = [&](int d) {
         if (direct) a.out[to + d] = 0x7FFFu;
@@ -1313,10 +1314,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             const bool direct = QUANT ? (x.shared & QUANT_DIRECT) != 0 : a.parts == 1;
             const bool more = QUANT && (x.shared & QUANT_MORE) != 0;
             // this row of the partial results
-            const int64_t prow = QUANT ? (int64_t)x.part * a.slot_rows + (int)rank * 64 + r
-                                                  : (int64_t)x.part * a.rows + row;
+            const int64_t prow = QUANT ? (int64_t)x.part * a.slot_rows + (int)rank * 64 + r : 0;
             bool had = false;
-            float e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
+            float e = 0.f;  // (bf16 rows: of the threads that store it; with that and a place of the partial results in every
+                            // thread a prompt of 8K tokens took 1 percent more)
+            if (QUANT || (tid < 64 && mine)) e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
             if (more) {
                 const float before = mine ? __ldcg(a.part_lse + prow) : -INFINITY;
                 had = before != -INFINITY;
@@ -1334,7 +1336,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 named_bar_sync(1, 32 * LP_SOFT);  // (a row's threads have all read what one of them replaces)
             }
             if (tid < 64 && mine) {
-                if (!direct) a.part_lse[prow] = e;
+                if (!direct) a.part_lse[QUANT ? prow : (int64_t)x.part * a.rows + row] = e;
                 else if (a.lse) a.lse[row] = e;
             }
             // ---- row r of the CTA, dims [256 half + 128 ch, + 128), normalised.  Four lanes exchange their rows'
@@ -1345,7 +1347,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 const int64_t gr = row - j;  // the group's first row
                 const int left = x.nrows - ((int)rank * 64 + r - j);
                 uint8_t* dst = (direct ? reinterpret_cast<uint8_t*>(a.out + gr * D + at)
-                                       : reinterpret_cast<uint8_t*>(a.part_o + (prow - j) * D + at)) +
+                                       : reinterpret_cast<uint8_t*>(
+                                             a.part_o + (QUANT ? prow - j : (int64_t)x.part * a.rows + gr) * D + at)) +
                                j * 32;
                 const float* was = a.part_o + prow * D + at;  // (more)
                 const int64_t pitch = direct ? D * 2 : D * 4;
@@ -1420,7 +1423,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 tc_fence_before();
                 if (QUANT ? LAT_RARE(lost[64] == q) : lost[64] == q) {
                     __syncwarp();  // (behind the other lanes' stores to this lane's row)
-                    lat_not_finite<QUANT>(a, row, x.part, prow, direct, half * 256 + ch * 128, l_run,
+                    lat_not_finite<QUANT>(a, row, x.part, QUANT ? prow : 0, direct, half * 256 + ch * 128, l_run,
                                                      mine && lost[r] == q);
                 }
             }
