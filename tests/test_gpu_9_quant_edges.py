@@ -5,10 +5,10 @@ import random
 
 import pytest
 
-from test_gpu_5_operators import D, SCALE, attend, gen, m, randn  # noqa: F401
+from test_gpu_5_operators import BOUNDS, D, SCALE, attend, gen, m, randn  # noqa: F401
 from test_gpu_6_operator_edges import capped  # noqa: F401
 from test_gpu_7_operator_draws import check_formula
-from test_gpu_8_quant import ALL, Cache, attention, check_tokens, keys, power, values
+from test_gpu_8_quant import ALL, Cache, attention, check_tokens, keys, page_bytes, power, quantised, values
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -282,3 +282,33 @@ def test_codes_that_are_no_numbers_beside_infinite_rows(m):  # noqa: F811
         assert torch.equal(torch.isnan(out[i]), nan), i
         assert bool(torch.isnan(lse[i]).all()) == (i >= 20)
     assert bool(torch.isfinite(out[:20, :, 4:]).all()) and bool(torch.isnan(out[:, :, 3]).all())
+
+
+@pytest.mark.parametrize("B", [257, 5000, 65535])
+def test_batches_of_very_many_sequences(m, B):  # noqa: F811
+    """A row of each sequence, and batches that have next to no rows; whichever sequence is outside is reported."""
+    g = gen(B)
+    pool = torch.zeros(B, page_bytes(1), dtype=torch.uint8, device="cuda")
+    table = torch.randperm(B, generator=g, device="cuda").to(torch.int32).view(B, 1)
+    kv = m.paged(pool, 1, 516, table, page_stride_bytes=pool.shape[1], n_pages=B)
+    x = randn(g, B, D)
+    at, n = torch.arange(B + 1, device="cuda"), torch.ones(B, dtype=torch.int64, device="cuda")
+    m.csa_quant_write(x, kv, 1, B, at, n, B, 1)
+    out = torch.full((B, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    m.csa_quant_read(kv, 1, B, at, n, B, 1, out)
+    assert m.csa_read_device_status() == 0
+    assert torch.equal(out.double(), values(*quantised(x)))
+    # one row, the last sequence's; then a sequence without rows that is too long
+    at = torch.zeros(B + 1, dtype=torch.int64, device="cuda")
+    at[B] = 1
+    out.fill_(7.0)
+    m.csa_quant_read(kv, 1, B, at, n, 1, 1, out)
+    assert m.csa_read_device_status() == 0
+    assert torch.equal(out[0].double(), values(*quantised(x[-1:]))[0]) and bool((out[1:] == 7).all())
+    for b in (0, 31, 32, 255, 256, B // 2, B - 2):
+        n[b] = 1 << 31
+        m.csa_quant_read(kv, 1, B, at, n, 1, 1, out)
+        assert m.csa_read_device_status() == BOUNDS, b
+        m.csa_quant_write(x, kv, 1, B, at, n, 1, 1)
+        assert m.csa_read_device_status() == BOUNDS, b
+        n[b] = 1
