@@ -2091,6 +2091,8 @@ __global__ void __launch_bounds__(128, IN > 8 ? 4 : 8) lat_merge_kernel(LatArgs 
 // columns 4 l + 128 k.
 constexpr int QM_IN = 4;                         // partial rows in flight
 constexpr int QM_CTAS = 2 * 2 * LP_PAIRS;
+constexpr float QM_MOST = 128.f;                 // more than a row has partial results; a power of two: the same bits
+static_assert(QR < QM_MOST, "partial results of a row");
 __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
     // (each CTA reads the runs once: warps that all read them for themselves took 24 us and more at the few L2 lines they are in)
     __shared__ int listed[3 * (QR + 1)];
@@ -2162,7 +2164,7 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
 #pragma unroll
             for (int s = 0; s < QM_IN; ++s) {
                 if (v[s] == -INFINITY) continue;  // (no keys that its rows see)
-                const float w = lat_ex2((v[s] - M) * LP_LOG2E);
+                const float w = lat_ex2((v[s] - M) * LP_LOG2E) * (1.f / QM_MOST);  // (sums of large values stay finite)
                 L += w;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -2180,7 +2182,7 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
             reinterpret_cast<uint2*>(a.out + (int64_t)row * D)[lane + 32 * c] =
                 make_uint2(pack_bf16x2(o[4 * c] * inv, o[4 * c + 1] * inv), pack_bf16x2(o[4 * c + 2] * inv, o[4 * c + 3] * inv));
         if (lane == 0 && a.lse)
-            a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f || lost ? -INFINITY : M + log2f(L) * LP_LN2);
+            a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f || lost ? -INFINITY : M + log2f(L * QM_MOST) * LP_LN2);
     }
 }
 

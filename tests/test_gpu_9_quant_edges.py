@@ -312,3 +312,83 @@ def test_batches_of_very_many_sequences(m, B):  # noqa: F811
         m.csa_quant_write(x, kv, 1, B, at, n, 1, 1)
         assert m.csa_read_device_status() == BOUNDS, b
         n[b] = 1
+
+
+def test_values_next_to_the_largest_number(m):  # noqa: F811
+    """Means of values of 1.75 * 2^127 in every partial result: their sum would be none."""
+    for H, q_len, n in FORMS:
+        c = Cache(gen(36), [n], 64)
+        c.codes()[:] = 0x7E                              # 448
+        c.codes()[..., ::2] = 0xFE
+        c.scales()[:] = 127 + 119
+        q = torch.zeros(q_len, H, D, dtype=torch.bfloat16, device="cuda")
+        out, lse = attention(m, c, q, [q_len], [n])
+        assert m.csa_read_device_status() == 0
+        v = 1.75 * 2.0**127
+        assert bool(((out[..., 1::2].double() - v).abs() <= 2.0**-7 * v).all())  # (2^-8 of the values, 2^-8 of the rounding)
+        assert bool(((out[..., ::2].double() + v).abs() <= 2.0**-7 * v).all())
+        check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, q_len - 1)])
+
+
+def check_any_scales(c, b, q, out, lse, n, where):
+    """Rows of any finite scales.  Beside what attend() counts: a row's values are known to 2^-25 of its unit (half of fp16's least
+    step), the power of two of its tile's largest scale or, where the tile's rows are more than 2^15 apart, of its own
+    largest; a query's to 2^-39 of its largest; and a weight times its unit to 2^-32 of the largest such product
+    (test_small_queries_of_large_rows_and_the_other_way_round).  A logit's error moves a weight by twice that."""
+    js = torch.arange(n, device="cuda")
+    page = c.table[b].long()[js // c.rpp]
+    top = c.scales()[page, js % c.rpp].amax(-1).long()
+    unit = top.clone()
+    for t in range(0, n, 128):
+        rows = top[t: t + 128]
+        some = rows[rows > 10]
+        if len(some) and int(rows.max() - some.min()) <= 15:
+            unit[t: t + 128] = rows.max()
+    unit = power(unit - 127)
+    kv = c.rows(b, range(n))
+    x = SCALE * (q @ kv.t())
+    full = torch.logsumexp(x, -1)
+    w = torch.exp(x - full[:, None])
+    o, a = w @ kv, w @ kv.abs()
+    d = 2.0**-14 * SCALE * (q.abs() @ kv.abs().t()).amax(-1)
+    if float(d.max()) > 2.0**8:
+        return False                                     # no defined result
+    d = d + SCALE * ((q.abs().sum(-1)[:, None] * 2.0**-25 * unit).amax(-1) + 2.0**-39 * q.abs().amax(-1) * kv.abs().sum(-1).amax())
+    ok = d < 0.25                                        # (e^(2 d) - 1 <= 3 d)
+    to = 2.0**-8 * (a + o.abs()) + (3 * d[:, None] + 2.0**-20) * a + 2.0**-133
+    to = to + (2.0**-25 * (w @ unit) + 2.0**-32 * (w * unit).amax(-1) * (kv.abs() / unit[:, None]).sum(0).amax())[:, None]
+    assert float(((out.double() - o).abs() - to)[ok].max() if bool(ok.any()) else -1) <= 0, where
+    assert float(((lse.double() - full).abs() - d - 2.0**-20 * (1 + full.abs())).max()) <= 0, where
+    return True
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_drawn_scales(m, seed):  # noqa: F811
+    """Scales drawn for the cache, its tiles, its rows and their blocks; queries as large as they may be for them."""
+    r, g = random.Random(seed), gen(seed)
+    H, q_len, n = r.choice(FORMS + [(24, 7, 500), (128, 320, 400), (1, 1, 130)])
+    c = Cache(g, [n], r.choice((64, 16, 17, 1)))
+    js = torch.arange(n, device="cuda")
+
+    def spread(count, most):
+        return torch.randint(-most, most + 1, (count,), generator=g, device="cuda")
+
+    s = torch.full((n, 4), r.randint(0, 246), device="cuda")
+    s += spread(n // 128 + 1, r.choice((0, 0, 3, 20, 60, 120)))[js // 128][:, None]
+    s += spread(n, r.choice((0, 0, 2, 7, 16, 40)))[:, None]
+    s += spread(4 * n, r.choice((0, 1, 4, 12))).view(n, 4)
+    s = s.clamp(0, 246)
+    set_scales(c, 0, s)
+    if r.random() < 0.3:
+        set_scales(c, 0, torch.where((js % r.choice((2, 50, 300)) == 1)[:, None], torch.full_like(s, r.choice((0, 10, 11))), s))
+    if r.random() < 0.3:
+        set_codes(c, 0, torch.where((js % r.choice((2, 50, 300)) == 0)[:, None], 0, c.codes()[places(c, 0, n)]))
+    big = float(c.rows(0, range(n)).abs().max()) or 1.0
+    size = math.floor(math.log2(2.0 ** r.choice((-20, 0, 3, 6)) / big))
+    q = (randn(g, q_len, H, D).double() * power(torch.tensor(max(-126, min(size, 126)), device="cuda"))).to(torch.bfloat16)
+    if r.random() < 0.3:
+        q[:, :, r.randrange(512):] = 0
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    for i in {0, q_len // 2, q_len - 1}:
+        check_any_scales(c, 0, q[i].double(), out[i], lse[i], n - q_len + i + 1, (seed, i))
