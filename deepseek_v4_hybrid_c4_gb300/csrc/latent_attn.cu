@@ -63,12 +63,13 @@
 // it, and O and the weights (fp16, at most 2^15) are kept over a running maximum of weight times scale, while
 // the sum of the weights has one of the weights alone.  Rows more than 2^15 apart keep scales of their own, which the
 // softmax then looks up for each.  Q becomes fp16 in shared memory, each row with a power of two of its own.
-// 20 warps: 8 loading warps, two for Q (it is ready beside the item before), and 104 registers for the softmax, 88 for the others.
-// Work is dealt out in runs of one length cut anywhere (quant_item).
-// What bounds it (a chunk of 1,024 tokens of 128 heads over 24K rows: 6.6 ms, 1.02 PFLOP/s, 4,900 cycles a tile where the products take
-// 2,056): the L1's data pipe, 80 percent of its peak with the products' operands, the rows on their way in and out of
-// registers and what is looked up, and instruction fetch (85 percent of what the cache beyond an SM's delivers).  Every row is turned into fp16 twice in a
-// pair, as a key by one CTA and as a value by the CTA that has its dims.
+// 20 warps: 8 loading warps, two for Q (it is ready beside the item before), and 104 registers for the softmax, 88 for
+// the others.  Work is dealt out in runs of one length cut anywhere (quant_item).
+// What bounds it (a chunk of 1,024 tokens of 128 heads over 24K rows: 6.6 ms, 1.02 PFLOP/s, 4,900 cycles a tile where the
+// products take 2,056): the L1's data pipe, 80 percent of its peak with the products' operands, the rows on their way in
+// and out of registers and what is looked up, and instruction fetch (85 percent of what the cache beyond an SM's
+// delivers).  Every row is turned into fp16 twice in a pair, as a key by one CTA and as a value by the CTA that has its
+// dims.
 #include <cuda.h>
 
 #include <algorithm>
@@ -119,8 +120,8 @@ static_assert(LP_SMEM <= 227 * 1024, "latent attention shared memory");
 constexpr uint32_t LP_SM_FACTOR = LP_SM_P + 2 * LP_QSLAB;  // [8 tiles][128] fp32
 constexpr uint32_t LP_SM_RATIO = LP_SM_FACTOR + 8 * 512;   // [4 tiles][128][4] fp16
 constexpr uint32_t LP_QREADY = LP_TAKEN + 32;              // Q is there as fp16 (even CTA: of both)
-constexpr uint32_t LP_QTOP = LP_QREADY + 8;                // and its rows' exponents: [2 items][64] bytes, a barrier each (the
-                                                          // queries may be one item ahead of the softmax, not two)
+constexpr uint32_t LP_QTOP = LP_QREADY + 8;                // and its rows' exponents: [2 items][64] bytes, a barrier each
+                                                           // (the queries may be one item ahead of the softmax, not two)
 constexpr uint32_t LP_SM_QTOP = LP_SM_NEXT;
 static_assert(LP_SM_RATIO + 4 * 1024 <= LP_SM_BAR && LP_QTOP + 16 <= LP_SM_BAR + 512, "places of quantised rows");
 // Of a tile: plain; one factor for all rows; values of 2^128; from bit 8 on the largest scale code of its rows.
@@ -254,7 +255,8 @@ __device__ __forceinline__ int seq_of(const LatArgs& a, int64_t tok) {
 __device__ __forceinline__ int ceil_div(int x, int y) { return (int)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y); }
 
 // Row tile `tile` of a sequence: its rows and the units that they see.
-__device__ __forceinline__ void window_item(const LatArgs& a, LatItem& x, int tile, int ql, int64_t q0, int64_t nt, int trow) {
+__device__ __forceinline__ void window_item(const LatArgs& a, LatItem& x, int tile, int ql, int64_t q0, int64_t nt,
+                                            int trow) {
     x.rr0 = tile * 128;
     x.nrows = min(128, ql * a.H - x.rr0);
     x.row0 = (int)q0 * a.H + x.rr0;
@@ -425,7 +427,8 @@ __device__ __forceinline__ bool lat_item(const LatArgs& a, SeqCursor& cur, int& 
 // with those before it in its slot), whatever the batch.
 struct QuantCursor {
     int c0 = -32, tiles = 0, ql = 0, g = 0;
-    int64_t base = 0, sum = 0, incl = 0, q0 = 0, nt = 0;  // of the 32 sequences: places before them, in them, up to the lane's
+    int64_t base = 0, sum = 0, incl = 0;  // of the 32 sequences: places before them, in them, up to the lane's
+    int64_t q0 = 0, nt = 0;
     int64_t total = 0, cut = 1, pos = -1, end = 0;
     int run = 0, left = 0, slot = 0;
     bool direct = false;
@@ -745,7 +748,8 @@ __device__ __noinline__ void lat_not_finite(const LatArgs& a, int row, int part,
             const int pg = lat_entry(a, pt, key(k), slot);
             if (pg < 0 || pg >= a.kv.n_pages) continue;
             if (QUANT) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(q_codes(a.kv.base, a.kv.page_stride, pg, slot) + at) + c);
+                const uint8_t* row = q_codes(a.kv.base, a.kv.page_stride, pg, slot);
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + at) + c);
                 const uint32_t s = __ldg(q_scales(a.kv.base, a.kv.page_stride, a.kv.rpp, pg, slot) + at / 128);
                 uint4 none;
                 q_values(make_uint4(w.x, w.y, 0, 0), q_factor(s), v[e], none);
@@ -799,6 +803,12 @@ __device__ __forceinline__ float lat_unit(float sl2, int e) {
 // The part of e of a query whose largest value has the exponent E and is now in [2^14, 2^15).
 __device__ __forceinline__ int lat_q_power(uint32_t E) { return (int)E - 141; }
 
+// The larger of top and v's magnitudes, as the bits of two bf16.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t top, const uint4& v) {
+    constexpr uint32_t m = 0x7FFF7FFFu;
+    return __vmaxu2(__vmaxu2(top, v.x & m), __vmaxu2(v.y & m, __vmaxu2(v.z & m, v.w & m)));
+}
+
 // The CTA's 64 rows of Q in place from bf16 to fp16, each with its largest value in [2^14, 2^15) (the softmax
 // warps).  Returns the row's lat_q_power().  A value 2^29 below its row's largest still has all
 // its bits, and what is lost of smaller ones is 2^-39 of the largest.
@@ -811,7 +821,7 @@ __device__ __noinline__ int lat_q_to_f16(uint32_t sb, float* shared, int tid, bo
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
             v[c] = ld_shared_v4(row + (c >> 3) * LP_QSLAB + (((c & 7) ^ (r & 7)) << 4));
-            top = __vmaxu2(__vmaxu2(top, v[c].x & 0x7FFF7FFFu), __vmaxu2(v[c].y & 0x7FFF7FFFu, __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)));
+            top = max_magnitude(top, v[c]);
         }
         if (LAT_RARE((top & 0x7FFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u)) {  // infinities and NaN do not count
             top = 0;
@@ -826,7 +836,8 @@ __device__ __noinline__ int lat_q_to_f16(uint32_t sb, float* shared, int tid, bo
     }
     shared[tid] = __uint_as_float(top);
     named_bar_sync(1, 32 * LP_SOFT);
-    top = max(max(top, __float_as_uint(shared[tid ^ 64])), max(__float_as_uint(shared[tid ^ 128]), __float_as_uint(shared[tid ^ 192])));
+    top = max(max(top, __float_as_uint(shared[tid ^ 64])),
+              max(__float_as_uint(shared[tid ^ 128]), __float_as_uint(shared[tid ^ 192])));
     const uint32_t E = max(top >> 7, 15u);
     const float f = __uint_as_float((268u - E) << 23);
     if (wanted) {
@@ -844,8 +855,8 @@ __device__ __noinline__ int lat_q_to_f16(uint32_t sb, float* shared, int tid, bo
     return lat_q_power(E);
 }
 
-// The same by the two warps that do nothing else, of all items but the first, a lane a row: beside the softmax and the output
-// of the item before (a prompt of 4K under a window of 128, two tiles an item: 610 -> 486 us).
+// The same by the two warps that do nothing else, of all items but the first, a lane a row: beside the softmax and the
+// output of the item before (a prompt of 4K under a window of 128, two tiles an item: 610 -> 486 us).
 __device__ __forceinline__ void lat_q_row(uint32_t sb, uint32_t top_at, int r) {
     const uint32_t row = sb + (uint32_t)r * 128;
     uint32_t top = 0;
@@ -854,7 +865,7 @@ __device__ __forceinline__ void lat_q_row(uint32_t sb, uint32_t top_at, int r) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint4 v = ld_shared_v4(row + c * LP_QSLAB + (uint32_t)((e ^ r) & 7) * 16);
-            top = __vmaxu2(__vmaxu2(top, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            top = max_magnitude(top, v);
         }
     }
     if (LAT_RARE((top & 0x7FFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u)) {
@@ -897,15 +908,16 @@ __device__ __noinline__ void lat_infinities(uint32_t to, uint32_t limit, int r0)
         uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            if ((w[x] & 0x7FFFu) >= most && (w[x] & 0x7FFFu) < 0x7C00u) w[x] = (w[x] & 0xFFFF8000u) | 0x7C00u;
-            if (((w[x] >> 16) & 0x7FFFu) >= most && ((w[x] >> 16) & 0x7FFFu) < 0x7C00u) w[x] = (w[x] & 0x8000FFFFu) | 0x7C000000u;
+            const uint32_t lo = w[x] & 0x7FFFu, hi = (w[x] >> 16) & 0x7FFFu;
+            if (lo >= most && lo < 0x7C00u) w[x] = (w[x] & 0xFFFF8000u) | 0x7C00u;
+            if (hi >= most && hi < 0x7C00u) w[x] = (w[x] & 0x8000FFFFu) | 0x7C000000u;
         }
         st_shared_v4(ad, v);
     }
 }
 
 // How a kernel's key rows are laid out and copied: bf16 rows by gathers or in boxes, or quantised rows, which the loading
-// warps turn into bf16.
+// warps turn into fp16.
 // (LK_QUANT4: four rows always share a page; LK_QUANT1: pages of any number of rows.)
 enum LatKeys { LK_GATHER, LK_BOX, LK_QUANT4, LK_QUANT1 };
 __host__ __device__ constexpr bool lat_quant(LatKeys keys) { return keys == LK_QUANT4 || keys == LK_QUANT1; }
@@ -915,7 +927,7 @@ constexpr int LQ_WARPS = 2;  // quantised rows: warps for the queries
 __host__ __device__ constexpr int lat_threads(LatKeys keys) {
     return 32 * (LP_SOFT + 2 + lat_loaders(keys) + (lat_quant(keys) ? LQ_WARPS : 0));
 }
-static_assert(lat_threads(LK_QUANT4) == 640, "five warpgroups: 2 x 104 + 3 x 88 registers of the 5 x 96 that they start with");
+static_assert(lat_threads(LK_QUANT4) == 640, "five warpgroups: 2 x 104 + 3 x 88 registers of 5 x 96 at the start");
 static_assert(lat_threads(LK_BOX) == LP_T, "the bf16 kernels' warps");
 
 // Ratios and factors of a tile whose rows each keep a scale of their own (lane l with rows 4 l ..., those of v there).
@@ -1066,7 +1078,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 float mt = -INFINITY;  // of the logits before scaling
                 bool bad = false;
                 float* xs = reinterpret_cast<float*>(sr);
-                // the unit of a logit; quantised: the largest weight times its row's scale, in log2 units; log2 of the tile's scale
+                // the unit of a logit; quantised: the largest weight times its row's scale, in log2 units; log2 of the tile's
+                // scale
                 float yt = -INFINITY, tsl2 = QUANT ? 1.f : a.sl2, tpow = 0.f;
                 const uint32_t fa = sb + LP_SM_FACTOR + (uint32_t)(g & 7) * 512 + (uint32_t)ub * 64;
                 if (QUANT) {
@@ -1079,7 +1092,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         // the logits themselves, in log2 units: times what makes them small before the rows' scales, times
                         // what makes them large behind them
                         const float u = lat_unit(a.sl2, qe);
-                        const uint64_t u0 = qe < 0 ? f32x2(u, u) : f32x2(1.f, 1.f), u1 = qe < 0 ? f32x2(1.f, 1.f) : f32x2(u, u);
+                        const uint64_t u0 = qe < 0 ? f32x2(u, u) : f32x2(1.f, 1.f);
+                        const uint64_t u1 = qe < 0 ? f32x2(1.f, 1.f) : f32x2(u, u);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             if (c < nc) {
@@ -1175,10 +1189,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                 }
                 const float mref = m_run == -INFINITY ? 0.f : m_run;
                 const float yref = QUANT && y_run != -INFINITY ? y_run : 0.f;
-                // Quantised and one scale: the weight in fp16 times that scale at once, and the sum without it.  Rows with scales
-                // of their own, and a scale so far below another's that the sum's terms could be lost under 2^-126 (the two
-                // references are at most LP_RESCALE - LQ_ROOM further apart than the scales): a weight times its scale has an
-                // exponential of its own (a weight, a scale and the largest product may each be next to nothing).
+                // Quantised and one scale: the weight in fp16 times that scale at once, and the sum without it.  Rows with
+                // scales of their own, and a scale so far below another's that the sum's terms could be lost under 2^-126
+                // (the two references are at most LP_RESCALE - LQ_ROOM further apart than the scales): a weight times its
+                // scale has an exponential of its own (a weight, a scale and the largest product may each be next to
+                // nothing).
                 const bool two = QUANT && some && LAT_RARE(!even || most - top > LQ_APART);
                 const float ref = even && !two ? yref - tpow - LQ_ROOM : mref;
                 const uint64_t sl2 = f32x2(tsl2, tsl2), mneg = f32x2(-ref, -ref);
@@ -1193,7 +1208,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                                 const uint2 f = ld_shared_v2(fa + 64 * c + 4 * j);
                                 const uint64_t y = f32x2(xs[16 * c + j], xs[16 * c + j + 1]);
                                 const float2 e = f32x2_split(f32x2_fma(y, sl2, mneg));
-                                const float2 t = f32x2_split(f32x2_fma(y, sl2, f32x2(q_log(f.x) + shift, q_log(f.y) + shift)));
+                                const uint64_t with = f32x2(q_log(f.x) + shift, q_log(f.y) + shift);
+                                const float2 t = f32x2_split(f32x2_fma(y, sl2, with));
                                 sum = f32x2_add(sum, f32x2(lat_ex2(e.x), lat_ex2(e.y)));
                                 xs[16 * c + j] = lat_ex2(t.x), xs[16 * c + j + 1] = lat_ex2(t.y);
                             }
@@ -1204,7 +1220,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         if (c < nc && some) {
 #pragma unroll
                             for (int j = 0; j < 16; j += 2) {
-                                const float2 e = f32x2_split(f32x2_fma(f32x2(xs[16 * c + j], xs[16 * c + j + 1]), sl2, mneg));
+                                const uint64_t y = f32x2(xs[16 * c + j], xs[16 * c + j + 1]);
+                                const float2 e = f32x2_split(f32x2_fma(y, sl2, mneg));
                                 const float p0 = lat_ex2(e.x), p1 = lat_ex2(e.y);
                                 sum = f32x2_add(sum, f32x2(p0, p1));
                                 if (!QUANT) sr[8 * c + (j >> 1)] = pack_bf16x2(p0, p1);
@@ -1220,7 +1237,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     for (int c = 0; c < 2; ++c)
                         if (c < nc) {
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) sr[8 * c + (j >> 1)] = pack_f16x2(xs[16 * c + j], xs[16 * c + j + 1]);
+                            for (int j = 0; j < 16; j += 2)
+                                sr[8 * c + (j >> 1)] = pack_f16x2(xs[16 * c + j], xs[16 * c + j + 1]);
                         }
                 }
                 // P and O are free once the product before this one is done; a short tile, the item's last, has a
@@ -1316,8 +1334,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             // this row of the partial results
             const int64_t prow = QUANT ? (int64_t)x.part * a.slot_rows + (int)rank * 64 + r : 0;
             bool had = false;
-            float e = 0.f;  // (bf16 rows: of the threads that store it; with that and a place of the partial results in every
-                            // thread a prompt of 8K tokens took 1 percent more)
+            float e = 0.f;  // (bf16 rows: of the threads that store it; with that and a place of the partial results in
+                            // every thread a prompt of 8K tokens took 1 percent more)
             if (QUANT || (tid < 64 && mine)) e = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LP_LN2;
             if (more) {
                 const float before = mine ? __ldcg(a.part_lse + prow) : -INFINITY;
@@ -1363,8 +1381,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                         tc_ld32(tmem + lane_off + 128 * ch + c, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]) * inv * root, root, had ? old * __ldcg(was + c + e) : 0.f));
+                        for (int e = 0; e < 32; ++e) {
+                            const float there = had ? old * __ldcg(was + c + e) : 0.f;
+                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]) * inv * root, root, there));
+                        }
                         tc_st32(tmem + lane_off + 128 * ch + c, o);
                     }
                     tc_wait_st();
@@ -1378,19 +1398,17 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = 0;
                     } else if (direct) {
-                        constexpr int COLS = 32;
 #pragma unroll
-                        for (int h = 0; h < 64 / COLS; ++h) {
-                            uint32_t o[COLS];
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t o[32];
                             const uint64_t inv2 = f32x2(inv, inv);
-                            if constexpr (COLS == 16) tc_ld16(tmem + lane_off + 128 * ch + 64 * c + 16 * h, o);
-                            else tc_ld32(tmem + lane_off + 128 * ch + 64 * c + 32 * h, o);
+                            tc_ld32(tmem + lane_off + 128 * ch + 64 * c + 32 * h, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < COLS / 2; ++e) {
+                            for (int e = 0; e < 16; ++e) {
                                 const float2 f = f32x2_split(
                                     f32x2_mul(f32x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2));
-                                v[COLS / 2 * h + e] = pack_bf16x2(f.x, f.y);
+                                v[16 * h + e] = pack_bf16x2(f.x, f.y);
                             }
                         }
                     } else {
@@ -1572,7 +1590,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     // scales: lane l has rows 4 l .. 4 l + 3.
                     uint32_t* at = reinterpret_cast<uint32_t*>(sm + LP_SM_LOOK) + (g & 3) * 128;
                     const int u = u0 + (lane >> 2), j0 = u < x.nU ? unit_row<WINDOW>(x, u) + 4 * (lane & 3) : x.hi;
-                    const int e0 = min(max(x.lo - j0, 0), 4), e1 = min(max(x.hi - j0, 0), 4), e2 = min(max(min(x.a1, x.hi) - j0, 0), 4);
+                    const int e0 = min(max(x.lo - j0, 0), 4), e1 = min(max(x.hi - j0, 0), 4);
+                    const int e2 = min(max(min(x.a1, x.hi) - j0, 0), 4);
                     uint32_t seen = (((1u << e1) - 1u) & ~((1u << e0) - 1u)) | ((1u << e2) - 1u);  // by any query
                     uint32_t id[4], sc[4], v = 0;
                     bool bad = false;
@@ -1588,8 +1607,10 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             v = seen;
                             id[0] = (uint32_t)pg * (uint32_t)(a.kv.page_stride / 16) + (uint32_t)rw * (Q_CODES / 16);
                             // (into L2, each CTA half of the tile, three tiles before the loading warps come for them)
-                            if (lane >> 4 == (int)rank) prefetch_l2(q_codes(a.kv.base, a.kv.page_stride, pg, rw), 4 * Q_CODES);
-                            w = __ldg(reinterpret_cast<const uint4*>(q_scales(a.kv.base, a.kv.page_stride, a.kv.rpp, pg, rw)));
+                            if (lane >> 4 == (int)rank)
+                                prefetch_l2(q_codes(a.kv.base, a.kv.page_stride, pg, rw), 4 * Q_CODES);
+                            w = __ldg(reinterpret_cast<const uint4*>(
+                                q_scales(a.kv.base, a.kv.page_stride, a.kv.rpp, pg, rw)));
                         }
                         sc[0] = w.x, sc[1] = w.y, sc[2] = w.z, sc[3] = w.w;
 #pragma unroll
@@ -1608,7 +1629,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                             bad = bad || (!there && ((seen >> e) & 1u));
                             id[e] = sc[e] = 0;
                             if (there) {
-                                id[e] = (uint32_t)pg[e] * (uint32_t)(a.kv.page_stride / 16) + (uint32_t)rw[e] * (Q_CODES / 16);
+                                id[e] = (uint32_t)pg[e] * (uint32_t)(a.kv.page_stride / 16) +
+                                        (uint32_t)rw[e] * (Q_CODES / 16);
                                 sc[e] = __ldg(reinterpret_cast<const uint32_t*>(
                                     q_scales(a.kv.base, a.kv.page_stride, a.kv.rpp, pg[e], rw[e])));
                                 v |= 1u << e;
@@ -1749,8 +1771,9 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         const int r0 = (lane >> 2) & 1, p0 = (lane & 3) + 4 * (lane >> 3);
         const uint32_t in_slot = (uint32_t)(r0 * 128 + (((lane & 3) * 2 ^ r0) << 4));
         const uint32_t k_slot = 2 * (w >> 2), v_slot = 4 + (w >> 1);
-        const uint32_t k_to = sb + LP_SM_RING + k_slot * LP_SLOT + in_slot + ((uint32_t)lane >> 3) * 8192 + (uint32_t)(w & 3) * 2048;
-        const uint32_t v_to = sb + LP_SM_RING + v_slot * LP_SLOT + in_slot + ((uint32_t)lane >> 3) * 4096 + (uint32_t)(w & 1) * 2048;
+        const uint32_t ring = sb + LP_SM_RING + in_slot, slab = (uint32_t)lane >> 3;
+        const uint32_t k_to = ring + k_slot * LP_SLOT + slab * 8192 + (uint32_t)(w & 3) * 2048;
+        const uint32_t v_to = ring + v_slot * LP_SLOT + slab * 4096 + (uint32_t)(w & 1) * 2048;
         const uint8_t* base = a.kv.base + p0 * 16;
         // K rows have the ring's first four slots, V rows the others: each part of them is one warp's alone, tile
         // after tile, so that a wait for it to be free cannot be two uses behind.
@@ -1789,7 +1812,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             }
             t.units = min(8, units - 8 * i);
             t.g = g++;
-            if (!__all_sync(0xffffffffu, looked)) ok = ok && __all_sync(0xffffffffu, lat_wait<QUANT>(sb + LP_LOOK + 8 * (t.g & 7), (t.g >> 3) & 1, dead));
+            if (!__all_sync(0xffffffffu, looked))
+                ok = ok && __all_sync(0xffffffffu, lat_wait<QUANT>(sb + LP_LOOK + 8 * (t.g & 7), (t.g >> 3) & 1, dead));
             return ok;
         };
         uint4 c[8];
@@ -1799,9 +1823,12 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             return r0 + (k ? (int)rank * ((t.units + 1) >> 1) * 16 + 16 * (w & 3) : 16 * w);
         };
         auto half_of = [&](bool k) { return k ? (uint32_t)w >> 2 : rank; };
-        auto rows_at = [&](const Tile& t, bool k) { return sb + LP_SM_LOOK + (uint32_t)(t.g & 3) * 512 + (uint32_t)row_of(t, k) * 4; };
+        auto rows_at = [&](const Tile& t, bool k) {
+            return sb + LP_SM_LOOK + (uint32_t)(t.g & 3) * 512 + (uint32_t)row_of(t, k) * 4;
+        };
         auto ratios_at = [&](const Tile& t, bool k) {
-            return sb + LP_SM_RATIO + (uint32_t)(t.g & 3) * 1024 + (uint32_t)row_of(t, k) * 8 + half_of(k) * 4 + (uint32_t)(p0 >> 3) * 2;
+            return sb + LP_SM_RATIO + (uint32_t)(t.g & 3) * 1024 + (uint32_t)row_of(t, k) * 8 + half_of(k) * 4 +
+                   (uint32_t)(p0 >> 3) * 2;
         };
         Tile cur = {0, 0}, next = {0, 0}, v_first = {0, 0}, v_last = {0, 0};  // tiles whose V rows are still to come
         int pending = 0;
@@ -1857,7 +1884,8 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             }
             if (have) {
                 if (LAT_RARE(full && (ld_shared_u32(sb + LP_SM_PLAIN + (cur.g & 7) * 4) & LQ_HUGE))) {
-                    const uint32_t at = sb + LP_SM_FACTOR + (uint32_t)(cur.g & 7) * 512 + (uint32_t)(row_of(cur, is_k) - r0 + (lane & 15)) * 4;
+                    const uint32_t at = sb + LP_SM_FACTOR + (uint32_t)(cur.g & 7) * 512 +
+                                        (uint32_t)(row_of(cur, is_k) - r0 + (lane & 15)) * 4;
                     lat_infinities(to, q_limit(ld_shared_u32(at) >> 23), r0);
                 }
                 fence_proxy_async_smem();
@@ -2094,7 +2122,8 @@ constexpr int QM_CTAS = 2 * 2 * LP_PAIRS;
 constexpr float QM_MOST = 128.f;                 // more than a row has partial results; a power of two: the same bits
 static_assert(QR < QM_MOST, "partial results of a row");
 __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
-    // (each CTA reads the runs once: warps that all read them for themselves took 24 us and more at the few L2 lines they are in)
+    // (each CTA reads the runs once: warps that all read them for themselves took 24 us and more at the few L2 lines that
+    // they are in)
     __shared__ int listed[3 * (QR + 1)];
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -2145,7 +2174,8 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
                 v[s] = r <= last ? __ldcg(a.part_lse + prow) : -INFINITY;
                 if (r <= last) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) f[s][c] = __ldcg(reinterpret_cast<const float4*>(a.part_o + prow * D) + lane + 32 * c);
+                    for (int c = 0; c < 4; ++c)
+                        f[s][c] = __ldcg(reinterpret_cast<const float4*>(a.part_o + prow * D) + lane + 32 * c);
                 }
             }
             float m = M;
@@ -2180,7 +2210,8 @@ __global__ void __launch_bounds__(256, 2) quant_merge_kernel(LatArgs a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             reinterpret_cast<uint2*>(a.out + (int64_t)row * D)[lane + 32 * c] =
-                make_uint2(pack_bf16x2(o[4 * c] * inv, o[4 * c + 1] * inv), pack_bf16x2(o[4 * c + 2] * inv, o[4 * c + 3] * inv));
+                make_uint2(pack_bf16x2(o[4 * c] * inv, o[4 * c + 1] * inv),
+                           pack_bf16x2(o[4 * c + 2] * inv, o[4 * c + 3] * inv));
         if (lane == 0 && a.lse)
             a.lse[row] = nan ? __int_as_float(0x7FFFFFFF) : (L == 0.f || lost ? -INFINITY : M + log2f(L * QM_MOST) * LP_LN2);
     }
@@ -2331,7 +2362,13 @@ static size_t parts_bytes(const LatArgs& a) {
 }
 
 // Quantised rows: runs where there are few row tiles (QUANT_FEW at most, and QUANT_SEQS sequences, whose lengths every
-// CTA adds up before it begins); else whole row tiles are dealt out in turn.
+// CTA adds up before it begins); else whole row tiles are dealt out in turn.  Both sides, whole row tiles and runs: chunks of
+// 100, 152, 200, 304, 320, 400, 700 and 1,024 tokens of 128 heads (as many row tiles) over 8K rows 325 and 238 us, 330 and
+// 333, 487 and 452, 654 and 663, 810 and 714, 974 and 894, 1,644 and 1,588, 2,338 and 2,377; 400 and 1,024 over 1K 180 and
+// 194, 483 and 590; 400 and 1,000 under a window of 128 63 and 68, 130 and 138.  (So row tiles that come out unevenly gain
+// up to a thousand of them, short ones lose.)  Single tokens of 16 heads, ragged: 128 over 8K rows 324 and 184 us, 256
+// 532 and 340; beyond QUANT_SEQS runs would be the faster too, 300 over 8K 566 and 394, 1,000 over 2K 455 and 407, and 300
+// of which one has 128K rows 2,579 and 132.
 constexpr int QUANT_FEW = 4 * LP_PAIRS, QUANT_SEQS = 256;
 constexpr int QUANT_CUT = 2;                     // places of a run at least (6: one token of 16 heads over 4K 29 us
                                                  // instead of 20, without the merge)

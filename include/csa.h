@@ -316,8 +316,8 @@ csa_status csa_window_attn(const void* q, int32_t H, float scale, csa_paged kv_r
  * codes at s * 512 and its scales at rows_per_page * 512 + s * 4.  Such a pool is one of a csa_page_pools like any other.
  * page_table [B, page_table_stride] is required; n_pages < 2^31 and n_pages * page_stride_bytes <= 64 GiB (else
  * CSA_ERR_UNSUPPORTED).  The e4m3 codes 0x7F and 0xFF, which are no numbers, do not occur in a row that csa_quant_write
- * made.  In any other csa_quant_attn takes them as NaN, and csa_quant_read, which does not tell them from the codes below them,
- * gives 480 and -480 times the scale.
+ * made.  In any other csa_quant_attn takes them as NaN, and csa_quant_read, which does not tell them from the codes below
+ * them, gives 480 and -480 times the scale.
  *
  * The three calls take a ragged batch the same way: B sequences, sequence b with offsets[b+1] - offsets[b] rows of the
  * batch's buffers (device int64 [B+1], non-decreasing), which are the last of its n_tokens[b] tokens (device int64 [B]).
@@ -347,9 +347,12 @@ csa_status csa_quant_read(csa_paged cache, int64_t page_table_stride, int32_t B,
 /* csa_window_attn over quantised rows: causal attention of each sequence's new tokens, a chunk of a prompt, a draft or a
  * single token, whose own rows are in the cache already.  Arguments, results, limits and accuracy (against the values
  * that the rows stand for) as there, with these differences.  A window of 2^30 is attention over everything before a token.
- * The workspace is at most 61 MB, whatever the context and the window.  The products are made in fp16: of a query the values
- * 2^39 below its largest, and of the rows of 128 neighbouring keys those 2^33 below the largest, may count as 0.  A query
- * for which scale * sum |q_i k_i| passes 2^22 for some key has no defined result. */
+ * The workspace is at most 61 MB, whatever the context and the window; smaller calls may need more of it than larger ones
+ * (only calls with few row tiles of 128 query rows cut them), and 61 MB do for any call.  The products are made in fp16: of
+ * a query the values 2^39 below its largest, and of the rows of 128 neighbouring keys those 2^33 below the largest, may
+ * count as 0.  So may, in an output, a row whose weight times its largest scale is 2^32 below the largest such product of
+ * the rows that the query sees; in lse it counts.  A query for which scale * sum |q_i k_i| passes 2^22 for some key has no
+ * defined result. */
 size_t csa_quant_attn_workspace_size(int32_t B, int32_t H, int64_t total_q, int64_t max_q, int32_t window,
                                      int32_t n_sink);
 csa_status csa_quant_attn(const void* q, int32_t H, float scale, csa_paged cache, int64_t page_table_stride,
@@ -599,8 +602,9 @@ csa_status csa_selftest_pairs(int32_t pairs);
 /*
  * Merge self-test: the last kernel of a csa_quant_attn call alone, over a workspace of any contents, as a call whose waits
  * ran out may leave it.  out bf16 [rows, 512] (16-byte aligned), lse fp32 [rows] (nullable): nothing outside them is written
- * and nothing outside the workspace (16-byte aligned, csa_quant_attn_workspace_size(1, 1, rows, rows, 1, 0) bytes, or that of
- * 128 rows where there are more) is read, whatever it holds.  rows < 1 or bad pointers: CSA_ERR_INVALID_ARG.
+ * and nothing outside the workspace (16-byte aligned, csa_quant_attn_workspace_size(1, 1, rows, rows, 1, 0) bytes, or that
+ * of 128 rows where there are more) is read, whatever it holds.  rows < 1 or bad pointers: CSA_ERR_INVALID_ARG; a smaller
+ * workspace: CSA_ERR_WORKSPACE.
  */
 csa_status csa_selftest_quant_merge(const void* workspace, size_t ws_bytes, int32_t rows, void* out, float* lse,
                                     void* stream);
