@@ -392,3 +392,22 @@ def test_drawn_scales(m, seed):  # noqa: F811
     assert m.csa_read_device_status() == 0
     for i in {0, q_len // 2, q_len - 1}:
         check_any_scales(c, 0, q[i].double(), out[i], lse[i], n - q_len + i + 1, (seed, i))
+
+
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+def test_buffers_and_workspaces_that_are_16_byte_aligned_and_no_more(m, H, q_len, n):  # noqa: F811
+    g = gen(37)
+    c = Cache(g, [n], 64)
+    q = randn(g, q_len, H, D)
+    want = attention(m, c, q, [q_len], [n])
+    q2 = torch.empty(q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view_as(q).copy_(q)
+    out = torch.empty(q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view_as(q)
+    lse = torch.empty(q_len * H + 1, device="cuda")[1:].view(q_len, H)
+    need = m.csa_quant_attn_workspace_size(1, H, q_len, q_len, ALL, 0)
+    ws = torch.full((need + 32,), 255, dtype=torch.uint8, device="cuda")[16:]
+    assert q2.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16 and lse.data_ptr() % 8 == 4 and ws.data_ptr() % 32 == 16
+    m.csa_quant_attn(q2, H, SCALE, c.paged(m), c.width, 1, torch.tensor([0, q_len], device="cuda"),
+                     torch.tensor([n], device="cuda"), q_len, q_len, ALL, 0, out, lse, ws, need)
+    assert m.csa_read_device_status() == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert bool((ws[need:] == 255).all())
