@@ -483,8 +483,9 @@ __device__ __forceinline__ bool quant_item(const LatArgs& a, QuantCursor& c, int
             c.c0 = -32;
             c.base = c.sum = 0;
             if (report && pair == 0 && lane == 0) a.runs[QR].row0 = (int)((c.total + c.cut - 1) / c.cut);
-            for (int r = pair + lane * pairs; report && r < QR; r += 32 * pairs) a.runs[r] = {0, 0, r};
-            __syncwarp();
+            if (report && lane == 0)
+#pragma unroll 1
+                for (int r = pair; r < QR; r += pairs) a.runs[r] = {0, 0, r};
         }
         c.pos = c.end = 0;
         c.run = pair - pairs;
@@ -916,6 +917,17 @@ __device__ __noinline__ void lat_infinities(uint32_t to, uint32_t limit, int r0)
     }
 }
 
+// Whether any of n logits is not finite (a warp).
+__device__ __noinline__ bool lat_infinite(uint32_t ts, int n) {
+    uint32_t v = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        v = max(v, tc_ld1(ts + j) & 0x7FFFFFFFu);
+        __syncwarp();
+    }
+    return v >= 0x7F800000u;
+}
+
 // How a kernel's key rows are laid out and copied: bf16 rows by gathers or in boxes, or quantised rows, which the loading
 // warps turn into fp16.
 // (LK_QUANT4: four rows always share a page; LK_QUANT1: pages of any number of rows.)
@@ -1028,7 +1040,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
         while (next_item()) {
             const int row = x.row0 + (int)rank * 64 + r;  // this thread's query row
             const bool mine = (int)rank * 64 + r < x.nrows;
-            const bool some = !QUANT || __any_sync(0xffffffffu, mine);  // (warps without a row only wait)
+            const bool some = !QUANT || __any_sync(0xffffffffu, mine);  // (warps without a row only wait, as a rule)
             // rows that this query sees: [vlo, vhi) and [0, vs)
             int vlo = 0, vhi = 0, vs = 0;
             if (mine) {
@@ -1109,6 +1121,11 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
                     }
                 }
                 if (!some) {
+                    // (a CTA without any row has half of the values' dims all the same: it looks at the logits of the rows
+                    // that it does not have, which are not finite where a key is not)
+                    if (LAT_RARE(!plain && (int)rank * 64 >= x.nrows)) {
+                        bad = lat_infinite(ts, 16 * min(nc, nu - ub));
+                    }
                 } else if (plain) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) mt = fmaxf(mt, xs[j]);

@@ -411,3 +411,26 @@ def test_buffers_and_workspaces_that_are_16_byte_aligned_and_no_more(m, H, q_len
     assert m.csa_read_device_status() == 0
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert bool((ws[need:] == 255).all())
+
+
+@pytest.mark.parametrize("H,q_len,n", [(1, 20, 60), (1, 64, 90), (1, 100, 300), (16, 3, 90), (16, 4, 1000), (16, 5, 200), (24, 2, 2),
+                                       (64, 3, 140), (100, 2, 130), (128, 3, 129)])
+@pytest.mark.parametrize("scale", [255, 254])
+def test_no_numbers_that_later_tokens_see(m, H, q_len, n, scale):  # noqa: F811
+    """A row that is no number, or infinite, among a batch's new tokens: those before it are not touched, in any block of
+    dims, however few query rows there are."""
+    for block in range(4):
+        g = gen(38 + block)
+        c = Cache(g, [n], 64)
+        c.codes()[:] = c.codes() % 128 % 0x38 + c.codes() // 128 * 128
+        c.scales()[:] = 127
+        at = n - 1 - q_len // 2 if q_len > 2 else n - 1
+        page, slot = places(c, 0, n)
+        c.scales()[page[at], slot[at], block] = scale
+        c.codes()[page[at], slot[at], 128 * block: 128 * block + 128: 3] = 0x7E
+        q = randn(g, q_len, H, D)
+        out, lse = attention(m, c, q, [q_len], [n])
+        assert m.csa_read_device_status() == 0
+        check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in range(q_len)])
+        before = q_len - (n - at)
+        assert before >= 1 and bool(torch.isfinite(out[:before]).all()) and not bool(torch.isfinite(out[before]).all())
