@@ -58,7 +58,7 @@
 // noted (LP_SM_LOST), and its output mended behind the item (lat_not_finite).
 //
 // Quantised rows.  The loading warps turn codes into fp16 on their way to the ring, each value over the largest scale of its
-// tile: a conversion and a product for two values, where bf16, which has no conversion from e4m3, takes five
+// tile (times 2^Q_UP, as far as fp16 reaches): a conversion and a product for two values, where bf16, which has no conversion from e4m3, takes five
 // operations; S and P V are then fp16 products.  That scale, 2^T, comes back in the softmax: logits are multiplied by
 // it, and O and the weights (fp16, at most 2^15) are kept over a running maximum of weight times scale, while
 // the sum of the weights has one of the weights alone.  Rows more than 2^15 apart keep scales of their own, which the
@@ -801,8 +801,9 @@ __device__ __forceinline__ float lat_unit(float sl2, int e) {
     const float u = sl2 * __uint_as_float((uint32_t)(h + 127) << 23) * __uint_as_float((uint32_t)(e - h + 127) << 23);
     return fminf(fmaxf(u, __int_as_float(1)), 3.4028235e38f);
 }
-// The part of e of a query whose largest value has the exponent E and is now in [2^14, 2^15).
-__device__ __forceinline__ int lat_q_power(uint32_t E) { return (int)E - 141; }
+// The part of e of a query whose largest value has the exponent E and is now in [2^14, 2^15), for rows that are 2^Q_UP as
+// large as they should be.
+__device__ __forceinline__ int lat_q_power(uint32_t E) { return (int)E - 141 - Q_UP; }
 
 // The larger of top and v's magnitudes, as the bits of two bf16.
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t top, const uint4& v) {
@@ -1342,7 +1343,7 @@ __device__ __forceinline__ void lat_pair(const CUtensorMap& qmap, const KeyMaps&
             // quantised: O's unit too; one next to nothing would leave inv no bits, so that its root comes in twice
             float root = 1.f;
             if (QUANT && l_run != 0.f) {
-                const float unit = y_run - m_run - LQ_ROOM;
+                const float unit = y_run - m_run - LQ_ROOM - Q_UP;
                 if (LAT_RARE(unit < -64.f)) root = lat_ex2(0.5f * unit);
                 else inv *= lat_ex2(unit);
             }

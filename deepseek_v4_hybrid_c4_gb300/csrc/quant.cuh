@@ -65,10 +65,12 @@ CSA_DEV uint32_t q_top(uint32_t w) {
     return nan == 0x80808080u ? 127u : max(m & 255u, m >> 16);
 }
 CSA_DEV uint32_t q_power(uint32_t s) { return s ? s << 23 : 0x00400000u; }  // 2^(s - 127), fp32
-// Scale s over 2^(top - 127), in fp16.  A block 2^15 and more below loses bits of its smallest codes: at most 2^-25
-// of the larger unit.
+// 2^Q_UP times scale s over 2^(top - 127), in fp16: a value is at most 480 * 2^Q_UP, and the least ratio that there is
+// 2^-24, so that a block is lost only where its scale is 2^32 and more below (2^25 without Q_UP).  A block 2^22 and more below
+// loses bits of its smallest codes: at most 2^-32 of the larger unit.
+constexpr int Q_UP = 7;
 CSA_DEV uint32_t q_ratio(uint32_t s, uint32_t top) {
-    const int d = (int)(top - s);
+    const int d = (int)(top - s) - Q_UP;
     return s == 255u ? 0x7E00u : d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
 }
 
@@ -77,9 +79,9 @@ static __device__ __noinline__ uint2 q_ratios_any(uint32_t w, uint32_t top) {
                       q_ratio((w >> 16) & 255u, top) | q_ratio(w >> 24, top) << 16);
 }
 // Those of a row's four scales, all numbers (0 where the row is not there).  As a rule no block is 2^15 below: the upper
-// bytes are (15 - d) << 2, all four at once.
+// bytes are (15 + Q_UP - d) << 2, all four at once.
 CSA_DEV uint2 q_ratios(uint32_t w, uint32_t top, bool there) {
-    const uint32_t d = top * 0x01010101u - w, h = (0x0F0F0F0Fu - d) << 2;
+    const uint32_t d = top * 0x01010101u - w, h = ((15 + Q_UP) * 0x01010101u - d) << 2;
     uint2 r = make_uint2(__byte_perm(h, 0, 0x1404), __byte_perm(h, 0, 0x3424));
     if (!there) r = make_uint2(0, 0);
     else if ((d + 0x01010101u) & 0xF0F0F0F0u) r = q_ratios_any(w, top);
@@ -105,9 +107,9 @@ CSA_DEV void q_halves(const uint4& c, uint32_t bits, uint4& a, uint4& b) {
     e4m3x4_f16(c.w, r, b.z, b.w);
 }
 
-// Values of 2^128 and more, which are infinities as bf16: the least of them over a row's largest scale, in fp16
-// (infinity where the row has none).
-CSA_DEV uint32_t q_limit(uint32_t top) { return top >= 247u ? (270u - top) << 10 : 0x7C00u; }
+// Values of 2^128 and more, which are infinities as bf16: 2^Q_UP times the least of them over a row's largest scale, in
+// fp16 (infinity where the row has none).
+CSA_DEV uint32_t q_limit(uint32_t top) { return top >= 247u ? (270u + Q_UP - top) << 10 : 0x7C00u; }
 
 // The last sequence that starts at or before row `row` (a warp; B + 1 offsets that do not fall): 32 of those left
 // are looked at a time.

@@ -349,7 +349,7 @@ csa_status csa_quant_read(csa_paged cache, int64_t page_table_stride, int32_t B,
  * that the rows stand for) as there, with these differences.  A window of 2^30 is attention over everything before a token.
  * The workspace is at most 61 MB, whatever the context and the window; smaller calls may need more of it than larger ones
  * (only calls with few row tiles of 128 query rows cut them), and 61 MB do for any call.  The products are made in fp16: of
- * a query the values 2^39 below its largest, and of the rows of 128 neighbouring keys those 2^33 below the largest, may
+ * a query the values 2^39 below its largest, and of the rows of 128 neighbouring keys those 2^31 below the largest, may
  * count as 0.  So may, in an output, a row whose weight times its largest scale is 2^32 below the largest such product of
  * the rows that the query sees; in lse it counts.  A query for which scale * sum |q_i k_i| passes 2^22 for some key has no
  * defined result. */

@@ -331,21 +331,26 @@ def test_values_next_to_the_largest_number(m):  # noqa: F811
 
 
 def check_any_scales(c, b, q, out, lse, n, where):
-    """Rows of any finite scales.  Beside what attend() counts: a row's values are known to 2^-25 of its unit (half of fp16's least
-    step), the power of two of its tile's largest scale or, where the tile's rows are more than 2^15 apart, of its own
-    largest; a query's to 2^-39 of its largest; and a weight times its unit to 2^-32 of the largest such product
+    """Rows of any finite scales.  Beside what attend() counts: a row's values are kept in fp16 as 2^7 times their ratio to its unit,
+    the power of two of its tile's largest scale or, where the tile's rows are more than 2^15 apart, of its own largest.  So
+    they are known to 2^-32 of the unit (half of fp16's least step, 2^-25, over 2^7); a block whose scale is 2^32 and
+    more below has no such ratio (2^-25 is no fp16 number) and may count as 0.  A query's values are known to 2^-39 of its
+    largest, and a weight times its unit to 2^-32 of the largest such product
     (test_small_queries_of_large_rows_and_the_other_way_round).  A logit's error moves a weight by twice that."""
     js = torch.arange(n, device="cuda")
     page = c.table[b].long()[js // c.rpp]
-    top = c.scales()[page, js % c.rpp].amax(-1).long()
+    scale = c.scales()[page, js % c.rpp].long()
+    top = scale.amax(-1)
     unit = top.clone()
     for t in range(0, n, 128):
         rows = top[t: t + 128]
         some = rows[rows > 10]
         if len(some) and int(rows.max() - some.min()) <= 15:
             unit[t: t + 128] = rows.max()
+    lost = (unit[:, None] - scale >= 32).repeat_interleave(128, 1)
     unit = power(unit - 127)
     kv = c.rows(b, range(n))
+    off = torch.where(lost, kv.abs(), 2.0**-32 * unit[:, None])
     x = SCALE * (q @ kv.t())
     full = torch.logsumexp(x, -1)
     w = torch.exp(x - full[:, None])
@@ -353,10 +358,10 @@ def check_any_scales(c, b, q, out, lse, n, where):
     d = 2.0**-14 * SCALE * (q.abs() @ kv.abs().t()).amax(-1)
     if float(d.max()) > 2.0**8:
         return False                                     # no defined result
-    d = d + SCALE * ((q.abs().sum(-1)[:, None] * 2.0**-25 * unit).amax(-1) + 2.0**-39 * q.abs().amax(-1) * kv.abs().sum(-1).amax())
+    d = d + SCALE * ((q.abs() @ off.t()).amax(-1) + 2.0**-39 * q.abs().amax(-1) * kv.abs().sum(-1).amax())
     ok = d < 0.25                                        # (e^(2 d) - 1 <= 3 d)
     to = 2.0**-8 * (a + o.abs()) + (3 * d[:, None] + 2.0**-20) * a + 2.0**-133
-    to = to + (2.0**-25 * (w @ unit) + 2.0**-32 * (w * unit).amax(-1) * (kv.abs() / unit[:, None]).sum(0).amax())[:, None]
+    to = to + w @ off + (2.0**-32 * (w * unit).amax(-1) * (kv.abs() / unit[:, None]).sum(0).amax())[:, None]
     assert float(((out.double() - o).abs() - to)[ok].max() if bool(ok.any()) else -1) <= 0, where
     assert float(((lse.double() - full).abs() - d - 2.0**-20 * (1 + full.abs())).max()) <= 0, where
     return True
@@ -434,3 +439,26 @@ def test_no_numbers_that_later_tokens_see(m, H, q_len, n, scale):  # noqa: F811
         check_tokens(c, q, out, lse, [q_len], [n], ALL, 0, [(0, i) for i in range(q_len)])
         before = q_len - (n - at)
         assert before >= 1 and bool(torch.isfinite(out[:before]).all()) and not bool(torch.isfinite(out[before]).all())
+
+
+@pytest.mark.parametrize("H,q_len,n", FORMS)
+@pytest.mark.parametrize("below", [14, 15, 16, 21, 22, 24, 25, 28, 31])
+def test_blocks_far_below_their_rows_largest(m, H, q_len, n, below):  # noqa: F811
+    """Three blocks of a row below the other, up to 2^31: queries in those three see them, and outputs have them."""
+    g = gen(39)
+    c = Cache(g, [n], 64)
+    js = torch.arange(n, device="cuda")
+    big = js * 7 % 4                                     # the large block differs from row to row
+    s = torch.full((n, 4), 110 - below, device="cuda")
+    s[js, big] = 110
+    codes = torch.randint(0x40, 0x7F, (n, D), generator=g, device="cuda") + 128 * torch.randint(0, 2, (n, D), generator=g, device="cuda")
+    codes.view(n, 4, 128)[js, big] = 0x00                # and has nothing in it but one value
+    codes.view(n, 4, 128)[js, big, 5] = 0x7E
+    set_scales(c, 0, s)
+    set_codes(c, 0, codes)
+    q = (randn(g, q_len, H, D).double() * power(torch.tensor(17 + below - 8, device="cuda"))).to(torch.bfloat16)
+    q.view(q_len, H, 4, 128)[..., 5] = 0                 # (which no query meets)
+    out, lse = attention(m, c, q, [q_len], [n])
+    assert m.csa_read_device_status() == 0
+    for i in {0, q_len // 2, q_len - 1}:
+        assert check_any_scales(c, 0, q[i].double(), out[i], lse[i], n - q_len + i + 1, i)
